@@ -42,6 +42,16 @@ class PrefillOptions(ctypes.Structure):
                 ("A_log", ctypes.c_void_p), ("out_gate", ctypes.c_void_p),
                 ("out_norm_weight", ctypes.c_void_p)]
 
+
+class SsmIo(ctypes.Structure):
+    """``kda_ssm_io`` of include/kda.h, field for field."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "delta", "B", "C", "z", "y")] + \
+        [(n, ctypes.c_int64) for n in ("x_stride", "delta_stride", "B_stride", "C_stride",
+                                       "z_stride", "y_stride")] + \
+        [(n, ctypes.c_void_p) for n in ("A", "D_skip", "delta_bias")] + \
+        [("delta_softplus", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 # Every symbol include/kda.h declares.
 EXPORTED = (
     "kda_status_string",
@@ -64,6 +74,14 @@ EXPORTED = (
     "kda_segment_transition_workspace_size",
     "kda_segment_transition",
     "kda_segment_scan",
+    "kda_short_conv_workspace_size",
+    "kda_short_conv",
+    "kda_short_conv_step",
+    "kda_selective_scan_workspace_size",
+    "kda_selective_scan",
+    "kda_selective_scan_step",
+    "kda_state_store",
+    "kda_state_load",
 )
 
 _lib = None
@@ -141,6 +159,26 @@ def load():
                                                vp, vp, sz, vp]
         lib.kda_segment_scan.restype = i32
         lib.kda_segment_scan.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp]
+        lib.kda_short_conv_workspace_size.restype = sz
+        lib.kda_short_conv_workspace_size.argtypes = [i32]
+        lib.kda_short_conv.restype = i32
+        lib.kda_short_conv.argtypes = [i32, lp, i32, i32, i32, vp, i64, vp, vp, i32, vp, vp, vp,
+                                       i32, vp, i64, vp, sz, vp]
+        lib.kda_short_conv_step.restype = i32
+        lib.kda_short_conv_step.argtypes = [i32, i32, i32, i32, vp, i64, vp, vp, i32, vp, vp,
+                                            i32, vp, i64, vp]
+        sp = ctypes.POINTER(SsmIo)
+        lib.kda_selective_scan_workspace_size.restype = sz
+        lib.kda_selective_scan_workspace_size.argtypes = [i32, lp, i32, i32, i32, i32]
+        lib.kda_selective_scan.restype = i32
+        lib.kda_selective_scan.argtypes = [i32, lp, i32, i32, i32, i32, sp, vp, vp, vp, i32, i32,
+                                           vp, sz, vp]
+        lib.kda_selective_scan_step.restype = i32
+        lib.kda_selective_scan_step.argtypes = [i32, i32, i32, i32, i32, sp, vp, vp, i32, vp]
+        lib.kda_state_store.restype = i32
+        lib.kda_state_store.argtypes = [i32, i64, i32, i32, vp, vp, i32, vp, vp, vp, i32, vp]
+        lib.kda_state_load.restype = i32
+        lib.kda_state_load.argtypes = [i32, i64, i32, i32, vp, vp, vp, i32, vp, vp, i32, vp]
         _lib = lib
         return lib
 

@@ -13,7 +13,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_api.cpp", "kda_decode.hip", "kda_prefill.hip", "kda_prep.hip", "kda_fused.hip",
-           "kda_scratch.hip"]
+           "kda_scratch.hip", "kda_recurrent_api.cpp", "kda_conv.hip", "kda_ssm.hip",
+           "kda_state_cache.hip"]
 ARCH = "gfx950"
 
 

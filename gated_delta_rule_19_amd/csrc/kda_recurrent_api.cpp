@@ -1,0 +1,371 @@
+// Host side of the short convolution, the selective scan and the 8-bit state
+// cache: argument checks, then the launches.  Nothing here allocates or
+// throws; every check runs before anything is enqueued.
+#include "kda.h"
+#include "kda_recurrent.h"
+
+using namespace kda;
+
+static_assert(sizeof(kda_ssm_io) == 128, "kda_ssm_io layout");
+
+namespace {
+
+bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+bool aligned_elt(const void *p, kda_dtype dt) {
+  return ((uintptr_t)p & (dt == KDA_BF16 ? 1u : 3u)) == 0;
+}
+int64_t elt_size(kda_dtype dt) { return dt == KDA_BF16 ? 2 : 4; }
+
+// Rows, channels and strides are kept below 2^40 bytes or so: every byte
+// offset the kernels form fits an int64 with room to spare.
+constexpr int64_t kMaxStride = (int64_t)1 << 31;
+constexpr int64_t kMaxTokens = (int64_t)1 << 40;
+
+// Packed bounds: 0 first, nondecreasing, no sequence of 2^30 tokens or more.
+bool good_cu(int32_t num_seqs, const int64_t *cu) {
+  if (num_seqs < 0 || num_seqs > (1 << 24) || !cu || cu[0] != 0)
+    return false;
+  for (int32_t n = 0; n < num_seqs; ++n)
+    if (cu[n + 1] < cu[n] || cu[n + 1] - cu[n] >= ((int64_t)1 << 30))
+      return false;
+  return cu[num_seqs] < kMaxTokens;
+}
+
+// A token matrix the call reads or writes.
+bool good_rows(const void *p, int64_t stride, int64_t width, kda_dtype dt) {
+  return p && aligned_elt(p, dt) && stride >= width && stride <= kMaxStride;
+}
+
+// Whether two row-strided matrices of `rows` rows share a byte.  Matrices
+// with one stride may interleave (column ranges of one buffer).
+bool rows_overlap(const void *a, int64_t a_stride, int64_t a_width, const void *b,
+                  int64_t b_stride, int64_t b_width, int64_t rows, int64_t es) {
+  if (!a || !b || rows <= 0)
+    return false;
+  const uint8_t *pa = (const uint8_t *)a, *pb = (const uint8_t *)b;
+  const uint8_t *ea = pa + ((rows - 1) * a_stride + a_width) * es;
+  const uint8_t *eb = pb + ((rows - 1) * b_stride + b_width) * es;
+  if (ea <= pb || eb <= pa)
+    return false;
+  if (a_stride != b_stride)
+    return true;
+  const int64_t pitch = a_stride * es;
+  int64_t off = (pb - pa) % pitch; // b's column offset in a's rows
+  if (off < 0)
+    off += pitch;
+  return off < a_width * es || off + b_width * es > pitch;
+}
+
+bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+  const uint8_t *pa = (const uint8_t *)a, *pb = (const uint8_t *)b;
+  return a && b && a_bytes > 0 && b_bytes > 0 && pa < pb + b_bytes && pb < pa + a_bytes;
+}
+
+// Slot table: the state buffers' slice count against the batch's.
+bool good_slots(const int32_t *slots, int32_t num_slots, int32_t count, bool states) {
+  if (!aligned4(slots))
+    return false;
+  return !states || (num_slots >= 0 && (slots || num_slots >= count));
+}
+
+kda_status result(hipError_t e) {
+  if (e == hipSuccess)
+    return KDA_OK;
+  // (the launchers' own refusal of a grid past the device's limits)
+  return e == hipErrorInvalidConfiguration ? KDA_ERR_INVALID_ARG : KDA_ERR_HIP;
+}
+
+kda_status check_workspace(size_t need, const void *ws, size_t bytes) {
+  if (need == 0)
+    return KDA_OK;
+  if (!ws || bytes < need)
+    return KDA_ERR_WORKSPACE;
+  return ((uintptr_t)ws & 255u) == 0 ? KDA_OK : KDA_ERR_INVALID_ARG;
+}
+
+kda_status check_conv(int32_t D, int32_t W, kda_dtype dt, int32_t act) {
+  if (dt != KDA_F32 && dt != KDA_BF16)
+    return KDA_ERR_UNSUPPORTED;
+  if (W < 2 || W > KDA_CONV_MAX_WIDTH)
+    return KDA_ERR_UNSUPPORTED;
+  if (D < 1 || (act != KDA_ACT_NONE && act != KDA_ACT_SILU))
+    return KDA_ERR_INVALID_ARG;
+  return KDA_OK;
+}
+
+kda_status check_ssm(int32_t D, int32_t N, int32_t G, kda_dtype dt, const kda_ssm_io *io) {
+  if (dt != KDA_F32 && dt != KDA_BF16)
+    return KDA_ERR_UNSUPPORTED;
+  if (N > KDA_SSM_MAX_STATES)
+    return KDA_ERR_UNSUPPORTED;
+  if (D < 1 || N < 1 || G < 1 || D % G != 0 || !io || io->reserved != 0 ||
+      (io->delta_softplus != 0 && io->delta_softplus != 1))
+    return KDA_ERR_INVALID_ARG;
+  return KDA_OK;
+}
+
+// The matrices and parameters of a scan over `rows` >= 1 tokens.
+kda_status check_ssm_io(int64_t rows, int32_t D, int32_t N, int32_t G, kda_dtype dt,
+                        const kda_ssm_io *io) {
+  const int64_t gn = (int64_t)G * N;
+  if (!good_rows(io->x, io->x_stride, D, dt) || !good_rows(io->delta, io->delta_stride, D, dt) ||
+      !good_rows(io->B, io->B_stride, gn, dt) || !good_rows(io->C, io->C_stride, gn, dt) ||
+      !good_rows(io->y, io->y_stride, D, dt) ||
+      (io->z && !good_rows(io->z, io->z_stride, D, dt)))
+    return KDA_ERR_INVALID_ARG;
+  if (!io->A || !aligned16(io->A) || !aligned16(io->D_skip) || !aligned16(io->delta_bias))
+    return KDA_ERR_INVALID_ARG;
+  const int64_t es = elt_size(dt);
+  const auto hits = [&](const void *p, int64_t stride, int64_t width) {
+    return rows_overlap(io->y, io->y_stride, D, p, stride, width, rows, es);
+  };
+  if (hits(io->x, io->x_stride, D) || hits(io->delta, io->delta_stride, D) ||
+      hits(io->B, io->B_stride, gn) || hits(io->C, io->C_stride, gn) ||
+      hits(io->z, io->z_stride, D))
+    return KDA_ERR_INVALID_ARG;
+  return KDA_OK;
+}
+
+SsmCall ssm_call(int32_t D, int32_t N, int32_t G, const kda_ssm_io *io) {
+  SsmCall c{};
+  c.D = D;
+  c.N = N;
+  c.G = G;
+  c.softplus = io->delta_softplus;
+  c.x = io->x;
+  c.delta = io->delta;
+  c.B = io->B;
+  c.C = io->C;
+  c.z = io->z;
+  c.y = io->y;
+  c.x_stride = io->x_stride;
+  c.delta_stride = io->delta_stride;
+  c.B_stride = io->B_stride;
+  c.C_stride = io->C_stride;
+  c.z_stride = io->z_stride;
+  c.y_stride = io->y_stride;
+  c.A = io->A;
+  c.skip = io->D_skip;
+  c.bias = io->delta_bias;
+  return c;
+}
+
+kda_status check_cache(int32_t n, int64_t R, int32_t L, int32_t format, const int32_t *src,
+                       int32_t num_src, const int32_t *dst, int32_t num_dst) {
+  if (format != KDA_CODE_INT8 && format != KDA_CODE_E4M3)
+    return KDA_ERR_UNSUPPORTED;
+  if (L > 256)
+    return KDA_ERR_UNSUPPORTED;
+  if (n < 0 || R < 1 || R > ((int64_t)1 << 31) || L < 1 || num_src < 0 || num_dst < 0 ||
+      !aligned4(src) || !aligned4(dst) || (!src && num_src < n) || (!dst && num_dst < n))
+    return KDA_ERR_INVALID_ARG;
+  return KDA_OK;
+}
+
+} // namespace
+
+extern "C" {
+
+size_t kda_short_conv_workspace_size(int32_t num_seqs) {
+  return num_seqs < 0 ? 0 : seq_table_bytes(num_seqs);
+}
+
+kda_status kda_short_conv(int32_t num_seqs, const int64_t *cu_seqlens_host, int32_t D, int32_t W,
+                          kda_dtype dt, const void *x, int64_t x_stride, const void *weight,
+                          const void *bias, int32_t act, const void *initial_state,
+                          void *final_state, const int32_t *slots, int32_t num_slots, void *y,
+                          int64_t y_stride, void *workspace, size_t workspace_bytes,
+                          void *stream) {
+  kda_status st = check_conv(D, W, dt, act);
+  if (st != KDA_OK)
+    return st;
+  if (!good_cu(num_seqs, cu_seqlens_host) ||
+      !good_slots(slots, num_slots, num_seqs, initial_state || final_state))
+    return KDA_ERR_INVALID_ARG;
+  if (num_seqs == 0)
+    return KDA_OK;
+  const int64_t T = cu_seqlens_host[num_seqs], es = elt_size(dt);
+  if (T > 0 && (!good_rows(x, x_stride, D, dt) || !good_rows(y, y_stride, D, dt) ||
+                rows_overlap(x, x_stride, D, y, y_stride, D, T, es)))
+    return KDA_ERR_INVALID_ARG;
+  if (!weight || !aligned16(weight) || !aligned16(bias) || !aligned16(initial_state) ||
+      !aligned16(final_state))
+    return KDA_ERR_INVALID_ARG;
+  const int64_t bytes = (int64_t)num_slots * (W - 1) * D * es;
+  if (initial_state != final_state && overlap(initial_state, bytes, final_state, bytes))
+    return KDA_ERR_INVALID_ARG;
+  st = check_workspace(seq_table_bytes(num_seqs), workspace, workspace_bytes);
+  if (st != KDA_OK)
+    return st;
+  ConvCall c{};
+  c.D = D;
+  c.W = W;
+  c.act = act;
+  c.num_slots = num_slots;
+  c.x = x;
+  c.x_stride = x_stride;
+  c.weight = weight;
+  c.bias = bias;
+  c.init = initial_state;
+  c.fin = final_state;
+  c.slots = slots;
+  c.y = y;
+  c.y_stride = y_stride;
+  return result(launch_conv(dt == KDA_BF16 ? 1 : 0, c, num_seqs, cu_seqlens_host, workspace,
+                            (hipStream_t)stream));
+}
+
+kda_status kda_short_conv_step(int32_t N, int32_t D, int32_t W, kda_dtype dt, const void *x,
+                               int64_t x_stride, const void *weight, const void *bias,
+                               int32_t act, void *state, const int32_t *slots, int32_t num_slots,
+                               void *y, int64_t y_stride, void *stream) {
+  const kda_status st = check_conv(D, W, dt, act);
+  if (st != KDA_OK)
+    return st;
+  if (N < 0 || !good_slots(slots, num_slots, N, true))
+    return KDA_ERR_INVALID_ARG;
+  if (N == 0)
+    return KDA_OK;
+  if (!good_rows(x, x_stride, D, dt) || !good_rows(y, y_stride, D, dt) || !weight || !state ||
+      !aligned16(weight) || !aligned16(bias) || !aligned16(state))
+    return KDA_ERR_INVALID_ARG;
+  if (!(x == y && x_stride == y_stride) &&
+      rows_overlap(x, x_stride, D, y, y_stride, D, N, elt_size(dt)))
+    return KDA_ERR_INVALID_ARG;
+  ConvCall c{};
+  c.D = D;
+  c.W = W;
+  c.act = act;
+  c.num_slots = num_slots;
+  c.x = x;
+  c.x_stride = x_stride;
+  c.weight = weight;
+  c.bias = bias;
+  c.fin = state;
+  c.slots = slots;
+  c.y = y;
+  c.y_stride = y_stride;
+  return result(launch_conv_step(dt == KDA_BF16 ? 1 : 0, c, N, (hipStream_t)stream));
+}
+
+size_t kda_selective_scan_workspace_size(int32_t num_seqs, const int64_t *cu_seqlens_host,
+                                         int32_t D, int32_t N, int32_t G, int32_t split_hint) {
+  if (!good_cu(num_seqs, cu_seqlens_host) || D < 1 || N < 1 || N > KDA_SSM_MAX_STATES || G < 1 ||
+      D % G != 0 || split_hint < 0)
+    return 0;
+  return ssm_plan(num_seqs, cu_seqlens_host, D, N, G, split_hint).total;
+}
+
+kda_status kda_selective_scan(int32_t num_seqs, const int64_t *cu_seqlens_host, int32_t D,
+                              int32_t N, int32_t G, kda_dtype dt, const kda_ssm_io *io,
+                              const float *initial_state, float *final_state,
+                              const int32_t *slots, int32_t num_slots, int32_t split_hint,
+                              void *workspace, size_t workspace_bytes, void *stream) {
+  kda_status st = check_ssm(D, N, G, dt, io);
+  if (st != KDA_OK)
+    return st;
+  if (!good_cu(num_seqs, cu_seqlens_host) || split_hint < 0 ||
+      !good_slots(slots, num_slots, num_seqs, initial_state || final_state))
+    return KDA_ERR_INVALID_ARG;
+  if (num_seqs == 0)
+    return KDA_OK;
+  const int64_t T = cu_seqlens_host[num_seqs];
+  if (T > 0) {
+    st = check_ssm_io(T, D, N, G, dt, io);
+    if (st != KDA_OK)
+      return st;
+  } else if (!io->A || !aligned16(io->A)) {
+    return KDA_ERR_INVALID_ARG;
+  }
+  if (!aligned16(initial_state) || !aligned16(final_state))
+    return KDA_ERR_INVALID_ARG;
+  const int64_t bytes = (int64_t)num_slots * D * N * (int64_t)sizeof(float);
+  if (initial_state != final_state && overlap(initial_state, bytes, final_state, bytes))
+    return KDA_ERR_INVALID_ARG;
+  const SsmPlan plan = ssm_plan(num_seqs, cu_seqlens_host, D, N, G, split_hint);
+  st = check_workspace(plan.total, workspace, workspace_bytes);
+  if (st != KDA_OK)
+    return st;
+  SsmCall c = ssm_call(D, N, G, io);
+  c.init = initial_state;
+  c.fin = final_state;
+  c.slots = slots;
+  c.num_slots = num_slots;
+  return result(launch_ssm(dt == KDA_BF16 ? 1 : 0, c, num_seqs, cu_seqlens_host, plan, workspace,
+                           (hipStream_t)stream));
+}
+
+kda_status kda_selective_scan_step(int32_t rows, int32_t D, int32_t N, int32_t G, kda_dtype dt,
+                                   const kda_ssm_io *io, float *state, const int32_t *slots,
+                                   int32_t num_slots, void *stream) {
+  kda_status st = check_ssm(D, N, G, dt, io);
+  if (st != KDA_OK)
+    return st;
+  if (rows < 0 || !good_slots(slots, num_slots, rows, true))
+    return KDA_ERR_INVALID_ARG;
+  if (rows == 0)
+    return KDA_OK;
+  st = check_ssm_io(rows, D, N, G, dt, io);
+  if (st != KDA_OK)
+    return st;
+  if (!state || !aligned16(state))
+    return KDA_ERR_INVALID_ARG;
+  SsmCall c = ssm_call(D, N, G, io);
+  c.fin = state;
+  c.slots = slots;
+  c.num_slots = num_slots;
+  return result(launch_ssm_step(dt == KDA_BF16 ? 1 : 0, c, rows, (hipStream_t)stream));
+}
+
+kda_status kda_state_store(int32_t n, int64_t R, int32_t L, int32_t format, const float *state,
+                           const int32_t *src, int32_t num_src, void *codes, float *scales,
+                           const int32_t *dst, int32_t num_dst, void *stream) {
+  const kda_status st = check_cache(n, R, L, format, src, num_src, dst, num_dst);
+  if (st != KDA_OK)
+    return st;
+  if (n == 0)
+    return KDA_OK;
+  if (!state || !codes || !scales || !aligned4(state) || !aligned4(scales))
+    return KDA_ERR_INVALID_ARG;
+  CacheCall c{};
+  c.n = n;
+  c.R = R;
+  c.L = L;
+  c.format = format;
+  c.src = src;
+  c.num_src = num_src;
+  c.dst = dst;
+  c.num_dst = num_dst;
+  c.state_in = state;
+  c.codes_out = codes;
+  c.scales_out = scales;
+  return result(launch_state_store(c, (hipStream_t)stream));
+}
+
+kda_status kda_state_load(int32_t n, int64_t R, int32_t L, int32_t format, const void *codes,
+                          const float *scales, const int32_t *src, int32_t num_src, float *state,
+                          const int32_t *dst, int32_t num_dst, void *stream) {
+  const kda_status st = check_cache(n, R, L, format, src, num_src, dst, num_dst);
+  if (st != KDA_OK)
+    return st;
+  if (n == 0)
+    return KDA_OK;
+  if (!state || !codes || !scales || !aligned4(state) || !aligned4(scales))
+    return KDA_ERR_INVALID_ARG;
+  CacheCall c{};
+  c.n = n;
+  c.R = R;
+  c.L = L;
+  c.format = format;
+  c.src = src;
+  c.num_src = num_src;
+  c.dst = dst;
+  c.num_dst = num_dst;
+  c.codes_in = codes;
+  c.scales_in = scales;
+  c.state_out = state;
+  return result(launch_state_load(c, (hipStream_t)stream));
+}
+
+} // extern "C"

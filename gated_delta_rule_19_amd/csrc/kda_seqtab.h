@@ -1,0 +1,137 @@
+// Packed-sequence tables that travel with the launch.
+//
+// The calls that walk packed sequences tile by tile need, on the device, the
+// sequences' bounds and the number of tiles before each of them.  Up to
+// kInlineSeqs sequences the tables are the kernel's first argument, by value:
+// nothing is uploaded, the call takes no workspace and may be captured into a
+// graph (the argument block is part of the recorded launch).  Above that,
+// seq_table_kernel launches write them to the workspace, kTablePart
+// sequences each, from their own argument blocks; the tables are again part
+// of the recorded launches, never of a host buffer that a later call reuses.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace kda {
+
+constexpr int kInlineSeqs = 48;  // 49 entries of 16 bytes: 784 of the 4096 argument bytes
+constexpr int kTablePart = 160;  // entries per table-writing launch (2560 of the 4096 bytes)
+
+// Sequence n: its first token, and the blocks before it in each of a call's
+// (at most two) launches.  Entry num_seqs holds the totals.
+struct SeqEntry {
+  int64_t tok0;
+  int32_t blk[2];
+};
+static_assert(sizeof(SeqEntry) == 16, "SeqEntry layout");
+
+struct SeqTable {
+  const SeqEntry *ws; // null: the entries are `in`
+  int32_t num_seqs;
+  int32_t pad;
+  SeqEntry in[kInlineSeqs + 1];
+};
+
+struct TablePart {
+  SeqEntry e[kTablePart];
+};
+
+inline size_t seq_table_bytes(int32_t num_seqs) {
+  return num_seqs <= kInlineSeqs
+             ? 0
+             : (((size_t)num_seqs + 1) * sizeof(SeqEntry) + 255) / 256 * 256;
+}
+
+// Fills `t` from the host bounds and the tiles of each sequence
+// (tiles(n, length, which) blocks in launch `which`), and for long tables
+// enqueues the launches that write it to `ws` (seq_table_bytes of it).  The
+// totals come back in total[2]; false when one passes 2^31 - 1.
+hipError_t launch_table_part(const TablePart &part, int count, SeqEntry *dst, hipStream_t s);
+
+// (the closing-entry totals of a table that is only counted, not written)
+template <typename F>
+bool seq_totals(int32_t num_seqs, const int64_t *cu, F &&tiles, int64_t total[2]) {
+  total[0] = total[1] = 0;
+  for (int32_t n = 0; n < num_seqs; ++n)
+    for (int w = 0; w < 2; ++w) {
+      total[w] += tiles(cu[n + 1] - cu[n], w);
+      if (total[w] > INT32_MAX)
+        return false;
+    }
+  return true;
+}
+
+template <typename F>
+hipError_t make_seq_table(SeqTable &t, int32_t num_seqs, const int64_t *cu, F &&tiles, void *ws,
+                          hipStream_t s) {
+  t.num_seqs = num_seqs;
+  t.pad = 0;
+  t.ws = num_seqs <= kInlineSeqs ? nullptr : (const SeqEntry *)ws;
+  int64_t at[2] = {0, 0};
+  TablePart part;
+  for (int32_t n = 0; n <= num_seqs; ++n) {
+    SeqEntry &e = t.ws ? part.e[n % kTablePart] : t.in[n];
+    e.tok0 = cu[n];
+    e.blk[0] = (int32_t)at[0];
+    e.blk[1] = (int32_t)at[1];
+    if (n < num_seqs)
+      for (int w = 0; w < 2; ++w)
+        at[w] += tiles(cu[n + 1] - cu[n], w);
+    const int filled = n % kTablePart + 1;
+    if (t.ws && (filled == kTablePart || n == num_seqs)) {
+      const hipError_t err = launch_table_part(part, filled, (SeqEntry *)ws + (n + 1 - filled), s);
+      if (err != hipSuccess)
+        return err;
+    }
+  }
+  return hipSuccess;
+}
+
+#ifdef __HIP_DEVICE_COMPILE__
+#define KDA_CONST_AS __attribute__((address_space(4)))
+#else
+#define KDA_CONST_AS
+#endif
+
+// The table as the kernel sees it.  The SeqTable is the kernel's first
+// parameter, so inline entries are read straight from the argument block;
+// reads are wave-uniform and go through scalar loads.
+struct SeqView {
+  const KDA_CONST_AS SeqEntry *e;
+  int32_t num_seqs;
+
+  __device__ __forceinline__ explicit SeqView(const SeqTable &t) {
+#ifdef __HIP_DEVICE_COMPILE__
+    const KDA_CONST_AS char *args = (const KDA_CONST_AS char *)__builtin_amdgcn_kernarg_segment_ptr();
+    const KDA_CONST_AS SeqEntry *in =
+        (const KDA_CONST_AS SeqEntry *)(args + offsetof(SeqTable, in));
+    e = t.ws ? (const KDA_CONST_AS SeqEntry *)(uintptr_t)t.ws : in;
+#else
+    e = nullptr;
+#endif
+    num_seqs = t.num_seqs;
+  }
+  __device__ __forceinline__ int64_t tok0(int n) const { return e[n].tok0; }
+  __device__ __forceinline__ int32_t len(int n) const {
+    return (int32_t)(e[n + 1].tok0 - e[n].tok0);
+  }
+  __device__ __forceinline__ int32_t blk(int n, int w) const { return e[n].blk[w]; }
+
+  // The sequence that block b of launch w belongs to: the last n with
+  // blk(n) <= b (sequences without blocks share their successor's count).
+  __device__ __forceinline__ int find(int b, int w) const {
+    int lo = 0, hi = num_seqs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (e[mid].blk[w] <= b)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    return lo;
+  }
+};
+
+} // namespace kda

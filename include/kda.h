@@ -472,6 +472,163 @@ kda_status kda_segment_scan(int32_t num_segs, int32_t H, int32_t dk, int32_t dv,
                             const float *S_tilde, const float *initial_state, float *S_in,
                             void *stream);
 
+/* ------------------------------------------------------------------------
+ * Calls around the recurrence: the short convolution in front of it, the
+ * selective scan (another recurrent token mixer, served with the same
+ * prompts and batches), and the 8-bit cache that states are parked in.
+ *
+ * Conventions of these calls, beside those above
+ * - Token matrices ([T, D]) may be column ranges of a wider one: each has a
+ *   row stride in elements, at least its row length, and needs only its
+ *   element type's alignment (16-byte-aligned rows run the vector loads).
+ *   Weights, biases, A and states are dense and 16-byte aligned.
+ * - slots: DEVICE int32, one entry per sequence (or row), the slice of the
+ *   state buffers it uses; NULL means entry n uses slice n.  The state
+ *   buffers hold num_slots slices (with slots NULL, num_slots >= the number
+ *   of sequences).  An entry outside [0, num_slots) marks padding: a prompt
+ *   then starts from zeros and its final state is not kept; a single-token
+ *   row is skipped whole (its output row is left as it was).  Valid entries
+ *   of one call must differ: two sequences that update one slice race.
+ * - Every one of these calls may be captured into a HIP graph: sequence
+ *   bounds travel in the recorded launches' argument blocks, not in a host
+ *   buffer.  A call's workspace is its own until it has finished, replays
+ *   included: graphs that may run at the same time need different ones.
+ * - Infinities and NaN in the inputs go where the formulas carry them, and
+ *   never from one sequence, channel or row into another.
+ */
+
+#define KDA_ACT_NONE 0
+#define KDA_ACT_SILU 1
+#define KDA_CONV_MAX_WIDTH 8
+
+/*
+ * Short causal depthwise convolution over packed sequences, the step that q,
+ * k and v pass before the recurrence ("Kimi K3 的架構" (hao.cnyes.com), §七):
+ *     y[t, d] = act(bias[d] + sum_{j < W} w[d, j] x[t - (W - 1) + j, d])
+ * The W - 1 positions before a sequence's first token are the rows of its
+ * initial state (oldest first; zeros without one).
+ *
+ *   cu_seqlens_host : HOST, as for kda_chunk_prefill; each sequence shorter
+ *                     than 2^30 tokens.
+ *   D, W            : channels (>= 1), width (2 .. KDA_CONV_MAX_WIDTH).
+ *   x, y            : [T, D] of type dt, row strides x_stride, y_stride;
+ *                     y must not overlap x.
+ *   weight, bias    : [D, W], [D] (or NULL) of type dt.
+ *   act             : KDA_ACT_NONE or KDA_ACT_SILU.
+ *   initial_state, final_state : [num_slots, W - 1, D] of type dt, or NULL.
+ *                     The final state of a sequence is its last W - 1 inputs
+ *                     (with rows of its initial state in front when it is
+ *                     shorter), copied without rounding.  final_state ==
+ *                     initial_state is allowed; other overlaps are not.
+ *   workspace       : DEVICE, of the queried size (0 up to 48 sequences:
+ *                     then it may be NULL), 256-byte aligned.
+ * The sums are fp32; y is rounded once.
+ */
+size_t kda_short_conv_workspace_size(int32_t num_seqs);
+
+kda_status kda_short_conv(int32_t num_seqs, const int64_t *cu_seqlens_host, int32_t D, int32_t W,
+                          kda_dtype dt, const void *x, int64_t x_stride, const void *weight,
+                          const void *bias, int32_t act, const void *initial_state,
+                          void *final_state, const int32_t *slots, int32_t num_slots, void *y,
+                          int64_t y_stride, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/*
+ * The convolution for one token of each of N sequences: y [N, D] from x
+ * [N, D] and the state ([num_slots, W - 1, D]), which is shifted by the
+ * token in place.  y may be x itself (same pointer and stride).
+ */
+kda_status kda_short_conv_step(int32_t N, int32_t D, int32_t W, kda_dtype dt, const void *x,
+                               int64_t x_stride, const void *weight, const void *bias,
+                               int32_t act, void *state, const int32_t *slots, int32_t num_slots,
+                               void *y, int64_t y_stride, void *stream);
+
+/*
+ * Selective state space scan over packed sequences.  Per sequence, channel d
+ * (of group g = d / (D / G)) and state n:
+ *     delta = softplus(dt[t, d] + delta_bias[d])   (delta_softplus = 0: the sum itself)
+ *     h[d, n] = exp(delta A[d, n]) h[d, n] + delta x[t, d] B[t, g, n]
+ *     y[t, d] = (sum_n C[t, g, n] h[d, n] + D_skip[d] x[t, d]) * silu(z[t, d])
+ *
+ *   D, N, G    : channels, states per channel (1 .. KDA_SSM_MAX_STATES),
+ *                groups (D a multiple of G).
+ *   io         : the token matrices x, delta, z, y [T, D] and B, C [T, G, N]
+ *                (rows of G * N) of type dt with their row strides, and the
+ *                fp32 parameters A [D, N], D_skip [D], delta_bias [D].  z,
+ *                D_skip and delta_bias may be NULL: no gate, no skip, no
+ *                bias.  y must not overlap the inputs.
+ *   initial_state, final_state : [num_slots, D, N] fp32, or NULL (zeros /
+ *                not written).  final_state == initial_state is allowed;
+ *                other overlaps are not.
+ *   split_hint : 0: long sequences are cut into segments when their channels
+ *                alone leave the device idle; 1: never; n > 1: about n
+ *                segments for the longest sequence, others in segments of
+ *                that length.  The result is the same up to fp32 rounding.
+ *   workspace  : DEVICE, of the queried size, 256-byte aligned.
+ * States, decays and sums are fp32; y is rounded once.
+ */
+#define KDA_SSM_MAX_STATES 128
+
+typedef struct kda_ssm_io {
+  const void *x, *delta, *B, *C, *z;
+  void *y;
+  int64_t x_stride, delta_stride, B_stride, C_stride, z_stride, y_stride;
+  const float *A, *D_skip, *delta_bias;
+  int32_t delta_softplus;
+  int32_t reserved; /* 0 */
+} kda_ssm_io;
+
+size_t kda_selective_scan_workspace_size(int32_t num_seqs, const int64_t *cu_seqlens_host,
+                                         int32_t D, int32_t N, int32_t G, int32_t split_hint);
+
+kda_status kda_selective_scan(int32_t num_seqs, const int64_t *cu_seqlens_host, int32_t D,
+                              int32_t N, int32_t G, kda_dtype dt, const kda_ssm_io *io,
+                              const float *initial_state, float *final_state,
+                              const int32_t *slots, int32_t num_slots, int32_t split_hint,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The scan for one token of each of `rows` sequences: io's matrices have
+ * `rows` rows, state ([num_slots, D, N] fp32) is updated in place.
+ */
+kda_status kda_selective_scan_step(int32_t rows, int32_t D, int32_t N, int32_t G, kda_dtype dt,
+                                   const kda_ssm_io *io, float *state, const int32_t *slots,
+                                   int32_t num_slots, void *stream);
+
+/*
+ * 8-bit state cache: fp32 states quantised as they are written, and read
+ * back (the checkpoints of kda_chunk_prefill_ckpt, decode states of parked
+ * sequences, scan states).  An item is R rows of L values; each row has one
+ * fp32 scale:
+ *     scale = amax / qmax, at least 2^-126 and at most the largest whose
+ *             product with qmax is finite;
+ *     code  = round_to_nearest_even(x * (1 / scale));
+ *     x'    = code * scale,
+ * with qmax = 127 (KDA_CODE_INT8) or 448 (KDA_CODE_E4M3, OCP e4m3).  A row
+ * that holds an infinity or a NaN gets scale NaN and codes 0, so it reads
+ * back as NaN.  For KDA states R = H * dk, L = dv; for scan states R = D,
+ * L = N.
+ *
+ *   n        : items to move (>= 0).
+ *   R, L     : rows per item (>= 1), row length (1 .. 256).
+ *   state    : fp32 [items, R, L];  codes : [slots, R, L] bytes;
+ *   scales   : fp32 [slots, R].
+ *   src, dst : DEVICE int32 [n] or NULL (entry i is i): item i is read from
+ *              slice src[i] of num_src and written to slice dst[i] of
+ *              num_dst.  An entry outside its range skips the item.  The
+ *              valid entries of dst must differ.
+ */
+#define KDA_CODE_INT8 0
+#define KDA_CODE_E4M3 1
+
+kda_status kda_state_store(int32_t n, int64_t R, int32_t L, int32_t format, const float *state,
+                           const int32_t *src, int32_t num_src, void *codes, float *scales,
+                           const int32_t *dst, int32_t num_dst, void *stream);
+
+kda_status kda_state_load(int32_t n, int64_t R, int32_t L, int32_t format, const void *codes,
+                          const float *scales, const int32_t *src, int32_t num_src, float *state,
+                          const int32_t *dst, int32_t num_dst, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
