@@ -17,9 +17,10 @@ bool aligned_elt(const void *p, kda_dtype dt) {
 }
 int64_t elt_size(kda_dtype dt) { return dt == KDA_BF16 ? 2 : 4; }
 
-// Rows, channels and strides are kept below 2^40 bytes or so: every byte
-// offset the kernels form fits an int64 with room to spare.
-constexpr int64_t kMaxStride = (int64_t)1 << 31;
+// Row strides up to 2^24 elements keep the rows of one tile (16 tokens of at
+// most 4 bytes) within the 32-bit offsets the kernels form inside it; offsets
+// of whole rows are 64-bit.
+constexpr int64_t kMaxStride = (int64_t)1 << 24;
 constexpr int64_t kMaxTokens = (int64_t)1 << 40;
 
 // Packed bounds: 0 first, nondecreasing, no sequence of 2^30 tokens or more.

@@ -42,24 +42,21 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// log(1 + exp(x)) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1], by the
-// series log1p(e) = 2 (s + s^3 / 3 + s^5 / 5 + ...), s = e / (2 + e) <= 1/3:
-// eight terms leave 2 s^17 / 17 < 1e-9 of it.  (The logarithm of 1 + e
-// itself would lose the small steps: at delta = 0.001 its argument keeps ten
-// bits of e.)
+// log(1 + exp(x)) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1], with
+// log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3, and atanh(s) / s a polynomial
+// in s^2 (degree 4, fitted for the smallest relative error over [0, 1/9]:
+// 8e-9).  (The logarithm of 1 + e itself would lose the small steps: at
+// delta = 0.001 its argument keeps 13 of e's 23 bits.)
 __device__ __forceinline__ float softplus(float x) {
   const float e = exp2_hw(-fabsf(x) * kLog2e);
   const float s = e * __builtin_amdgcn_rcpf(2.f + e);
   const float q = s * s;
-  float p = 1.f / 15.f;
-  p = fmaf(p, q, 1.f / 13.f);
-  p = fmaf(p, q, 1.f / 11.f);
-  p = fmaf(p, q, 1.f / 9.f);
-  p = fmaf(p, q, 1.f / 7.f);
-  p = fmaf(p, q, 1.f / 5.f);
-  p = fmaf(p, q, 1.f / 3.f);
+  float p = 0.14089167f;
+  p = fmaf(p, q, 0.139803007f);
+  p = fmaf(p, q, 0.200124547f);
+  p = fmaf(p, q, 0.333331585f);
   p = fmaf(p, q, 1.f);
-  return fmaxf(x, 0.f) + 2.f * s * p;
+  return fmaf(s + s, p, fmaxf(x, 0.f));
 }
 
 __device__ __forceinline__ float silu(float x) {
@@ -73,7 +70,7 @@ struct SsmArgs {
   int32_t seg;     // tokens per segment
   int32_t vec_state; // a channel's states may be read and written NS at a time
   int64_t T;       // tokens (rows of the B / C table)
-  int64_t xs, dls, zs, ys;
+  int64_t xs, dls, zs, ys, Bs, Cs;
   const float *A, *skip, *bias;
   const float *init;
   float *fin;
@@ -298,21 +295,10 @@ __global__ __launch_bounds__(64 * S) void ssm_kernel(SeqTable tab, SsmArgs a, in
           h[i] = p[i];
     }
   } else if (full) {
-    // the entry state: the first segment's end state, carried over the
-    // segments between
-    const float *pe = a.pend + ((pair0 * blocks + gc) * S + wave) * NS * 64 + lane;
-    const float *ps = a.psum + (pair0 * blocks + gc) * 64 + lane;
+    const float *pe = a.pend + (((pair0 + j - 1) * blocks + gc) * S + wave) * NS * 64 + lane;
 #pragma unroll
     for (int i = 0; i < NS; ++i)
       h[i] = pe[i * 64];
-    for (int q = 1; q < j; ++q) {
-      pe += (int64_t)blocks * S * NS * 64;
-      ps += (int64_t)blocks * 64;
-      const float sd = *ps;
-#pragma unroll
-      for (int i = 0; i < NS; ++i)
-        h[i] = fmaf(exp2_hw(sd * A2[i]), h[i], pe[i * 64]);
-    }
   }
 
   const KDA_CONST_AS float *bc =
@@ -346,6 +332,311 @@ __global__ __launch_bounds__(64 * S) void ssm_kernel(SeqTable tab, SsmArgs a, in
       pe[i * 64] = h[i];
     if (j > 0 && wave == 0)
       a.psum[((pair0 + j) * blocks + gc) * 64 + lane] = sum;
+  }
+}
+
+// ---- all states of a channel in one lane --------------------------------------------
+// No exchange between waves and no barrier: a wave streams its 64 channels'
+// tokens, U at a time with the next U tokens' inputs in flight.  B and C come
+// through an LDS area of the wave's own: kBcTokens tokens' values, widened,
+// loaded a whole area ahead; every lane then reads the same 16 bytes.
+constexpr int kBcTokens = 16;
+
+template <int NS> struct LaneBc {
+  float v[2][kBcTokens][2 * NS]; // B then C of each token, two areas in turn
+};
+
+// One element per lane of a row of channels; lanes at or past `bytes` (the
+// row's end, or 0 for a token past the segment) read 0 and write nothing.
+// The loaded bits are kept as they are and widened where they are used, so
+// that nothing waits for a load before then.
+template <typename T> struct RawOf { typedef unsigned short type; };
+template <> struct RawOf<float> { typedef unsigned type; };
+template <typename T> using Raw = typename RawOf<T>::type;
+__device__ __forceinline__ float widen(unsigned short r) {
+  return __builtin_bit_cast(float, (unsigned)r << 16);
+}
+__device__ __forceinline__ float widen(unsigned r) { return __builtin_bit_cast(float, r); }
+__device__ __forceinline__ unsigned short buffer_raw(__amdgpu_buffer_rsrc_t r, int voff,
+                                                     const bf16 *) {
+  return __builtin_amdgcn_raw_buffer_load_b16(r, voff, 0, 0);
+}
+__device__ __forceinline__ unsigned buffer_raw(__amdgpu_buffer_rsrc_t r, int voff,
+                                               const float *) {
+  return __builtin_amdgcn_raw_buffer_load_b32(r, voff, 0, 0);
+}
+template <typename T>
+__device__ __forceinline__ Raw<T> row_load(const T *p, int bytes, int lane) {
+  return buffer_raw(buffer_rsrc(p, bytes), lane * (int)sizeof(T), p);
+}
+template <typename T>
+__device__ __forceinline__ void row_store(T *p, int bytes, int lane, float v) {
+  buffer_store(buffer_rsrc(p, bytes), from_f32<T>(v), lane * (int)sizeof(T), 0);
+}
+
+// The values of B and C a lane brings in per area: state i of every kStep-th
+// token.  Tokens past the segment and states past N read 0.
+template <typename T, int NS> struct BcLoader {
+  static constexpr int kStep = 64 / NS;
+  static constexpr int kPer = kBcTokens / kStep;
+  const T *B, *C;
+  int64_t Bs, Cs;
+  int t0, i;
+  bool on;
+  Raw<T> b[kPer], c[kPer];
+
+  __device__ __forceinline__ BcLoader(const T *B_, const T *C_, int64_t Bs_, int64_t Cs_, int N,
+                                      int lane)
+      : B(B_), C(C_), Bs(Bs_), Cs(Cs_) {
+    t0 = lane / NS;
+    i = lane % NS;
+    on = i < N;
+  }
+  __device__ __forceinline__ void fetch(int tok, int ntok) {
+    // (an area's rows lie within 2^31 bytes)
+    constexpr int kSpan = 0x7fffffff;
+    const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(B + tok * Bs, kSpan);
+    const __amdgpu_buffer_rsrc_t rc = buffer_rsrc(C + tok * Cs, kSpan);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int t = t0 + k * kStep;
+      const bool ok = on && tok + t < ntok;
+      b[k] = buffer_raw(rb, ok ? (t * (int)Bs + i) * (int)sizeof(T) : -1, B);
+      c[k] = buffer_raw(rc, ok ? (t * (int)Cs + i) * (int)sizeof(T) : -1, C);
+    }
+  }
+  __device__ __forceinline__ void put(float (*area)[2 * NS]) const {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      area[t0 + k * kStep][i] = widen(b[k]);
+      area[t0 + k * kStep][NS + i] = widen(c[k]);
+    }
+  }
+};
+
+template <typename T, int NS, bool FULL>
+__device__ __forceinline__ float lane_segment(const SsmArgs &a, LaneBc<NS> &lds, float (&h)[NS],
+                                              const float (&A2)[NS], BcLoader<T, NS> bc,
+                                              const T *x, const T *dl, const T *z, T *y, int ntok,
+                                              int row_bytes, int lane, float bias, float skip) {
+  constexpr int U = 4;
+  Raw<T> xr[U], dr[U], zr[U];
+  float sum = 0.f;
+  const auto bytes = [&](int t) { return t < ntok ? row_bytes : 0; };
+  const auto fetch = [&](int t0) {
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t t = t0 + k;
+      xr[k] = row_load(x + t * a.xs, bytes(t0 + k), lane);
+      dr[k] = row_load(dl + t * a.dls, bytes(t0 + k), lane);
+    }
+    if (FULL && z) {
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        zr[k] = row_load(z + (t0 + k) * a.zs, bytes(t0 + k), lane);
+    }
+  };
+  bc.fetch(0, ntok);
+  fetch(0);
+  for (int b0 = 0; b0 < ntok; b0 += kBcTokens) {
+    // this wave's reads of the area two before are done: its LDS
+    // instructions run in order
+    float(*area)[2 * NS] = lds.v[(b0 / kBcTokens) & 1];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    bc.put(area);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+    bc.fetch(b0 + kBcTokens, ntok);
+    for (int t0 = b0; t0 < min(b0 + kBcTokens, ntok); t0 += U) {
+      float xk[U], d[U], gate[U], acc[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        xk[k] = widen(xr[k]);
+        d[k] = widen(dr[k]) + bias;
+        gate[k] = 1.f;
+      }
+      if (a.softplus) {
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+          d[k] = softplus(d[k]);
+      }
+      if (FULL && z) {
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+          gate[k] = silu(widen(zr[k]));
+      }
+      // past the segment's end a step of 0 (with x and B 0) leaves h as it is
+      if (ntok - t0 < U) {
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+          d[k] = t0 + k < ntok ? d[k] : 0.f;
+      }
+      fetch(t0 + U);
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const float *row = area[t0 - b0 + k];
+        const float u = d[k] * xk[k];
+        acc[k] = 0.f;
+#pragma unroll
+        for (int q = 0; q < NS; q += 4) {
+          const f32x4 bv = *reinterpret_cast<const f32x4 *>(row + q);
+          f32x4 cv;
+          if (FULL)
+            cv = *reinterpret_cast<const f32x4 *>(row + NS + q);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            h[q + i] = fmaf(exp2_hw(d[k] * A2[q + i]), h[q + i], u * bv[i]);
+            if (FULL)
+              acc[k] = fmaf(cv[i], h[q + i], acc[k]);
+          }
+        }
+        if (FULL)
+          acc[k] = fmaf(skip, xk[k], acc[k]);
+        else
+          sum += d[k];
+      }
+      if (FULL) {
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+          row_store(y + (t0 + k) * a.ys, bytes(t0 + k), lane, z ? acc[k] * gate[k] : acc[k]);
+      }
+    }
+  }
+  return sum;
+}
+
+template <typename T, int NS>
+__global__ __launch_bounds__(256, 4) void ssm_lane_kernel(SeqTable tab, SsmArgs a, int pass,
+                                                       const T *__restrict__ x,
+                                                       const T *__restrict__ dl,
+                                                       const T *__restrict__ z,
+                                                       const T *__restrict__ B,
+                                                       const T *__restrict__ C,
+                                                       T *__restrict__ y) {
+  __shared__ LaneBc<NS> lds[4];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int blocks = a.G * a.cb, quads = (blocks + 3) / 4;
+  const int sb = blockIdx.x / quads, gc = (blockIdx.x - sb * quads) * 4 + wave;
+  if (gc >= blocks)
+    return;
+  const int g = gc / a.cb, cbi = gc - g * a.cb;
+  const SeqView seqs(tab);
+  const int n = seqs.find(sb, pass);
+  const int len = seqs.len(n);
+  const int64_t tok0 = seqs.tok0(n);
+  const int nseg = len > a.seg ? (len + a.seg - 1) / a.seg : 1;
+  const int j = sb - seqs.blk(n, pass) + pass;
+  const int64_t pair0 = seqs.blk(n, 1);
+  const int s0 = j * a.seg, ntok = min(a.seg, len - s0);
+
+  const int dg = cbi * 64 + lane;
+  const bool in = dg < a.Dg;
+  const int64_t d = (int64_t)g * a.Dg + dg;
+  float A2[NS], h[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    A2[i] = in && i < a.N ? a.A[d * a.N + i] * kLog2e : 0.f;
+    h[i] = 0.f;
+  }
+  int64_t slot = n;
+  bool kept = true;
+  if (a.slots) {
+    slot = a.slots[n];
+    kept = slot >= 0 && slot < a.num_slots;
+  }
+  if (j == 0) {
+    if (a.init && kept && in) {
+      const float *p = a.init + (slot * a.D + d) * a.N;
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        if (i < a.N)
+          h[i] = p[i];
+    }
+  } else if (pass == 1) {
+    const float *pe = a.pend + ((pair0 + j - 1) * blocks + gc) * NS * 64 + lane;
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      h[i] = pe[i * 64];
+  }
+
+  const int64_t t0 = tok0 + s0;
+  const BcLoader<T, NS> bc(B + t0 * a.Bs + g * a.N, C + t0 * a.Cs + g * a.N, a.Bs, a.Cs, a.N,
+                           lane);
+  const float bias = in && a.bias ? a.bias[d] : 0.f;
+  const float skip = in && a.skip ? a.skip[d] : 0.f;
+  const int64_t d0 = (int64_t)g * a.Dg + cbi * 64; // the wave's first channel
+  const int row_bytes = min(64, a.Dg - cbi * 64) * (int)sizeof(T);
+  float sum = 0.f;
+  if (pass == 1 || j == 0)
+    lane_segment<T, NS, true>(a, lds[wave], h, A2, bc, x + t0 * a.xs + d0, dl + t0 * a.dls + d0,
+                              z ? z + t0 * a.zs + d0 : nullptr, y + t0 * a.ys + d0, ntok,
+                              row_bytes, lane, bias, skip);
+  else
+    sum = lane_segment<T, NS, false>(a, lds[wave], h, A2, bc, x + t0 * a.xs + d0,
+                                     dl + t0 * a.dls + d0, nullptr, nullptr, ntok, row_bytes,
+                                     lane, bias, skip);
+
+  if (j == nseg - 1) {
+    if (a.fin && kept && in) {
+      float *p = a.fin + (slot * a.D + d) * a.N;
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        if (i < a.N)
+          p[i] = h[i];
+    }
+  } else if (pass == 0) {
+    float *pe = a.pend + ((pair0 + j) * blocks + gc) * NS * 64 + lane;
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      pe[i * 64] = h[i];
+    if (j > 0)
+      a.psum[((pair0 + j) * blocks + gc) * 64 + lane] = sum;
+  }
+}
+
+// ---- the segments' entry states -------------------------------------------------------
+// pend[0] is the state after the first segment; pend[j] becomes
+// pend[j] + exp(A sum_j) pend[j - 1], the state after segment j.  One wave per
+// (cut sequence, 64 channels, state); the pairs of 16 segments are in flight
+// together.
+__global__ __launch_bounds__(256) void ssm_fold_kernel(SeqTable tab, SsmArgs a, int SN) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int blocks = a.G * a.cb;
+  const int64_t wv = (int64_t)blockIdx.x * 4 + wave;
+  const int n = (int)(wv / ((int64_t)blocks * SN));
+  if (n >= tab.num_seqs)
+    return;
+  const int rest = (int)(wv - (int64_t)n * blocks * SN);
+  const int gc = rest / SN, i = rest - gc * SN;
+  const SeqView seqs(tab);
+  const int64_t pair0 = seqs.blk(n, 1);
+  const int pairs = (int)(seqs.blk(n + 1, 1) - pair0);
+  if (pairs <= 1 || i >= a.N)
+    return;
+  const int g = gc / a.cb, dg = (gc - g * a.cb) * 64 + lane;
+  const float A2 = dg < a.Dg ? a.A[((int64_t)g * a.Dg + dg) * a.N + i] * kLog2e : 0.f;
+  float *pe = a.pend + ((pair0 * blocks + gc) * SN + i) * 64 + lane;
+  const float *ps = a.psum + (pair0 * blocks + gc) * 64 + lane;
+  const int64_t pstep = (int64_t)blocks * SN * 64, sstep = (int64_t)blocks * 64;
+  float h = pe[0];
+  for (int j = 1; j < pairs; j += 16) {
+    float e[16], sd[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int q = min(j + k, pairs - 1);
+      e[k] = pe[q * pstep];
+      sd[k] = ps[q * sstep];
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (j + k < pairs) {
+        h = fmaf(exp2_hw(sd[k] * A2), h, e[k]);
+        pe[(j + k) * pstep] = h;
+      }
   }
 }
 
@@ -445,13 +736,12 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(StepArgs a, const T *__re
 }
 
 // ---- host ---------------------------------------------------------------------------
-// Waves per workgroup and states per wave.
+// Waves per workgroup and states per wave of the wide kernel (states dealt to
+// the waves), and states of the lane kernel.
 struct Shape {
   int S, NS;
 };
-Shape ssm_shape(int N) {
-  if (N <= 4)
-    return {1, 4};
+Shape wide_shape(int N) {
   if (N <= 8)
     return {2, 4};
   if (N <= 16)
@@ -462,31 +752,39 @@ Shape ssm_shape(int N) {
     return {16, 4};
   return {16, 8};
 }
+int lane_states(int N) { return N <= 4 ? 4 : (N <= 8 ? 8 : 16); }
+constexpr int kLaneMaxStates = 16;
 
-template <typename F> hipError_t with_shape(Shape sh, F &&f) {
+constexpr size_t kAlign = 256;
+size_t up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+int64_t chan_blocks(int32_t D, int32_t G) { return (int64_t)G * ((D / G + 63) / 64); }
+
+template <typename F> hipError_t with_wide(Shape sh, F &&f) {
   using std::integral_constant;
-  const auto go = [&](auto s, auto ns, auto tt) { return f(s, ns, tt); };
-  using i1 = integral_constant<int, 1>;
   using i2 = integral_constant<int, 2>;
   using i4 = integral_constant<int, 4>;
   using i8 = integral_constant<int, 8>;
   using i16 = integral_constant<int, 16>;
   using i32 = integral_constant<int, 32>;
   if (sh.NS == 8)
-    return go(i16(), i8(), i16());
+    return f(i16(), i8(), i16());
   switch (sh.S) {
-  case 1: return go(i1(), i4(), i16());
-  case 2: return go(i2(), i4(), i16());
-  case 4: return go(i4(), i4(), i32());
-  case 8: return go(i8(), i4(), i32());
-  default: return go(i16(), i4(), i16());
+  case 2: return f(i2(), i4(), i16());
+  case 4: return f(i4(), i4(), i32());
+  case 8: return f(i8(), i4(), i32());
+  default: return f(i16(), i4(), i16());
   }
 }
 
-constexpr size_t kAlign = 256;
-size_t up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-int64_t chan_blocks(int32_t D, int32_t G) { return (int64_t)G * ((D / G + 63) / 64); }
+template <typename F> hipError_t with_lane(int NS, F &&f) {
+  using std::integral_constant;
+  if (NS == 4)
+    return f(integral_constant<int, 4>());
+  if (NS == 8)
+    return f(integral_constant<int, 8>());
+  return f(integral_constant<int, 16>());
+}
 
 } // namespace
 
@@ -497,40 +795,42 @@ int64_t ssm_num_segments(int64_t len, const SsmPlan &p) {
 SsmPlan ssm_plan(int32_t num_seqs, const int64_t *cu, int32_t D, int32_t N, int32_t G,
                  int32_t split_hint) {
   SsmPlan p{};
-  const Shape sh = ssm_shape(N);
   const int64_t blocks = chan_blocks(D, G), tokens = cu[num_seqs];
   int64_t longest = 0;
   for (int32_t n = 0; n < num_seqs; ++n)
     longest = std::max(longest, cu[n + 1] - cu[n]);
   // multiples of 32 tokens: whole tiles
   const auto whole = [](int64_t x) { return std::max<int64_t>(32, (x + 31) / 32 * 32); };
+  const Shape sh = wide_shape(N);
   p.seg = whole(longest);
-  if (split_hint > 1)
+  p.lane = N <= kLaneMaxStates;
+  if (split_hint > 1) {
     p.seg = whole((longest + split_hint - 1) / split_hint);
-  else if (split_hint == 0) {
-    const int64_t want = 1024 / blocks;
-    if (want >= 3)
-      p.seg = std::min(p.seg, std::max<int64_t>(64, whole((tokens + want - 1) / want)));
+  } else if (split_hint == 0) {
+    const int64_t want = p.lane ? tokens * blocks / 4096 : tokens * blocks / 1024;
+    p.seg = std::min(p.seg, std::max<int64_t>(64, whole(want)));
   }
+  p.S = p.lane ? 1 : sh.S;
+  p.NS = p.lane ? lane_states(N) : sh.NS;
   for (int32_t n = 0; n < num_seqs; ++n)
     p.pairs += ssm_num_segments(cu[n + 1] - cu[n], p) - 1;
+  const size_t SN = (size_t)p.S * p.NS;
   size_t o = seq_table_bytes(num_seqs);
   p.off_bc = o;
-  o = up(o + (size_t)tokens * G * sh.S * sh.NS * 2 * sizeof(float));
+  o = up(o + (p.lane ? 0 : (size_t)tokens * G * SN * 2 * sizeof(float)));
   p.off_end = o;
-  o = up(o + (size_t)p.pairs * blocks * 64 * sh.S * sh.NS * sizeof(float));
+  o = up(o + (size_t)p.pairs * blocks * 64 * SN * sizeof(float));
   p.off_sum = o;
   o = up(o + (size_t)p.pairs * blocks * 64 * sizeof(float));
   p.total = o;
-  p.ok = longest < INT32_MAX - 64;
   return p;
 }
 
 hipError_t launch_ssm(int elt, const SsmCall &c, int32_t num_seqs, const int64_t *cu,
                       const SsmPlan &plan, void *ws, hipStream_t s) {
-  const Shape sh = ssm_shape(c.N);
   const int64_t tokens = cu[num_seqs];
   const int64_t blocks = chan_blocks(c.D, c.G);
+  const int SN = plan.S * plan.NS;
   uint8_t *w = (uint8_t *)ws;
 
   SsmArgs a{};
@@ -547,6 +847,8 @@ hipError_t launch_ssm(int elt, const SsmCall &c, int32_t num_seqs, const int64_t
   a.dls = c.delta_stride;
   a.zs = c.z_stride;
   a.ys = c.y_stride;
+  a.Bs = c.B_stride;
+  a.Cs = c.C_stride;
   a.A = c.A;
   a.skip = c.skip;
   a.bias = c.bias;
@@ -564,29 +866,52 @@ hipError_t launch_ssm(int elt, const SsmCall &c, int32_t num_seqs, const int64_t
   int64_t total[2];
   if (!seq_totals(num_seqs, cu, tiles, total))
     return hipErrorInvalidConfiguration;
+  // workgroups per (segment, all channels) and threads per workgroup
+  const int64_t per = plan.lane ? (blocks + 3) / 4 : blocks;
+  const int64_t threads = plan.lane ? 256 : 64 * plan.S;
   for (int pass = 0; pass < 2; ++pass)
-    if (total[pass] * blocks > INT32_MAX || total[pass] * blocks * 64 * sh.S > UINT32_MAX)
+    if (total[pass] * per > INT32_MAX || total[pass] * per * threads > UINT32_MAX)
       return hipErrorInvalidConfiguration;
-  const int64_t bcb = (tokens * c.G * sh.S + 255) / 256;
-  if (bcb * 256 > UINT32_MAX)
+  const int64_t bcb = (tokens * c.G * plan.S + 255) / 256;
+  const int64_t fold = plan.pairs > 0 ? ((int64_t)num_seqs * blocks * SN + 3) / 4 : 0;
+  if (bcb * 256 > UINT32_MAX || fold * 256 > UINT32_MAX)
     return hipErrorInvalidConfiguration;
   SeqTable tab;
   hipError_t e = make_seq_table(tab, num_seqs, cu, tiles, ws, s);
   if (e != hipSuccess)
     return e;
+
   const auto typed = [&](auto tag) {
     using T = decltype(tag);
-    return with_shape(sh, [&](auto cs, auto cns, auto ctt) {
-      constexpr int S = decltype(cs)::value, NS = decltype(cns)::value, TT = decltype(ctt)::value;
+    const T *x = (const T *)c.x, *dl = (const T *)c.delta, *z = (const T *)c.z;
+    T *y = (T *)c.y;
+    const auto table = [&](auto ns) {
       if (tokens > 0)
-        bc_kernel<T, NS><<<(unsigned)bcb, 256, 0, s>>>((const T *)c.B, (const T *)c.C, c.B_stride,
-                                                       c.C_stride, tokens, c.G, c.N, S,
-                                                       (float *)(w + plan.off_bc));
-      for (int pass = 0; pass < 2; ++pass)
-        if (total[pass] > 0)
-          ssm_kernel<T, S, NS, TT><<<(unsigned)(total[pass] * blocks), 64 * S, 0, s>>>(
-              tab, a, pass, (const T *)c.x, (const T *)c.delta, (const T *)c.z, (T *)c.y);
+        bc_kernel<T, decltype(ns)::value><<<(unsigned)bcb, 256, 0, s>>>(
+            (const T *)c.B, (const T *)c.C, c.B_stride, c.C_stride, tokens, c.G, c.N, plan.S,
+            (float *)(w + plan.off_bc));
+    };
+    const auto passes = [&](auto &&run) {
+      run(0, (unsigned)(total[0] * per));
+      if (total[1] > 0) {
+        ssm_fold_kernel<<<(unsigned)fold, 256, 0, s>>>(tab, a, SN);
+        run(1, (unsigned)(total[1] * per));
+      }
       return hipGetLastError();
+    };
+    if (plan.lane)
+      return with_lane(plan.NS, [&](auto ns) {
+        return passes([&](int pass, unsigned grid) {
+          ssm_lane_kernel<T, decltype(ns)::value>
+              <<<grid, 256, 0, s>>>(tab, a, pass, x, dl, z, (const T *)c.B, (const T *)c.C, y);
+        });
+      });
+    return with_wide({plan.S, plan.NS}, [&](auto cs, auto ns, auto tt) {
+      table(ns);
+      return passes([&](int pass, unsigned grid) {
+        ssm_kernel<T, decltype(cs)::value, decltype(ns)::value, decltype(tt)::value>
+            <<<grid, 64 * decltype(cs)::value, 0, s>>>(tab, a, pass, x, dl, z, y);
+      });
     });
   };
   return elt == 1 ? typed(bf16()) : typed(float());

@@ -137,9 +137,9 @@ def ssm_io(**kw):
     (INVALID, {}, dict(fin=PTR + (7 << 24), num_slots=0)),
     (INVALID, {}, dict(init=PTR + (7 << 24), fin=PTR + (7 << 24) + 64)),
     (INVALID, {}, dict(slots=PTR + 1)),
-    (WORKSPACE, {}, dict(wsb=0)),
-    (WORKSPACE, {}, dict(ws=None)),
-    (INVALID, {}, dict(ws=PTR + (8 << 24) + 64)),
+    (WORKSPACE, {}, dict(cu=(0, 4096), split=8, wsb=0)),
+    (WORKSPACE, {}, dict(cu=(0, 4096), split=8, ws=None)),
+    (INVALID, {}, dict(cu=(0, 4096), split=8, ws=PTR + (8 << 24) + 64)),
 ])
 def test_selective_scan_refuses(lib, status, io, kw):
     a = dict(cu=(0, 5), D=64, N=16, G=1, dt=BF16, init=None, fin=None, slots=None, num_slots=1,
@@ -165,8 +165,8 @@ def test_selective_scan_refuses_a_null_block_and_bad_bounds(lib):
 def test_selective_scan_workspace_grows_with_the_cut(lib):
     keep, p = cu_ptr(0, 4096)
     one = lib.kda_selective_scan_workspace_size(1, p, 64, 16, 1, 1)
-    assert one >= 4096 * 32 * 4
-    assert lib.kda_selective_scan_workspace_size(1, p, 64, 16, 1, 8) > one
+    # seven transition pairs more: end states [64, 16] and sums [64] each
+    assert lib.kda_selective_scan_workspace_size(1, p, 64, 16, 1, 8) >= one + 7 * 64 * 17 * 4
 
 
 @pytest.mark.parametrize("status,io,kw", [
