@@ -144,10 +144,10 @@ __global__ __launch_bounds__(256) void conv_kernel(SeqTable tab, ConvArgs a,
   const int t0 = (blk - seqs.blk(n, 0)) * a.tile;
   const int len = seqs.len(n);
   const int64_t tok0 = seqs.tok0(n);
-  int64_t slot = n;
+  int64_t slot = seqs.seq(n);
   bool kept = true;
   if (a.slots) {
-    slot = a.slots[n];
+    slot = a.slots[slot];
     kept = slot >= 0 && slot < a.num_slots;
   }
   if (d >= a.D)

@@ -47,9 +47,9 @@ struct SsmCall {
 struct SsmPlan {
   int64_t seg;    // tokens per segment
   int64_t pairs;  // transition pairs of all cut sequences
-  int32_t S, NS;  // waves that share a channel's states, states of each
-  bool lane;      // all states of a channel in one lane
-  size_t off_bc, off_end, off_sum, total; // workspace layout (the table first)
+  bool lane;      // all states of a channel in one lane, or across 16
+  int32_t states; // of a lane
+  size_t off_end, off_sum, total; // workspace layout (the table first)
 };
 SsmPlan ssm_plan(int32_t num_seqs, const int64_t *cu, int32_t D, int32_t N, int32_t G,
                  int32_t split_hint);

@@ -17,10 +17,10 @@ bool aligned_elt(const void *p, kda_dtype dt) {
 }
 int64_t elt_size(kda_dtype dt) { return dt == KDA_BF16 ? 2 : 4; }
 
-// Row strides up to 2^24 elements keep the rows of one tile (16 tokens of at
-// most 4 bytes) within the 32-bit offsets the kernels form inside it; offsets
-// of whole rows are 64-bit.
-constexpr int64_t kMaxStride = (int64_t)1 << 24;
+// Row strides up to 2^22 elements keep the rows of one tile (64 tokens of at
+// most 4 bytes) within the 31-bit offsets the kernels form inside it; offsets
+// of whole tiles are 64-bit.
+constexpr int64_t kMaxStride = (int64_t)1 << 22;
 constexpr int64_t kMaxTokens = (int64_t)1 << 40;
 
 // Packed bounds: 0 first, nondecreasing, no sequence of 2^30 tokens or more.

@@ -16,16 +16,20 @@
 
 namespace kda {
 
-constexpr int kInlineSeqs = 48;  // 49 entries of 16 bytes: 784 of the 4096 argument bytes
-constexpr int kTablePart = 160;  // entries per table-writing launch (2560 of the 4096 bytes)
+constexpr int kInlineSeqs = 48;  // 49 entries of 24 bytes: 1176 of the 4096 argument bytes
+constexpr int kTablePart = 128;  // entries per table-writing launch (3 of the 4 KB)
 
-// Sequence n: its first token, and the blocks before it in each of a call's
-// (at most two) launches.  Entry num_seqs holds the totals.
+// One sequence: its first token, length and number, and the blocks of the
+// entries before it in each of a call's (at most two) launches.  The entry
+// past the last holds the totals.  Inline tables put the longest sequences
+// first, so that the longest serial work starts first and the short ones
+// fill in behind it; longer tables keep the sequences' order.
 struct SeqEntry {
   int64_t tok0;
+  int32_t len, seq;
   int32_t blk[2];
 };
-static_assert(sizeof(SeqEntry) == 16, "SeqEntry layout");
+static_assert(sizeof(SeqEntry) == 24, "SeqEntry layout");
 
 struct SeqTable {
   const SeqEntry *ws; // null: the entries are `in`
@@ -69,19 +73,30 @@ hipError_t make_seq_table(SeqTable &t, int32_t num_seqs, const int64_t *cu, F &&
   t.num_seqs = num_seqs;
   t.pad = 0;
   t.ws = num_seqs <= kInlineSeqs ? nullptr : (const SeqEntry *)ws;
+  int32_t order[kInlineSeqs];
+  if (!t.ws)
+    for (int32_t n = 0; n < num_seqs; ++n) { // by length, stable
+      const int64_t len = cu[n + 1] - cu[n];
+      int32_t i = n;
+      for (; i > 0 && cu[order[i - 1] + 1] - cu[order[i - 1]] < len; --i)
+        order[i] = order[i - 1];
+      order[i] = n;
+    }
   int64_t at[2] = {0, 0};
   TablePart part;
-  for (int32_t n = 0; n <= num_seqs; ++n) {
-    SeqEntry &e = t.ws ? part.e[n % kTablePart] : t.in[n];
+  for (int32_t i = 0; i <= num_seqs; ++i) {
+    SeqEntry &e = t.ws ? part.e[i % kTablePart] : t.in[i];
+    const int32_t n = t.ws || i == num_seqs ? i : order[i];
     e.tok0 = cu[n];
-    e.blk[0] = (int32_t)at[0];
-    e.blk[1] = (int32_t)at[1];
-    if (n < num_seqs)
-      for (int w = 0; w < 2; ++w)
-        at[w] += tiles(cu[n + 1] - cu[n], w);
-    const int filled = n % kTablePart + 1;
-    if (t.ws && (filled == kTablePart || n == num_seqs)) {
-      const hipError_t err = launch_table_part(part, filled, (SeqEntry *)ws + (n + 1 - filled), s);
+    e.seq = n;
+    e.len = i < num_seqs ? (int32_t)(cu[n + 1] - cu[n]) : 0;
+    for (int w = 0; w < 2; ++w) {
+      e.blk[w] = (int32_t)at[w];
+      at[w] += i < num_seqs ? tiles(cu[n + 1] - cu[n], w) : 0;
+    }
+    const int filled = i % kTablePart + 1;
+    if (t.ws && (filled == kTablePart || i == num_seqs)) {
+      const hipError_t err = launch_table_part(part, filled, (SeqEntry *)ws + (i + 1 - filled), s);
       if (err != hipSuccess)
         return err;
     }
@@ -114,13 +129,12 @@ struct SeqView {
     num_seqs = t.num_seqs;
   }
   __device__ __forceinline__ int64_t tok0(int n) const { return e[n].tok0; }
-  __device__ __forceinline__ int32_t len(int n) const {
-    return (int32_t)(e[n + 1].tok0 - e[n].tok0);
-  }
+  __device__ __forceinline__ int32_t len(int n) const { return e[n].len; }
+  __device__ __forceinline__ int32_t seq(int n) const { return e[n].seq; }
   __device__ __forceinline__ int32_t blk(int n, int w) const { return e[n].blk[w]; }
 
-  // The sequence that block b of launch w belongs to: the last n with
-  // blk(n) <= b (sequences without blocks share their successor's count).
+  // The entry that block b of launch w belongs to: the last n with
+  // blk(n) <= b (entries without blocks share their successor's count).
   __device__ __forceinline__ int find(int b, int w) const {
     int lo = 0, hi = num_seqs;
     while (hi - lo > 1) {

@@ -68,270 +68,375 @@ struct SsmArgs {
   int32_t Dg;      // channels per group
   int32_t cb;      // 64-channel blocks per group
   int32_t seg;     // tokens per segment
-  int32_t vec_state; // a channel's states may be read and written NS at a time
-  int64_t T;       // tokens (rows of the B / C table)
   int64_t xs, dls, zs, ys, Bs, Cs;
   const float *A, *skip, *bias;
   const float *init;
   float *fin;
   const int32_t *slots;
-  const float *bc;     // [G][S][T][2 NS]
-  float *pend;         // [pairs][G cb][S NS][64] end states of the segments
+  float *pend;         // [pairs][G cb][SN][64] end states of the segments
   float *psum;         // [pairs][G cb][64] their sums of delta
 };
 
-// ---- B and C as fp32, per wave ---------------------------------------------------
-// Entry (g, w, t): the NS values of B, then of C, that wave w uses for token
-// t and group g; states past N read 0.
-template <typename T, int NS>
-__global__ __launch_bounds__(256) void bc_kernel(const T *__restrict__ B, const T *__restrict__ C,
-                                                 int64_t Bs, int64_t Cs, int64_t tokens, int G,
-                                                 int N, int S, float *__restrict__ out) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  // neighbouring lanes: the waves of one token, so a row of B is read whole
-  const int64_t t = i / (G * S);
-  if (t >= tokens)
-    return;
-  const int gw = (int)(i - t * (G * S)), g = gw / S, w = gw - g * S;
-  float v[2 * NS];
-#pragma unroll
-  for (int k = 0; k < NS; ++k) {
-    const int n = w * NS + k;
-    v[k] = n < N ? to_f32(B[t * Bs + g * N + n]) : 0.f;
-    v[NS + k] = n < N ? to_f32(C[t * Cs + g * N + n]) : 0.f;
-  }
-  float *o = out + ((int64_t)gw * tokens + t) * (2 * NS);
-#pragma unroll
-  for (int k = 0; k < 2 * NS; ++k)
-    o[k] = v[k];
+// ---- raw elements --------------------------------------------------------------------
+// The loaded bits are kept as they are and widened where they are used, so
+// that nothing waits for a load before then.
+template <typename T> struct RawOf { typedef unsigned short type; };
+template <> struct RawOf<float> { typedef unsigned type; };
+template <typename T> using Raw = typename RawOf<T>::type;
+__device__ __forceinline__ float widen(unsigned short r) {
+  return __builtin_bit_cast(float, (unsigned)r << 16);
+}
+__device__ __forceinline__ float widen(unsigned r) { return __builtin_bit_cast(float, r); }
+// The element at byte voff + soff (soff wave-uniform).  voff -1 reads 0 and
+// writes nothing.
+__device__ __forceinline__ unsigned short buffer_raw(__amdgpu_buffer_rsrc_t r, int voff, int soff,
+                                                     const bf16 *) {
+  return __builtin_amdgcn_raw_buffer_load_b16(r, voff, soff, 0);
+}
+__device__ __forceinline__ unsigned buffer_raw(__amdgpu_buffer_rsrc_t r, int voff, int soff,
+                                               const float *) {
+  return __builtin_amdgcn_raw_buffer_load_b32(r, voff, soff, 0);
 }
 
-// ---- one segment of one sequence, 64 channels -------------------------------------
-template <int NS> struct BcVec {
-  float b[NS], c[NS];
+// ---- a channel's states across a row of 16 lanes -------------------------------------
+// Lane (c, i) of a wave, c = lane / 16, i = lane % 16, holds states i, 16 + i,
+// ... (E of them) of channel c, and for every 16 tokens computes delta and
+// delta x of token i of that channel; a token's pair reaches the other lanes
+// of the row as the DPP row broadcast of the two products it enters, at no
+// cost.  The read-out leaves 16 partial products a lane, one for each token,
+// and row_reduce16 adds them across the row so that token i's sum ends in
+// lane i: 33 instructions for 16 tokens instead of 64.
+
+// Token I's value of every row, in all of the row's lanes.
+template <int I> __device__ __forceinline__ float row_bcast(float x) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x150 + I, 0xf, 0xf, true));
+}
+
+template <int CTRL> __device__ __forceinline__ float quad_swap(float x) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+
+// Sum of p[i] over the 16 lanes of each row, in the row's lane i.  Each step
+// halves both the tokens and the lanes still to be added: lanes whose bit is
+// 0 go on with the lower token of a pair, the others with the upper one, each
+// adding its partner's share.  The first two steps write their two halves by
+// DPP bank masks (4 lanes a bank).  (s_nop 1: a DPP operand must be two
+// instructions old, which the compiler does not see inside or around asm.)
+__device__ __forceinline__ float row_reduce16(float (&p)[16], int lane) {
+  asm volatile(
+      "s_nop 1\n\t"
+      "v_add_f32_dpp %0, %0, %0 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %1, %1, %1 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %2, %2, %2 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %3, %3, %3 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %4, %4, %4 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %5, %5, %5 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %6, %6, %6 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %7, %7, %7 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %0, %8, %8 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %1, %9, %9 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %2, %10, %10 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %3, %11, %11 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %4, %12, %12 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %5, %13, %13 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %6, %14, %14 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %7, %15, %15 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "s_nop 1\n\t"
+      "v_add_f32_dpp %0, %0, %0 row_shl:4 row_mask:0xf bank_mask:0x5\n\t"
+      "v_add_f32_dpp %1, %1, %1 row_shl:4 row_mask:0xf bank_mask:0x5\n\t"
+      "v_add_f32_dpp %2, %2, %2 row_shl:4 row_mask:0xf bank_mask:0x5\n\t"
+      "v_add_f32_dpp %3, %3, %3 row_shl:4 row_mask:0xf bank_mask:0x5\n\t"
+      "v_add_f32_dpp %0, %4, %4 row_shr:4 row_mask:0xf bank_mask:0xa\n\t"
+      "v_add_f32_dpp %1, %5, %5 row_shr:4 row_mask:0xf bank_mask:0xa\n\t"
+      "v_add_f32_dpp %2, %6, %6 row_shr:4 row_mask:0xf bank_mask:0xa\n\t"
+      "v_add_f32_dpp %3, %7, %7 row_shr:4 row_mask:0xf bank_mask:0xa\n\t"
+      "s_nop 1"
+      : "+v"(p[0]), "+v"(p[1]), "+v"(p[2]), "+v"(p[3]), "+v"(p[4]), "+v"(p[5]), "+v"(p[6]),
+        "+v"(p[7])
+      : "v"(p[8]), "v"(p[9]), "v"(p[10]), "v"(p[11]), "v"(p[12]), "v"(p[13]), "v"(p[14]),
+        "v"(p[15]));
+  const bool b1 = lane & 2, b0 = lane & 1;
+  float r[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const float keep = b1 ? p[j + 2] : p[j], give = b1 ? p[j] : p[j + 2];
+    r[j] = keep + quad_swap<0x4e>(give); // quad_perm [2, 3, 0, 1]
+  }
+  const float keep = b0 ? r[1] : r[0], give = b0 ? r[0] : r[1];
+  return keep + quad_swap<0xb1>(give); // quad_perm [1, 0, 3, 2]
+}
+
+// One token of the recurrence in all rows: I-th of its 16, k-th of its 4.
+template <int I, int E, bool FULL>
+__device__ __forceinline__ void row_token(float delta, float u, const float (&A2)[E],
+                                          float (&h)[E], const f32x4 (&b)[E], const f32x4 (&c)[E],
+                                          float &p) {
+  const float d = row_bcast<I>(delta), ui = row_bcast<I>(u);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    h[e] = fmaf(exp2_hw(d * A2[e]), h[e], ui * b[e][I & 3]);
+    if (FULL)
+      p = e == 0 ? c[e][I & 3] * h[e] : fmaf(c[e][I & 3], h[e], p);
+  }
+}
+
+constexpr int row_tile(int E) { return E >= 4 ? 16 : 64 / E; }
+
+// Four waves a workgroup: 16 channels; workgroups of one 64-channel stretch.
+constexpr int kRowChans = 16, kRowNear = 64 / kRowChans;
+
+// TT tokens of a workgroup's channels.  (Row pads: the staging threads
+// go down the channels, 64 / CH tokens side by side.)
+template <int E> struct __align__(16) RowLds {
+  static constexpr int TT = row_tile(E), CH = kRowChans;
+  float bc[2][16 * E][TT + 4];       // B, C by state
+  float2 du[CH][TT + 32 / CH];       // (delta, delta x)
+  float y[CH][TT + 64 / CH];         // read-outs
 };
 
-template <int TT, int S> struct SsmLds {
-  f32x4 dx[TT / 2][64];        // (delta, delta x) of two tokens, per channel
-  f32x4 y[S][TT / 4][64];      // partial sums of four tokens, per channel
+// Values a thread stages from a matrix: rows r0, r0 + kStep, ... of a tile,
+// one column.  Rows past the segment and columns past the matrix read 0.
+template <typename T, int kN, int kStep> struct Stage {
+  const T *p;     // the tile's first row
+  int64_t stride; // elements
+  int voff;       // this thread's byte offset in the tile, -1: no column
+  int r0;
+  Raw<T> r[kN];
+
+  __device__ __forceinline__ Stage(const T *p_, int64_t s, int row, int col, bool on)
+      : p(p_), stride(s), voff(on ? (row * (int)s + col) * (int)sizeof(T) : -1), r0(row) {}
+  // rows: how many of the tile's lie in the segment
+  __device__ __forceinline__ void fetch(int rows) {
+    const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(p, rows > 0 ? 0x7fffffff : 0);
+    const int step = kStep * (int)stride * (int)sizeof(T);
+    if (rows >= kN * kStep) {
+#pragma unroll
+      for (int k = 0; k < kN; ++k)
+        r[k] = buffer_raw(rs, voff, k * step, p);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kN; ++k)
+        r[k] = buffer_raw(rs, r0 + k * kStep < rows ? voff : -1, k * step, p);
+    }
+  }
+  __device__ __forceinline__ void next(int rows) { p += rows * stride; }
 };
 
-// FULL: outputs and (last segment) the final state.  Otherwise only the end
-// state from h = 0 and the sum of delta.
-template <typename T, int S, int NS, int TT, bool FULL>
-__device__ __forceinline__ float scan_segment(const SsmArgs &a, SsmLds<TT, S> &lds,
-                                              float (&h)[NS], const float (&A2)[NS],
-                                              const KDA_CONST_AS float *bc, const T *x,
-                                              const T *dl, const T *z, T *y, int ntok, int wave,
-                                              int lane, bool in, float bias, float skip) {
-  constexpr int RP = TT / S > 0 ? TT / S : 1; // tokens a wave stages and finishes
-  constexpr int kBusy = TT / RP;              // waves that do
-  const bool stager = wave < kBusy;
-  const int r0 = wave * RP;
-  T xr[RP], dr[RP], zr[RP];
-  float xk[RP];
+template <typename T, int E, bool FULL>
+__device__ __forceinline__ float row_segment(const SsmArgs &a, RowLds<E> &lds, float (&h)[E],
+                                             const float (&A2)[E], const T *x, const T *dl,
+                                             const T *z, const T *B, const T *C, T *y, int ntok,
+                                             int chans, float bias, float skip) {
+  constexpr int TT = row_tile(E), CH = kRowChans, NP = 16 * E;
+  constexpr int kRows = TT / 16;                     // staged elements per thread
+  constexpr int kBc = TT * NP / 256;                 // B (and C) values per thread
+  constexpr int kBcStep = 256 / NP;                  // tokens between them
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int sc = tid % CH, sr = tid / CH; // channel and first row it stages
+  const int sn = tid % NP, st = tid / NP; // state and first token of B and C
+  const int rc = wave * 4 + (lane >> 4), ri = lane & 15;
+  const bool in = sc < chans;
+  Stage<T, kRows, 16> sx(x, a.xs, sr, sc, in), sd(dl, a.dls, sr, sc, in), sz(z, a.zs, sr, sc, in);
+  Stage<T, kBc, kBcStep> sb(B, a.Bs, st, sn, sn < a.N), scc(C, a.Cs, st, sn, sn < a.N);
+  const int yoff = in ? (sr * (int)a.ys + sc) * (int)sizeof(T) : -1;
+  const int ystep = 16 * (int)a.ys * (int)sizeof(T);
+  float xk[kRows];
   float sum = 0.f;
 
-  const auto fetch = [&](int t0) {
-    const int n = ntok - t0;
-#pragma unroll
-    for (int r = 0; r < RP; ++r) {
-      const int64_t t = t0 + r0 + r;
-      xr[r] = T(0.f);
-      dr[r] = T(0.f);
-      if (stager && r0 + r < n && in) {
-        xr[r] = x[t * a.xs];
-        dr[r] = dl[t * a.dls];
-      }
+  const auto fetch = [&](int rows) {
+    sx.fetch(rows);
+    sd.fetch(rows);
+    sb.fetch(rows);
+    if (FULL) {
+      scc.fetch(rows);
+      if (z)
+        sz.fetch(rows);
     }
+    sx.next(TT);
+    sd.next(TT);
+    sz.next(TT);
+    sb.next(TT);
+    scc.next(TT);
   };
 
-  fetch(0);
+  fetch(ntok);
   for (int t0 = 0; t0 < ntok; t0 += TT) {
     const int n = min(TT, ntok - t0);
-    // stage this tile's delta and delta x
-    if (stager) {
-      float pair[RP][2];
+    float d[kRows], gate[kRows];
 #pragma unroll
-      for (int r = 0; r < RP; ++r) {
-        const float xv = to_f32(xr[r]);
-        float d = to_f32(dr[r]) + bias;
-        if (a.softplus)
-          d = softplus(d);
-        xk[r] = xv;
-        pair[r][0] = d;
-        pair[r][1] = d * xv;
-      }
-      if constexpr (RP % 2 == 0) {
-#pragma unroll
-        for (int r = 0; r < RP; r += 2)
-          lds.dx[(r0 + r) / 2][lane] =
-              f32x4{pair[r][0], pair[r][1], pair[r + 1][0], pair[r + 1][1]};
-      } else {
-        float *p = reinterpret_cast<float *>(&lds.dx[r0 / 2][lane]) + (r0 & 1) * 2;
-        p[0] = pair[0][0];
-        p[1] = pair[0][1];
-      }
+    for (int k = 0; k < kRows; ++k) {
+      xk[k] = widen(sx.r[k]);
+      d[k] = widen(sd.r[k]) + bias;
+      gate[k] = 1.f;
     }
-    __syncthreads();
-
-    // in flight during the recurrence: the next tile's inputs, this one's gate
-    fetch(t0 + TT);
+    if (a.softplus) {
+#pragma unroll
+      for (int k = 0; k < kRows; ++k)
+        d[k] = softplus(d[k]);
+    }
     if (FULL && z) {
 #pragma unroll
-      for (int r = 0; r < RP; ++r)
-        if (stager && r0 + r < n && in)
-          zr[r] = z[(int64_t)(t0 + r0 + r) * a.zs];
+      for (int k = 0; k < kRows; ++k)
+        gate[k] = silu(widen(sz.r[k]));
     }
+    // past the segment's end a step of 0 (with x and B 0) leaves h as it is
+    if (n < TT) {
+#pragma unroll
+      for (int k = 0; k < kRows; ++k)
+        d[k] = sr + 16 * k < n ? d[k] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+      lds.du[sc][sr + 16 * k] = float2{d[k], d[k] * xk[k]};
+#pragma unroll
+    for (int k = 0; k < kBc; ++k) {
+      lds.bc[0][sn][st + k * kBcStep] = widen(sb.r[k]);
+      if (FULL)
+        lds.bc[1][sn][st + k * kBcStep] = widen(scc.r[k]);
+    }
+    __syncthreads();
+    fetch(ntok - t0 - TT); // in flight during the recurrence
 
-    const KDA_CONST_AS float *tb = bc + (int64_t)t0 * (2 * NS);
-    int t = 0;
-    for (; t + 4 <= n; t += 4) {
-      const f32x4 p0 = lds.dx[t / 2][lane], p1 = lds.dx[t / 2 + 1][lane];
-      const float d[4] = {p0[0], p0[2], p1[0], p1[2]};
-      const float u[4] = {p0[1], p0[3], p1[1], p1[3]};
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int s0 = 0; s0 < n; s0 += 16) {
+      const float2 du = lds.du[rc][s0 + ri];
+      float p[16];
+      const auto quad = [&](auto q) {
+        constexpr int Q = decltype(q)::value;
+        f32x4 b[E], c[E];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const KDA_CONST_AS float *row = tb + (t + k) * (2 * NS);
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          h[i] = fmaf(exp2_hw(d[k] * A2[i]), h[i], u[k] * row[i]);
+        for (int e = 0; e < E; ++e) {
+          b[e] = *reinterpret_cast<const f32x4 *>(&lds.bc[0][16 * e + ri][s0 + 4 * Q]);
           if (FULL)
-            acc[k] = fmaf(row[NS + i], h[i], acc[k]);
+            c[e] = *reinterpret_cast<const f32x4 *>(&lds.bc[1][16 * e + ri][s0 + 4 * Q]);
         }
-        if (!FULL)
-          sum += d[k];
-      }
+        row_token<4 * Q, E, FULL>(du.x, du.y, A2, h, b, c, p[4 * Q]);
+        row_token<4 * Q + 1, E, FULL>(du.x, du.y, A2, h, b, c, p[4 * Q + 1]);
+        row_token<4 * Q + 2, E, FULL>(du.x, du.y, A2, h, b, c, p[4 * Q + 2]);
+        row_token<4 * Q + 3, E, FULL>(du.x, du.y, A2, h, b, c, p[4 * Q + 3]);
+      };
+      quad(std::integral_constant<int, 0>());
+      quad(std::integral_constant<int, 1>());
+      quad(std::integral_constant<int, 2>());
+      quad(std::integral_constant<int, 3>());
       if (FULL)
-        lds.y[wave][t / 4][lane] = acc;
-    }
-    for (; t < n; ++t) { // the last tokens of a segment, one by one
-      const f32x4 p0 = lds.dx[t / 2][lane];
-      const float d = t & 1 ? p0[2] : p0[0], u = t & 1 ? p0[3] : p0[1];
-      const KDA_CONST_AS float *row = tb + t * (2 * NS);
-      float acc = 0.f;
-#pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        h[i] = fmaf(exp2_hw(d * A2[i]), h[i], u * row[i]);
-        if (FULL)
-          acc = fmaf(row[NS + i], h[i], acc);
-      }
-      if (FULL)
-        reinterpret_cast<float *>(&lds.y[wave][t / 4][lane])[t & 3] = acc;
+        lds.y[rc][s0 + ri] = row_reduce16(p, lane);
       else
-        sum += d;
+        sum += du.x; // (lane i: the tokens i of every 16)
     }
     __syncthreads();
 
-    if (FULL && stager) {
+    if (FULL) {
+      const __amdgpu_buffer_rsrc_t ry = buffer_rsrc(y, 0x7fffffff);
 #pragma unroll
-      for (int r = 0; r < RP; ++r) {
-        const int row = r0 + r;
-        if (row >= n)
-          break;
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < S; ++w)
-          v += reinterpret_cast<const float *>(&lds.y[w][row / 4][lane])[row & 3];
-        v = fmaf(skip, xk[r], v);
-        if (z)
-          v *= silu(to_f32(zr[r]));
-        if (in)
-          y[(int64_t)(t0 + row) * a.ys] = from_f32<T>(v);
+      for (int k = 0; k < kRows; ++k) {
+        const int row = sr + 16 * k;
+        const float v = fmaf(skip, xk[k], lds.y[sc][row]);
+        buffer_store(ry, from_f32<T>(z ? v * gate[k] : v), row < n ? yoff : -1, k * ystep);
       }
+      y += TT * a.ys;
     }
   }
   return sum;
 }
 
-// pass 0: first segments (full) and middle ones (end states); pass 1: every
-// segment but the first, in full.
-template <typename T, int S, int NS, int TT>
-__global__ __launch_bounds__(64 * S) void ssm_kernel(SeqTable tab, SsmArgs a, int pass,
-                                                     const T *__restrict__ x,
-                                                     const T *__restrict__ dl,
-                                                     const T *__restrict__ z,
-                                                     T *__restrict__ y) {
-  __shared__ SsmLds<TT, S> lds;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int blocks = a.G * a.cb;
-  const int sb = blockIdx.x / blocks, gc = blockIdx.x - sb * blocks;
-  const int g = gc / a.cb, cbi = gc - g * a.cb;
+template <typename T, int E>
+__global__ __launch_bounds__(256) void ssm_row_kernel(SeqTable tab, SsmArgs a, int pass,
+                                                          int64_t grid,
+                                                          const T *__restrict__ x,
+                                                          const T *__restrict__ dl,
+                                                          const T *__restrict__ z,
+                                                          const T *__restrict__ B,
+                                                          const T *__restrict__ C,
+                                                          T *__restrict__ y) {
+  __shared__ RowLds<E> lds;
+  constexpr int CH = kRowChans;
+  // Workgroups go round the eight dies; those of one 64-channel stretch, which
+  // share its cache lines, are put on one die.
+  constexpr int kNear = kRowNear;
+  const int64_t bid =
+      ((int64_t)(blockIdx.x / (8 * kNear)) * 8 + blockIdx.x % 8) * kNear + blockIdx.x / 8 % kNear;
+  if (bid >= grid)
+    return;
+  const int rb = (a.Dg + CH - 1) / CH, blocks = a.G * rb;
+  const int sb = (int)(bid / blocks), gr = (int)(bid - (int64_t)sb * blocks);
+  const int g = gr / rb, c0 = (gr - g * rb) * CH; // first channel in its group
   const SeqView seqs(tab);
   const int n = seqs.find(sb, pass);
   const int len = seqs.len(n);
   const int64_t tok0 = seqs.tok0(n);
   const int nseg = len > a.seg ? (len + a.seg - 1) / a.seg : 1;
   const int j = sb - seqs.blk(n, pass) + pass;
-  const int64_t pair0 = seqs.blk(n, 1); // its nseg - 1 transition pairs
+  const int64_t pair0 = seqs.blk(n, 1);
   const int s0 = j * a.seg, ntok = min(a.seg, len - s0);
-  const bool full = pass == 1 || j == 0;
 
-  const int dg = cbi * 64 + lane; // channel in its group
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int ri = lane & 15;
+  const int dg = c0 + (tid >> 6) * 4 + (lane >> 4); // the channel whose states it holds
   const bool in = dg < a.Dg;
   const int64_t d = (int64_t)g * a.Dg + dg;
-  const int n0 = wave * NS;
-
-  float A2[NS], h[NS];
+  float A2[E], h[E];
 #pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    A2[i] = in && n0 + i < a.N ? a.A[d * a.N + n0 + i] * kLog2e : 0.f;
-    h[i] = 0.f;
+  for (int e = 0; e < E; ++e) {
+    A2[e] = in && 16 * e + ri < a.N ? a.A[d * a.N + 16 * e + ri] * kLog2e : 0.f;
+    h[e] = 0.f;
   }
-  int64_t slot = n;
+  int64_t slot = seqs.seq(n);
   bool kept = true;
   if (a.slots) {
-    slot = a.slots[n];
+    slot = a.slots[slot];
     kept = slot >= 0 && slot < a.num_slots;
   }
+  // states in segment pairs: [pair][64-channel block][state][channel]
+  const int64_t at = ((int64_t)(g * a.cb + dg / 64) * (16 * E) + ri) * 64 + dg % 64;
+  const int64_t pstep = (int64_t)a.G * a.cb * (16 * E) * 64;
   if (j == 0) {
     if (a.init && kept && in) {
-      const float *p = a.init + (slot * a.D + d) * a.N + n0;
 #pragma unroll
-      for (int i = 0; i < NS; ++i)
-        if (n0 + i < a.N)
-          h[i] = p[i];
+      for (int e = 0; e < E; ++e)
+        if (16 * e + ri < a.N)
+          h[e] = a.init[(slot * a.D + d) * a.N + 16 * e + ri];
     }
-  } else if (full) {
-    const float *pe = a.pend + (((pair0 + j - 1) * blocks + gc) * S + wave) * NS * 64 + lane;
+  } else if (pass == 1 && in) {
 #pragma unroll
-    for (int i = 0; i < NS; ++i)
-      h[i] = pe[i * 64];
+    for (int e = 0; e < E; ++e)
+      h[e] = a.pend[(pair0 + j - 1) * pstep + at + e * 16 * 64];
   }
 
-  const KDA_CONST_AS float *bc =
-      (const KDA_CONST_AS float *)(uintptr_t)(a.bc +
-                                              (((int64_t)g * S + wave) * a.T + tok0 + s0) * 2 * NS);
-  const int64_t t0 = tok0 + s0;
-  const float bias = in && a.bias ? a.bias[d] : 0.f;
-  const float skip = in && a.skip ? a.skip[d] : 0.f;
+  const int64_t t0 = tok0 + s0, d0 = (int64_t)g * a.Dg + c0;
+  const int chans = min(CH, a.Dg - c0);
+  const int sc = tid % CH; // the channel it stages
+  const float bias = a.bias && sc < chans ? a.bias[d0 + sc] : 0.f;
+  const float skip = a.skip && sc < chans ? a.skip[d0 + sc] : 0.f;
+  x += t0 * a.xs + d0;
+  dl += t0 * a.dls + d0;
+  B += t0 * a.Bs + g * a.N;
+  C += t0 * a.Cs + g * a.N;
   float sum = 0.f;
-  if (full)
-    scan_segment<T, S, NS, TT, true>(a, lds, h, A2, bc, x + t0 * a.xs + d, dl + t0 * a.dls + d,
-                                     z ? z + t0 * a.zs + d : nullptr, y + t0 * a.ys + d, ntok,
-                                     wave, lane, in, bias, skip);
+  if (pass == 1 || j == 0)
+    row_segment<T, E, true>(a, lds, h, A2, x, dl, z ? z + t0 * a.zs + d0 : nullptr, B, C,
+                                y + t0 * a.ys + d0, ntok, chans, bias, skip);
   else
-    sum = scan_segment<T, S, NS, TT, false>(a, lds, h, A2, bc, x + t0 * a.xs + d,
-                                            dl + t0 * a.dls + d, nullptr, nullptr, ntok, wave,
-                                            lane, in, bias, skip);
+    sum = row_segment<T, E, false>(a, lds, h, A2, x, dl, nullptr, B, C, nullptr, ntok, chans,
+                                       bias, skip);
 
   if (j == nseg - 1) {
     if (a.fin && kept && in) {
-      float *p = a.fin + (slot * a.D + d) * a.N + n0;
 #pragma unroll
-      for (int i = 0; i < NS; ++i)
-        if (n0 + i < a.N)
-          p[i] = h[i];
+      for (int e = 0; e < E; ++e)
+        if (16 * e + ri < a.N)
+          a.fin[(slot * a.D + d) * a.N + 16 * e + ri] = h[e];
     }
   } else if (pass == 0) {
-    float *pe = a.pend + (((pair0 + j) * blocks + gc) * S + wave) * NS * 64 + lane;
+    sum = row_scan16(sum); // lane 15: the whole segment's
+    if (in) {
 #pragma unroll
-    for (int i = 0; i < NS; ++i)
-      pe[i * 64] = h[i];
-    if (j > 0 && wave == 0)
-      a.psum[((pair0 + j) * blocks + gc) * 64 + lane] = sum;
+      for (int e = 0; e < E; ++e)
+        a.pend[(pair0 + j) * pstep + at + e * 16 * 64] = h[e];
+      if (j > 0 && ri == 15)
+        a.psum[((pair0 + j) * a.G * a.cb + g * a.cb + dg / 64) * 64 + dg % 64] = sum;
+    }
   }
 }
 
@@ -348,26 +453,9 @@ template <int NS> struct LaneBc {
 
 // One element per lane of a row of channels; lanes at or past `bytes` (the
 // row's end, or 0 for a token past the segment) read 0 and write nothing.
-// The loaded bits are kept as they are and widened where they are used, so
-// that nothing waits for a load before then.
-template <typename T> struct RawOf { typedef unsigned short type; };
-template <> struct RawOf<float> { typedef unsigned type; };
-template <typename T> using Raw = typename RawOf<T>::type;
-__device__ __forceinline__ float widen(unsigned short r) {
-  return __builtin_bit_cast(float, (unsigned)r << 16);
-}
-__device__ __forceinline__ float widen(unsigned r) { return __builtin_bit_cast(float, r); }
-__device__ __forceinline__ unsigned short buffer_raw(__amdgpu_buffer_rsrc_t r, int voff,
-                                                     const bf16 *) {
-  return __builtin_amdgcn_raw_buffer_load_b16(r, voff, 0, 0);
-}
-__device__ __forceinline__ unsigned buffer_raw(__amdgpu_buffer_rsrc_t r, int voff,
-                                               const float *) {
-  return __builtin_amdgcn_raw_buffer_load_b32(r, voff, 0, 0);
-}
 template <typename T>
 __device__ __forceinline__ Raw<T> row_load(const T *p, int bytes, int lane) {
-  return buffer_raw(buffer_rsrc(p, bytes), lane * (int)sizeof(T), p);
+  return buffer_raw(buffer_rsrc(p, bytes), lane * (int)sizeof(T), 0, p);
 }
 template <typename T>
 __device__ __forceinline__ void row_store(T *p, int bytes, int lane, float v) {
@@ -401,8 +489,8 @@ template <typename T, int NS> struct BcLoader {
     for (int k = 0; k < kPer; ++k) {
       const int t = t0 + k * kStep;
       const bool ok = on && tok + t < ntok;
-      b[k] = buffer_raw(rb, ok ? (t * (int)Bs + i) * (int)sizeof(T) : -1, B);
-      c[k] = buffer_raw(rc, ok ? (t * (int)Cs + i) * (int)sizeof(T) : -1, C);
+      b[k] = buffer_raw(rb, ok ? (t * (int)Bs + i) * (int)sizeof(T) : -1, 0, B);
+      c[k] = buffer_raw(rc, ok ? (t * (int)Cs + i) * (int)sizeof(T) : -1, 0, C);
     }
   }
   __device__ __forceinline__ void put(float (*area)[2 * NS]) const {
@@ -541,10 +629,10 @@ __global__ __launch_bounds__(256, 4) void ssm_lane_kernel(SeqTable tab, SsmArgs 
     A2[i] = in && i < a.N ? a.A[d * a.N + i] * kLog2e : 0.f;
     h[i] = 0.f;
   }
-  int64_t slot = n;
+  int64_t slot = seqs.seq(n);
   bool kept = true;
   if (a.slots) {
-    slot = a.slots[n];
+    slot = a.slots[slot];
     kept = slot >= 0 && slot < a.num_slots;
   }
   if (j == 0) {
@@ -736,46 +824,15 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(StepArgs a, const T *__re
 }
 
 // ---- host ---------------------------------------------------------------------------
-// Waves per workgroup and states per wave of the wide kernel (states dealt to
-// the waves), and states of the lane kernel.
-struct Shape {
-  int S, NS;
-};
-Shape wide_shape(int N) {
-  if (N <= 8)
-    return {2, 4};
-  if (N <= 16)
-    return {4, 4};
-  if (N <= 32)
-    return {8, 4};
-  if (N <= 64)
-    return {16, 4};
-  return {16, 8};
-}
+// States a lane holds in the lane kernel, and in the row kernel.
 int lane_states(int N) { return N <= 4 ? 4 : (N <= 8 ? 8 : 16); }
+int row_states(int N) { return N <= 16 ? 1 : (N <= 32 ? 2 : (N <= 64 ? 4 : 8)); }
 constexpr int kLaneMaxStates = 16;
 
 constexpr size_t kAlign = 256;
 size_t up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 int64_t chan_blocks(int32_t D, int32_t G) { return (int64_t)G * ((D / G + 63) / 64); }
-
-template <typename F> hipError_t with_wide(Shape sh, F &&f) {
-  using std::integral_constant;
-  using i2 = integral_constant<int, 2>;
-  using i4 = integral_constant<int, 4>;
-  using i8 = integral_constant<int, 8>;
-  using i16 = integral_constant<int, 16>;
-  using i32 = integral_constant<int, 32>;
-  if (sh.NS == 8)
-    return f(i16(), i8(), i16());
-  switch (sh.S) {
-  case 2: return f(i2(), i4(), i16());
-  case 4: return f(i4(), i4(), i32());
-  case 8: return f(i8(), i4(), i32());
-  default: return f(i16(), i4(), i16());
-  }
-}
 
 template <typename F> hipError_t with_lane(int NS, F &&f) {
   using std::integral_constant;
@@ -786,12 +843,33 @@ template <typename F> hipError_t with_lane(int NS, F &&f) {
   return f(integral_constant<int, 16>());
 }
 
+template <typename F> hipError_t with_row(int E, F &&f) {
+  using std::integral_constant;
+  switch (E) {
+  case 1: return f(integral_constant<int, 1>());
+  case 2: return f(integral_constant<int, 2>());
+  case 4: return f(integral_constant<int, 4>());
+  default: return f(integral_constant<int, 8>());
+  }
+}
+
 } // namespace
 
 int64_t ssm_num_segments(int64_t len, const SsmPlan &p) {
   return len > p.seg ? (len + p.seg - 1) / p.seg : 1;
 }
 
+// Which kernel, and the cut.  Times in us from runs over D = 1536 .. 12288,
+// 1 .. 64 sequences and 1024 .. 16384 tokens, N = 16 (measured / chosen over):
+//   row kernel, uncut: 36 ns a token of the longest sequence where its waves
+//     have a SIMD each to themselves; a wave more on the SIMD adds 16.5 ns.
+//     A sequence costs some 80 tokens to begin (tiles of 64).
+//   lane kernel, uncut: 0.25 ns per token and 64 channels at full occupancy,
+//     0.45 us a token of the longest sequence for a wave alone.
+//   lane kernel, cut into segments for four waves a SIMD: 0.43 ns per token
+//     and 64 channels (the middle segments run twice) plus 55 us.
+// 8192 tokens x 8192 channels: row 419, lane cut 463.  131072 x 1536: row
+// 4700, lane cut 1331.  64 sequences of 16 tokens x 8192: row 189, lane 110.
 SsmPlan ssm_plan(int32_t num_seqs, const int64_t *cu, int32_t D, int32_t N, int32_t G,
                  int32_t split_hint) {
   SsmPlan p{};
@@ -801,23 +879,39 @@ SsmPlan ssm_plan(int32_t num_seqs, const int64_t *cu, int32_t D, int32_t N, int3
     longest = std::max(longest, cu[n + 1] - cu[n]);
   // multiples of 32 tokens: whole tiles
   const auto whole = [](int64_t x) { return std::max<int64_t>(32, (x + 31) / 32 * 32); };
-  const Shape sh = wide_shape(N);
   p.seg = whole(longest);
-  p.lane = N <= kLaneMaxStates;
+  const int NS = lane_states(N), E = row_states(N);
+  const double T = (double)tokens, L = (double)longest, W = (double)blocks, n = num_seqs;
+  // (states beside 16: the states' share of each kernel's instructions)
+  const double row_scale = (33. * E + 15.) / 48., full = (24. * NS + 150.) / 534. * 0.25e-3,
+               half = (20. * NS + 90.) / 410. * 0.18e-3;
+  const double per_simd = W * 16. / 1024.; // row waves a SIMD, one sequence
+  const double row = row_scale * std::max(0.036 * L, 0.020 * L + 0.0165 * per_simd * (T + 80. * n));
+  const double lane = 0.45 * L * NS / 16. + W * (T + 24. * n) * full;
+  const int64_t lane_seg = std::max<int64_t>(64, whole(tokens * blocks / 4096));
+  const double cut = 55. + W * T * (full + half);
+  p.lane = false;
   if (split_hint > 1) {
+    p.lane = N <= kLaneMaxStates;
     p.seg = whole((longest + split_hint - 1) / split_hint);
+  } else if (N <= kLaneMaxStates) {
+    p.lane = lane < row;
+    if (split_hint == 0 && cut < std::min(lane, row) && lane_seg * 3 <= longest) {
+      p.lane = true;
+      p.seg = lane_seg;
+    }
   } else if (split_hint == 0) {
-    const int64_t want = p.lane ? tokens * blocks / 4096 : tokens * blocks / 1024;
-    p.seg = std::min(p.seg, std::max<int64_t>(64, whole(want)));
+    // more states than the lane kernel holds: cut for two row waves a SIMD,
+    // where that leaves at least four segments (their middle ones run twice)
+    const int64_t seg = std::max<int64_t>(128, whole(tokens * blocks * 16 / 2048));
+    if (seg * 4 <= longest)
+      p.seg = seg;
   }
-  p.S = p.lane ? 1 : sh.S;
-  p.NS = p.lane ? lane_states(N) : sh.NS;
+  p.states = p.lane ? NS : E;
   for (int32_t n = 0; n < num_seqs; ++n)
     p.pairs += ssm_num_segments(cu[n + 1] - cu[n], p) - 1;
-  const size_t SN = (size_t)p.S * p.NS;
+  const size_t SN = (size_t)p.states * (p.lane ? 1 : 16);
   size_t o = seq_table_bytes(num_seqs);
-  p.off_bc = o;
-  o = up(o + (p.lane ? 0 : (size_t)tokens * G * SN * 2 * sizeof(float)));
   p.off_end = o;
   o = up(o + (size_t)p.pairs * blocks * 64 * SN * sizeof(float));
   p.off_sum = o;
@@ -830,7 +924,7 @@ hipError_t launch_ssm(int elt, const SsmCall &c, int32_t num_seqs, const int64_t
                       const SsmPlan &plan, void *ws, hipStream_t s) {
   const int64_t tokens = cu[num_seqs];
   const int64_t blocks = chan_blocks(c.D, c.G);
-  const int SN = plan.S * plan.NS;
+  const int SN = plan.states * (plan.lane ? 1 : 16);
   uint8_t *w = (uint8_t *)ws;
 
   SsmArgs a{};
@@ -842,7 +936,6 @@ hipError_t launch_ssm(int elt, const SsmCall &c, int32_t num_seqs, const int64_t
   a.Dg = c.D / c.G;
   a.cb = (a.Dg + 63) / 64;
   a.seg = (int32_t)plan.seg;
-  a.T = tokens;
   a.xs = c.x_stride;
   a.dls = c.delta_stride;
   a.zs = c.z_stride;
@@ -855,7 +948,6 @@ hipError_t launch_ssm(int elt, const SsmCall &c, int32_t num_seqs, const int64_t
   a.init = c.init;
   a.fin = c.fin;
   a.slots = c.slots;
-  a.bc = (const float *)(w + plan.off_bc);
   a.pend = (float *)(w + plan.off_end);
   a.psum = (float *)(w + plan.off_sum);
 
@@ -866,15 +958,18 @@ hipError_t launch_ssm(int elt, const SsmCall &c, int32_t num_seqs, const int64_t
   int64_t total[2];
   if (!seq_totals(num_seqs, cu, tiles, total))
     return hipErrorInvalidConfiguration;
-  // workgroups per (segment, all channels) and threads per workgroup
-  const int64_t per = plan.lane ? (blocks + 3) / 4 : blocks;
-  const int64_t threads = plan.lane ? 256 : 64 * plan.S;
-  for (int pass = 0; pass < 2; ++pass)
-    if (total[pass] * per > INT32_MAX || total[pass] * per * threads > UINT32_MAX)
+  // workgroups per (segment, all channels); the row kernel's grid is rounded
+  // up to whole rounds over the dies
+  const int64_t per = plan.lane ? (blocks + 3) / 4 : (int64_t)c.G * ((a.Dg + kRowChans - 1) / kRowChans);
+  const int64_t round = plan.lane ? 1 : 8 * kRowNear;
+  int64_t grid[2];
+  for (int pass = 0; pass < 2; ++pass) {
+    grid[pass] = (total[pass] * per + round - 1) / round * round;
+    if (grid[pass] * 256 > UINT32_MAX)
       return hipErrorInvalidConfiguration;
-  const int64_t bcb = (tokens * c.G * plan.S + 255) / 256;
+  }
   const int64_t fold = plan.pairs > 0 ? ((int64_t)num_seqs * blocks * SN + 3) / 4 : 0;
-  if (bcb * 256 > UINT32_MAX || fold * 256 > UINT32_MAX)
+  if (fold * 256 > UINT32_MAX)
     return hipErrorInvalidConfiguration;
   SeqTable tab;
   hipError_t e = make_seq_table(tab, num_seqs, cu, tiles, ws, s);
@@ -884,33 +979,26 @@ hipError_t launch_ssm(int elt, const SsmCall &c, int32_t num_seqs, const int64_t
   const auto typed = [&](auto tag) {
     using T = decltype(tag);
     const T *x = (const T *)c.x, *dl = (const T *)c.delta, *z = (const T *)c.z;
+    const T *B = (const T *)c.B, *C = (const T *)c.C;
     T *y = (T *)c.y;
-    const auto table = [&](auto ns) {
-      if (tokens > 0)
-        bc_kernel<T, decltype(ns)::value><<<(unsigned)bcb, 256, 0, s>>>(
-            (const T *)c.B, (const T *)c.C, c.B_stride, c.C_stride, tokens, c.G, c.N, plan.S,
-            (float *)(w + plan.off_bc));
-    };
     const auto passes = [&](auto &&run) {
-      run(0, (unsigned)(total[0] * per));
+      run(0, (unsigned)grid[0]);
       if (total[1] > 0) {
         ssm_fold_kernel<<<(unsigned)fold, 256, 0, s>>>(tab, a, SN);
-        run(1, (unsigned)(total[1] * per));
+        run(1, (unsigned)grid[1]);
       }
       return hipGetLastError();
     };
     if (plan.lane)
-      return with_lane(plan.NS, [&](auto ns) {
-        return passes([&](int pass, unsigned grid) {
-          ssm_lane_kernel<T, decltype(ns)::value>
-              <<<grid, 256, 0, s>>>(tab, a, pass, x, dl, z, (const T *)c.B, (const T *)c.C, y);
+      return with_lane(plan.states, [&](auto ns) {
+        return passes([&](int pass, unsigned n) {
+          ssm_lane_kernel<T, decltype(ns)::value><<<n, 256, 0, s>>>(tab, a, pass, x, dl, z, B, C, y);
         });
       });
-    return with_wide({plan.S, plan.NS}, [&](auto cs, auto ns, auto tt) {
-      table(ns);
-      return passes([&](int pass, unsigned grid) {
-        ssm_kernel<T, decltype(cs)::value, decltype(ns)::value, decltype(tt)::value>
-            <<<grid, 64 * decltype(cs)::value, 0, s>>>(tab, a, pass, x, dl, z, y);
+    return with_row(plan.states, [&](auto e) {
+      return passes([&](int pass, unsigned n) {
+        ssm_row_kernel<T, decltype(e)::value>
+            <<<n, 256, 0, s>>>(tab, a, pass, total[pass] * per, x, dl, z, B, C, y);
       });
     });
   };

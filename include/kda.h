@@ -479,7 +479,7 @@ kda_status kda_segment_scan(int32_t num_segs, int32_t H, int32_t dk, int32_t dv,
  *
  * Conventions of these calls, beside those above
  * - Token matrices ([T, D]) may be column ranges of a wider one: each has a
- *   row stride in elements, at least its row length and at most 2^24, and
+ *   row stride in elements, at least its row length and at most 2^22, and
  *   needs only its element type's alignment (16-byte-aligned rows run the
  *   vector loads).
  *   Weights, biases, A and states are dense and 16-byte aligned.

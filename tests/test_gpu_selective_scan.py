@@ -312,3 +312,18 @@ def test_offsets_past_32_bits():
     y2 = kda.selective_scan_step(last, **a)
     torch.cuda.synchronize()
     assert torch.equal(y, y2) and torch.equal(pool[-1:], last)
+
+
+@pytest.mark.parametrize("name,lengths,D,N,G", [
+    ("many short prompts of many channels", [1 + i % 5 for i in range(300)], 1024, 16, 1),
+    ("few states, many prompts", [7] * 100, 512, 3, 2),
+    ("many states, one long prompt", [2100, 40], 64, 20, 1),
+    ("all states, one long prompt", [1030], 32, 128, 2),
+    ("one long prompt", [4000], 128, 16, 1),
+])
+def test_automatic_choice_at_its_edges(name, lengths, D, N, G):
+    """Shapes for which the call picks each of its kernels and cuts by itself."""
+    print("scan", name, flush=True)
+    for dtype in (F32, BF16):
+        c = case(lengths, D, N, G, dtype, 180)
+        compare(c, *run(c))
