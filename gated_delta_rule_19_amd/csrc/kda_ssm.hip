@@ -730,18 +730,19 @@ __global__ __launch_bounds__(256) void ssm_fold_kernel(SeqTable tab, SsmArgs a, 
 
 // ---- single tokens ------------------------------------------------------------------
 // A channel's N states lie side by side on `lanes` neighbouring lanes, VEC on
-// each, K times; a wave takes 64 / lanes channels of one row.  The state is
-// read once and written once: bound by HBM.
+// each, K times; a wave takes 64 / lanes channels of R rows, whose A, bias
+// and skip it reads once.  The state is read once and written once: bound by
+// HBM.
 struct StepArgs {
-  int32_t D, N, Dg, softplus, num_slots, lanes_log2;
-  int64_t cw, waves; // waves per row, all waves
+  int32_t D, N, Dg, rows, softplus, num_slots, lanes_log2;
+  int64_t cw, waves; // waves per R rows, all waves
   int64_t xs, dls, zs, ys, Bs, Cs;
   const float *A, *skip, *bias;
   float *state;
   const int32_t *slots;
 };
 
-template <typename T, int VEC, int K>
+template <typename T, int VEC, int K, int R>
 __global__ __launch_bounds__(256) void ssm_step_kernel(StepArgs a, const T *__restrict__ x,
                                                        const T *__restrict__ dl,
                                                        const T *__restrict__ B,
@@ -750,76 +751,111 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(StepArgs a, const T *__re
   const int64_t wv = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (wv >= a.waves)
     return;
-  const int row = (int)(wv / a.cw);
-  const int64_t slot = a.slots ? a.slots[row] : row;
-  if (slot < 0 || slot >= a.num_slots)
-    return; // a padding row: nothing is read or written
+  const int64_t rg = wv / a.cw;
   const int lanes = 1 << a.lanes_log2;
   const int lane = threadIdx.x & (lanes - 1);
   const int64_t d =
-      (wv - row * a.cw) * (64 >> a.lanes_log2) + ((threadIdx.x & 63) >> a.lanes_log2);
+      (wv - rg * a.cw) * (64 >> a.lanes_log2) + ((threadIdx.x & 63) >> a.lanes_log2);
   const bool in = d < a.D;
   const int64_t g = in ? d / a.Dg : 0;
 
-  float h[K][VEC], A[K][VEC], b[K][VEC], c[K][VEC];
-  float *st = a.state + (slot * a.D + d) * a.N;
+  // everything the R rows read is in flight together
+  float *st[R];
+  bool on[R]; // a padding row: nothing is read or written
+  float h[R][K][VEC], b[R][K][VEC], c[R][K][VEC], xv[R], dv[R], zv[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t row = rg * R + r;
+    int64_t slot = -1;
+    if (row < a.rows)
+      slot = a.slots ? a.slots[row] : row;
+    on[r] = slot >= 0 && slot < a.num_slots;
+    st[r] = a.state + (slot * a.D + d) * a.N;
+    xv[r] = dv[r] = zv[r] = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int n = (k * lanes + lane) * VEC;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        h[r][k][i] = b[r][k][i] = c[r][k][i] = 0.f;
+      if (on[r] && in && n < a.N) {
+        if constexpr (VEC == 4) {
+          const f32x4 hv = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(st[r] + n));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            h[r][k][i] = hv[i];
+        } else {
+          h[r][k][0] = st[r][n];
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          b[r][k][i] = to_f32(B[row * a.Bs + g * a.N + n + i]);
+          c[r][k][i] = to_f32(C[row * a.Cs + g * a.N + n + i]);
+        }
+      }
+    }
+    if (on[r] && in) {
+      xv[r] = to_f32(x[row * a.xs + d]);
+      dv[r] = to_f32(dl[row * a.dls + d]);
+      if (z)
+        zv[r] = to_f32(z[row * a.zs + d]);
+    }
+  }
+  float A2[K][VEC];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int n = (k * lanes + lane) * VEC;
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
-      h[k][i] = A[k][i] = b[k][i] = c[k][i] = 0.f;
+      A2[k][i] = 0.f;
     if (in && n < a.N) {
       if constexpr (VEC == 4) {
-        const f32x4 hv = *reinterpret_cast<const f32x4 *>(st + n);
         const f32x4 av = *reinterpret_cast<const f32x4 *>(a.A + d * a.N + n);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          h[k][i] = hv[i];
-          A[k][i] = av[i];
-        }
+        for (int i = 0; i < 4; ++i)
+          A2[k][i] = av[i] * kLog2e;
       } else {
-        h[k][0] = st[n];
-        A[k][0] = a.A[d * a.N + n];
+        A2[k][0] = a.A[d * a.N + n] * kLog2e;
       }
+    }
+  }
+  const float bias = in && a.bias ? a.bias[d] : 0.f, skip = in && a.skip ? a.skip[d] : 0.f;
+
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t row = rg * R + r;
+    if (!on[r])
+      continue;
+    float delta = dv[r] + bias;
+    if (a.softplus)
+      delta = softplus(delta);
+    const float u = delta * xv[r];
+    float acc = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int n = (k * lanes + lane) * VEC;
+      float nh[VEC];
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        b[k][i] = to_f32(B[row * a.Bs + g * a.N + n + i]);
-        c[k][i] = to_f32(C[row * a.Cs + g * a.N + n + i]);
+        nh[i] = fmaf(exp2_hw(delta * A2[k][i]), h[r][k][i], u * b[r][k][i]);
+        acc = fmaf(c[r][k][i], nh[i], acc);
+      }
+      if (in && n < a.N) {
+        if constexpr (VEC == 4)
+          __builtin_nontemporal_store(f32x4{nh[0], nh[1], nh[2], nh[3]},
+                                      reinterpret_cast<f32x4 *>(st[r] + n));
+        else
+          st[r][n] = nh[0];
       }
     }
-  }
-  float xv = 0.f, dv = 0.f;
-  if (in) {
-    xv = to_f32(x[row * a.xs + d]);
-    dv = to_f32(dl[row * a.dls + d]) + (a.bias ? a.bias[d] : 0.f);
-  }
-  if (a.softplus)
-    dv = softplus(dv);
-  const float u = dv * xv;
-  float acc = 0.f;
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int n = (k * lanes + lane) * VEC;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      h[k][i] = fmaf(exp2_hw(dv * (A[k][i] * kLog2e)), h[k][i], u * b[k][i]);
-      acc = fmaf(c[k][i], h[k][i], acc);
+    for (int m = 0; m < a.lanes_log2; ++m)
+      acc += __shfl_xor(acc, 1 << m);
+    if (in && lane == 0) {
+      float v = fmaf(skip, xv[r], acc);
+      if (z)
+        v *= silu(zv[r]);
+      y[row * a.ys + d] = from_f32<T>(v);
     }
-    if (in && n < a.N) {
-      if constexpr (VEC == 4)
-        *reinterpret_cast<f32x4 *>(st + n) = f32x4{h[k][0], h[k][1], h[k][2], h[k][3]};
-      else
-        st[n] = h[k][0];
-    }
-  }
-  for (int m = 0; m < a.lanes_log2; ++m)
-    acc += __shfl_xor(acc, 1 << m);
-  if (in && lane == 0) {
-    float v = fmaf(a.skip ? a.skip[d] : 0.f, xv, acc);
-    if (z)
-      v *= silu(to_f32(z[row * a.zs + d]));
-    y[row * a.ys + d] = from_f32<T>(v);
   }
 }
 
@@ -1028,25 +1064,32 @@ hipError_t launch_ssm_step(int elt, const SsmCall &c, int32_t rows, hipStream_t 
   while ((1 << a.lanes_log2) < need && a.lanes_log2 < 6)
     ++a.lanes_log2;
   const int per = 64 >> a.lanes_log2;
+  a.rows = rows;
   a.cw = (c.D + per - 1) / per;
-  a.waves = a.cw * rows;
+  // four rows a wave where that leaves four waves a SIMD
+  const int R = a.cw * (rows / 4) >= 4096 ? 4 : 1;
+  a.waves = a.cw * ((rows + R - 1) / R);
   if ((a.waves + 3) / 4 * 256 > UINT32_MAX)
     return hipErrorInvalidConfiguration;
-  const auto run = [&](auto tag, auto vec, auto k) {
+  using std::integral_constant;
+  const auto run = [&](auto tag, auto vec, auto k, auto r) {
     using T = decltype(tag);
-    ssm_step_kernel<T, decltype(vec)::value, decltype(k)::value>
+    ssm_step_kernel<T, decltype(vec)::value, decltype(k)::value, decltype(r)::value>
         <<<(unsigned)((a.waves + 3) / 4), 256, 0, s>>>(a, (const T *)c.x, (const T *)c.delta,
                                                        (const T *)c.B, (const T *)c.C,
                                                        (const T *)c.z, (T *)c.y);
     return hipGetLastError();
   };
   const auto shaped = [&](auto tag) {
-    using std::integral_constant;
+    const auto rowed = [&](auto vec, auto k) {
+      return R == 4 ? run(tag, vec, k, integral_constant<int, 4>())
+                    : run(tag, vec, k, integral_constant<int, 1>());
+    };
     if (wide)
-      return run(tag, integral_constant<int, 4>(), integral_constant<int, 1>());
+      return rowed(integral_constant<int, 4>(), integral_constant<int, 1>());
     if (need <= 64)
-      return run(tag, integral_constant<int, 1>(), integral_constant<int, 1>());
-    return run(tag, integral_constant<int, 1>(), integral_constant<int, 2>());
+      return rowed(integral_constant<int, 1>(), integral_constant<int, 1>());
+    return rowed(integral_constant<int, 1>(), integral_constant<int, 2>());
   };
   return elt == 1 ? shaped(bf16()) : shaped(float());
 }
