@@ -729,133 +729,182 @@ __global__ __launch_bounds__(256) void ssm_fold_kernel(SeqTable tab, SsmArgs a, 
 }
 
 // ---- single tokens ------------------------------------------------------------------
-// A channel's N states lie side by side on `lanes` neighbouring lanes, VEC on
-// each, K times; a wave takes 64 / lanes channels of R rows, whose A, bias
-// and skip it reads once.  The state is read once and written once: bound by
-// HBM.
+// A wave takes 64 channels of one row.  The state is read once and written
+// once, so HBM bounds the call as long as little else goes through the memory
+// pipe: x, delta, z and y move one channel a lane (softplus and gate are
+// evaluated there), B and C once a wave; the states pass in chunks of 64 / W
+// channels, W lanes a channel with VEC states on each (K times), which get
+// their channel's delta and delta x from its lane and give their sum back to
+// it.
 struct StepArgs {
-  int32_t D, N, Dg, rows, softplus, num_slots, lanes_log2;
-  int64_t cw, waves; // waves per R rows, all waves
+  int32_t D, N, G, Dg, cb, rows, softplus, num_slots, wlog, bcvec;
   int64_t xs, dls, zs, ys, Bs, Cs;
   const float *A, *skip, *bias;
   float *state;
   const int32_t *slots;
 };
 
-template <typename T, int VEC, int K, int R>
+// Sum over groups of 2^wlog neighbouring lanes, in every lane of the group.
+__device__ __forceinline__ float group_sum(float x, int wlog) {
+  if (wlog > 0)
+    x += quad_swap<0xb1>(x); // lane ^ 1
+  if (wlog > 1)
+    x += quad_swap<0x4e>(x); // lane ^ 2
+  if (wlog > 2)
+    x += quad_swap<0x141>(x); // mirrored in 8 lanes: the other quad
+  if (wlog > 3)
+    x += quad_swap<0x140>(x); // mirrored in 16 lanes: the other eight
+  if (wlog > 4)
+    x = add_xor16(x);
+  if (wlog > 5)
+    x = add_xor32(x);
+  return x;
+}
+
+// Four consecutive values of B or C.
+__device__ __forceinline__ void load4(const bf16 *p, float (&v)[4]) {
+  const bf16x4 r = *reinterpret_cast<const bf16x4 *>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = to_f32(r[i]);
+}
+__device__ __forceinline__ void load4(const float *p, float (&v)[4]) {
+  const f32x4 r = *reinterpret_cast<const f32x4 *>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = r[i];
+}
+
+template <typename T, int VEC, int K>
 __global__ __launch_bounds__(256) void ssm_step_kernel(StepArgs a, const T *__restrict__ x,
                                                        const T *__restrict__ dl,
                                                        const T *__restrict__ B,
                                                        const T *__restrict__ C,
                                                        const T *__restrict__ z, T *y) {
+  // the waves of a workgroup: four rows of the same channels, whose A they
+  // share in the compute unit's cache
   const int64_t wv = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (wv >= a.waves)
+  const int64_t blocks = (int64_t)a.G * a.cb, q = wv / (4 * blocks);
+  const int64_t row = q * 4 + wv % 4, gc = wv / 4 % blocks;
+  if (row >= a.rows)
     return;
-  const int64_t rg = wv / a.cw;
-  const int lanes = 1 << a.lanes_log2;
-  const int lane = threadIdx.x & (lanes - 1);
-  const int64_t d =
-      (wv - rg * a.cw) * (64 >> a.lanes_log2) + ((threadIdx.x & 63) >> a.lanes_log2);
-  const bool in = d < a.D;
-  const int64_t g = in ? d / a.Dg : 0;
+  const int64_t slot = a.slots ? a.slots[row] : row;
+  if (slot < 0 || slot >= a.num_slots)
+    return; // a padding row: nothing is read or written
+  const int lane = threadIdx.x & 63;
+  const int64_t g = gc / a.cb;
+  const int c0 = (int)(gc - g * a.cb) * 64; // first channel, in its group
+  const int64_t d0 = g * a.Dg + c0;
+  const int chans = min(64, a.Dg - c0);
+  const int W = 1 << a.wlog, per = 64 >> a.wlog; // lanes a channel, channels a chunk
+  const int w = lane & (W - 1), cc = lane >> a.wlog;
 
-  // everything the R rows read is in flight together
-  float *st[R];
-  bool on[R]; // a padding row: nothing is read or written
-  float h[R][K][VEC], b[R][K][VEC], c[R][K][VEC], xv[R], dv[R], zv[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int64_t row = rg * R + r;
-    int64_t slot = -1;
-    if (row < a.rows)
-      slot = a.slots ? a.slots[row] : row;
-    on[r] = slot >= 0 && slot < a.num_slots;
-    st[r] = a.state + (slot * a.D + d) * a.N;
-    xv[r] = dv[r] = zv[r] = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int n = (k * lanes + lane) * VEC;
-#pragma unroll
-      for (int i = 0; i < VEC; ++i)
-        h[r][k][i] = b[r][k][i] = c[r][k][i] = 0.f;
-      if (on[r] && in && n < a.N) {
-        if constexpr (VEC == 4) {
-          const f32x4 hv = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(st[r] + n));
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            h[r][k][i] = hv[i];
-        } else {
-          h[r][k][0] = st[r][n];
-        }
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          b[r][k][i] = to_f32(B[row * a.Bs + g * a.N + n + i]);
-          c[r][k][i] = to_f32(C[row * a.Cs + g * a.N + n + i]);
-        }
-      }
-    }
-    if (on[r] && in) {
-      xv[r] = to_f32(x[row * a.xs + d]);
-      dv[r] = to_f32(dl[row * a.dls + d]);
-      if (z)
-        zv[r] = to_f32(z[row * a.zs + d]);
-    }
+  // this lane's channel
+  float xv = 0.f, delta = 0.f, zv = 0.f, skip = 0.f;
+  if (lane < chans) {
+    xv = to_f32(x[row * a.xs + d0 + lane]);
+    delta = to_f32(dl[row * a.dls + d0 + lane]) + (a.bias ? a.bias[d0 + lane] : 0.f);
+    if (z)
+      zv = to_f32(z[row * a.zs + d0 + lane]);
+    if (a.skip)
+      skip = a.skip[d0 + lane];
   }
-  float A2[K][VEC];
+  // this lane's states in every chunk
+  float b[K][VEC], c[K][VEC];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int n = (k * lanes + lane) * VEC;
+    const int n = (k * W + w) * VEC;
+    const T *pb = B + row * a.Bs + g * a.N + n, *pc = C + row * a.Cs + g * a.N + n;
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
-      A2[k][i] = 0.f;
-    if (in && n < a.N) {
-      if constexpr (VEC == 4) {
-        const f32x4 av = *reinterpret_cast<const f32x4 *>(a.A + d * a.N + n);
+      b[k][i] = c[k][i] = 0.f;
+    if (n < a.N) {
+      bool done = false;
+      if constexpr (VEC == 4)
+        if (a.bcvec) {
+          load4(pb, b[k]);
+          load4(pc, c[k]);
+          done = true;
+        }
+      if (!done) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          A2[k][i] = av[i] * kLog2e;
-      } else {
-        A2[k][0] = a.A[d * a.N + n] * kLog2e;
+        for (int i = 0; i < VEC; ++i) {
+          b[k][i] = to_f32(pb[i]);
+          c[k][i] = to_f32(pc[i]);
+        }
       }
     }
   }
-  const float bias = in && a.bias ? a.bias[d] : 0.f, skip = in && a.skip ? a.skip[d] : 0.f;
+  if (a.softplus)
+    delta = softplus(delta);
+  const float u = delta * xv;
 
+  float *st = a.state + (slot * a.D + d0) * a.N;
+  const float *Ad = a.A + d0 * a.N;
+  float out = 0.f;
+  constexpr int kU = K == 1 ? 4 : 2; // chunks whose states are in flight together
+  for (int k0 = 0; k0 < W; k0 += kU) {
+    float h[kU][K][VEC], A[kU][K][VEC];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int64_t row = rg * R + r;
-    if (!on[r])
-      continue;
-    float delta = dv[r] + bias;
-    if (a.softplus)
-      delta = softplus(delta);
-    const float u = delta * xv[r];
-    float acc = 0.f;
+    for (int j = 0; j < kU; ++j) {
+      const int ch = (k0 + j) * per + cc;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int n = (k * lanes + lane) * VEC;
-      float nh[VEC];
+      for (int k = 0; k < K; ++k) {
+        const int n = (k * W + w) * VEC;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        nh[i] = fmaf(exp2_hw(delta * A2[k][i]), h[r][k][i], u * b[r][k][i]);
-        acc = fmaf(c[r][k][i], nh[i], acc);
-      }
-      if (in && n < a.N) {
-        if constexpr (VEC == 4)
-          __builtin_nontemporal_store(f32x4{nh[0], nh[1], nh[2], nh[3]},
-                                      reinterpret_cast<f32x4 *>(st[r] + n));
-        else
-          st[r][n] = nh[0];
+        for (int i = 0; i < VEC; ++i)
+          h[j][k][i] = A[j][k][i] = 0.f;
+        if (k0 + j < W && ch < chans && n < a.N) {
+          if constexpr (VEC == 4) {
+            const f32x4 hv = __builtin_nontemporal_load(
+                reinterpret_cast<const f32x4 *>(st + ch * a.N + n));
+            const f32x4 av = *reinterpret_cast<const f32x4 *>(Ad + ch * a.N + n);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              h[j][k][i] = hv[i];
+              A[j][k][i] = av[i];
+            }
+          } else {
+            h[j][k][0] = st[ch * a.N + n];
+            A[j][k][0] = Ad[ch * a.N + n];
+          }
+        }
       }
     }
-    for (int m = 0; m < a.lanes_log2; ++m)
-      acc += __shfl_xor(acc, 1 << m);
-    if (in && lane == 0) {
-      float v = fmaf(skip, xv[r], acc);
-      if (z)
-        v *= silu(zv[r]);
-      y[row * a.ys + d] = from_f32<T>(v);
+#pragma unroll
+    for (int j = 0; j < kU; ++j) {
+      if (k0 + j >= W)
+        break;
+      const int ch = (k0 + j) * per + cc;
+      const float dj = __shfl(delta, ch) * kLog2e, uj = __shfl(u, ch);
+      float acc = 0.f;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int n = (k * W + w) * VEC;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          h[j][k][i] = fmaf(exp2_hw(dj * A[j][k][i]), h[j][k][i], uj * b[k][i]);
+          acc = fmaf(c[k][i], h[j][k][i], acc);
+        }
+        if (ch < chans && n < a.N) {
+          if constexpr (VEC == 4)
+            __builtin_nontemporal_store(f32x4{h[j][k][0], h[j][k][1], h[j][k][2], h[j][k][3]},
+                                        reinterpret_cast<f32x4 *>(st + ch * a.N + n));
+          else
+            st[ch * a.N + n] = h[j][k][0];
+        }
+      }
+      acc = group_sum(acc, a.wlog);
+      // channel's lane l: chunk l / per, whose lanes (l % per) W .. hold it
+      const float mine = __shfl(acc, (lane & (per - 1)) << a.wlog);
+      out = lane >> (6 - a.wlog) == k0 + j ? mine : out;
     }
+  }
+  if (lane < chans) {
+    float v = fmaf(skip, xv, out);
+    if (z)
+      v *= silu(zv);
+    y[row * a.ys + d0 + lane] = from_f32<T>(v);
   }
 }
 
@@ -1059,37 +1108,33 @@ hipError_t launch_ssm_step(int elt, const SsmCall &c, int32_t rows, hipStream_t 
   a.bias = c.bias;
   a.state = c.fin;
   a.slots = c.slots;
+  a.G = c.G;
+  a.cb = (a.Dg + 63) / 64;
+  a.rows = rows;
   const bool wide = c.N % 4 == 0; // (the state and A are 16-byte aligned)
   const int need = wide ? c.N / 4 : c.N;
-  while ((1 << a.lanes_log2) < need && a.lanes_log2 < 6)
-    ++a.lanes_log2;
-  const int per = 64 >> a.lanes_log2;
-  a.rows = rows;
-  a.cw = (c.D + per - 1) / per;
-  // four rows a wave where that leaves four waves a SIMD
-  const int R = a.cw * (rows / 4) >= 4096 ? 4 : 1;
-  a.waves = a.cw * ((rows + R - 1) / R);
-  if ((a.waves + 3) / 4 * 256 > UINT32_MAX)
+  while ((1 << a.wlog) < need && a.wlog < 6)
+    ++a.wlog;
+  const uintptr_t quad = elt == 1 ? 8 : 16;
+  a.bcvec = (uintptr_t)c.B % quad == 0 && (uintptr_t)c.C % quad == 0 && c.B_stride % 4 == 0 &&
+            c.C_stride % 4 == 0;
+  const int64_t grid = ((int64_t)rows + 3) / 4 * c.G * a.cb;
+  if (grid * 256 > UINT32_MAX)
     return hipErrorInvalidConfiguration;
-  using std::integral_constant;
-  const auto run = [&](auto tag, auto vec, auto k, auto r) {
+  const auto run = [&](auto tag, auto vec, auto k) {
     using T = decltype(tag);
-    ssm_step_kernel<T, decltype(vec)::value, decltype(k)::value, decltype(r)::value>
-        <<<(unsigned)((a.waves + 3) / 4), 256, 0, s>>>(a, (const T *)c.x, (const T *)c.delta,
-                                                       (const T *)c.B, (const T *)c.C,
-                                                       (const T *)c.z, (T *)c.y);
+    ssm_step_kernel<T, decltype(vec)::value, decltype(k)::value><<<(unsigned)grid, 256, 0, s>>>(
+        a, (const T *)c.x, (const T *)c.delta, (const T *)c.B, (const T *)c.C, (const T *)c.z,
+        (T *)c.y);
     return hipGetLastError();
   };
   const auto shaped = [&](auto tag) {
-    const auto rowed = [&](auto vec, auto k) {
-      return R == 4 ? run(tag, vec, k, integral_constant<int, 4>())
-                    : run(tag, vec, k, integral_constant<int, 1>());
-    };
+    using std::integral_constant;
     if (wide)
-      return rowed(integral_constant<int, 4>(), integral_constant<int, 1>());
+      return run(tag, integral_constant<int, 4>(), integral_constant<int, 1>());
     if (need <= 64)
-      return rowed(integral_constant<int, 1>(), integral_constant<int, 1>());
-    return rowed(integral_constant<int, 1>(), integral_constant<int, 2>());
+      return run(tag, integral_constant<int, 1>(), integral_constant<int, 1>());
+    return run(tag, integral_constant<int, 1>(), integral_constant<int, 2>());
   };
   return elt == 1 ? shaped(bf16()) : shaped(float());
 }
