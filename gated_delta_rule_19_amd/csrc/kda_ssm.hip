@@ -78,24 +78,51 @@ struct SsmArgs {
 };
 
 // ---- raw elements --------------------------------------------------------------------
-// The loaded bits are kept as they are and widened where they are used, so
-// that nothing waits for a load before then.
-template <typename T> struct RawOf { typedef unsigned short type; };
-template <> struct RawOf<float> { typedef unsigned type; };
-template <typename T> using Raw = typename RawOf<T>::type;
-__device__ __forceinline__ float widen(unsigned short r) {
-  return __builtin_bit_cast(float, (unsigned)r << 16);
+// The loaded bits (of P = 1 or 2 neighbouring elements) are kept as they are
+// and widened where they are used, so that nothing waits for a load before
+// then.
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+template <typename T, int P> struct RawOf;
+template <> struct RawOf<bf16, 1> { typedef unsigned short type; };
+template <> struct RawOf<bf16, 2> { typedef unsigned type; };
+template <> struct RawOf<float, 1> { typedef unsigned type; };
+template <> struct RawOf<float, 2> { typedef u32x2 type; };
+template <typename T, int P = 1> using Raw = typename RawOf<T, P>::type;
+
+template <typename T, int P> __device__ __forceinline__ float widen(Raw<T, P> r, int j) {
+  unsigned u;
+  if constexpr (sizeof(T) == 2)
+    u = P == 1 || j == 0 ? (unsigned)r << 16 : (unsigned)r & 0xffff0000u;
+  else if constexpr (P == 1)
+    u = r;
+  else
+    u = j == 0 ? r.x : r.y;
+  return __builtin_bit_cast(float, u);
 }
-__device__ __forceinline__ float widen(unsigned r) { return __builtin_bit_cast(float, r); }
-// The element at byte voff + soff (soff wave-uniform).  voff -1 reads 0 and
+// The elements at byte voff + soff (soff wave-uniform).  voff -1 reads 0 and
 // writes nothing.
-__device__ __forceinline__ unsigned short buffer_raw(__amdgpu_buffer_rsrc_t r, int voff, int soff,
-                                                     const bf16 *) {
-  return __builtin_amdgcn_raw_buffer_load_b16(r, voff, soff, 0);
+template <typename T, int P>
+__device__ __forceinline__ Raw<T, P> buffer_raw(__amdgpu_buffer_rsrc_t r, int voff, int soff) {
+  if constexpr (sizeof(T) * P == 2)
+    return __builtin_amdgcn_raw_buffer_load_b16(r, voff, soff, 0);
+  else if constexpr (sizeof(T) * P == 4)
+    return __builtin_amdgcn_raw_buffer_load_b32(r, voff, soff, 0);
+  else
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, voff, soff, 0));
 }
-__device__ __forceinline__ unsigned buffer_raw(__amdgpu_buffer_rsrc_t r, int voff, int soff,
-                                               const float *) {
-  return __builtin_amdgcn_raw_buffer_load_b32(r, voff, soff, 0);
+template <typename T, int P>
+__device__ __forceinline__ void buffer_put(__amdgpu_buffer_rsrc_t r, const float (&v)[P], int voff,
+                                           int soff) {
+  if constexpr (P == 1) {
+    buffer_store(r, from_f32<T>(v[0]), voff, soff);
+  } else if constexpr (sizeof(T) == 2) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 w = {static_cast<bf16>(v[0]), static_cast<bf16>(v[1])};
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, w), r, voff, soff, 0);
+  } else {
+    const f32x2_t w = {v[0], v[1]};
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, w), r, voff, soff, 0);
+  }
 }
 
 // ---- a channel's states across a row of 16 lanes -------------------------------------
@@ -196,14 +223,15 @@ template <int E> struct __align__(16) RowLds {
   float y[CH][TT + 64 / CH];         // read-outs
 };
 
-// Values a thread stages from a matrix: rows r0, r0 + kStep, ... of a tile,
-// one column.  Rows past the segment and columns past the matrix read 0.
-template <typename T, int kN, int kStep> struct Stage {
+// Values a thread stages from a matrix: rows r0, r0 + kStep, ... of a tile, P
+// neighbouring columns.  Rows past the segment and columns past the matrix
+// read 0.
+template <typename T, int P, int kN, int kStep> struct Stage {
   const T *p;     // the tile's first row
   int64_t stride; // elements
   int voff;       // this thread's byte offset in the tile, -1: no column
   int r0;
-  Raw<T> r[kN];
+  Raw<T, P> r[kN];
 
   __device__ __forceinline__ Stage(const T *p_, int64_t s, int row, int col, bool on)
       : p(p_), stride(s), voff(on ? (row * (int)s + col) * (int)sizeof(T) : -1), r0(row) {}
@@ -214,35 +242,40 @@ template <typename T, int kN, int kStep> struct Stage {
     if (rows >= kN * kStep) {
 #pragma unroll
       for (int k = 0; k < kN; ++k)
-        r[k] = buffer_raw(rs, voff, k * step, p);
+        r[k] = buffer_raw<T, P>(rs, voff, k * step);
     } else {
 #pragma unroll
       for (int k = 0; k < kN; ++k)
-        r[k] = buffer_raw(rs, r0 + k * kStep < rows ? voff : -1, k * step, p);
+        r[k] = buffer_raw<T, P>(rs, r0 + k * kStep < rows ? voff : -1, k * step);
     }
   }
+  __device__ __forceinline__ float at(int k, int j) const { return widen<T, P>(r[k], j); }
   __device__ __forceinline__ void next(int rows) { p += rows * stride; }
 };
 
-template <typename T, int E, bool FULL>
+template <typename T, int E, int P, bool FULL>
 __device__ __forceinline__ float row_segment(const SsmArgs &a, RowLds<E> &lds, float (&h)[E],
                                              const float (&A2)[E], const T *x, const T *dl,
                                              const T *z, const T *B, const T *C, T *y, int ntok,
-                                             int chans, float bias, float skip) {
+                                             int chans, const float (&bias)[P],
+                                             const float (&skip)[P]) {
   constexpr int TT = row_tile(E), CH = kRowChans, NP = 16 * E;
-  constexpr int kRows = TT / 16;                     // staged elements per thread
-  constexpr int kBc = TT * NP / 256;                 // B (and C) values per thread
-  constexpr int kBcStep = 256 / NP;                  // tokens between them
+  constexpr int kStep = 256 * P / CH;       // rows the threads stage at a time
+  constexpr int kRows = TT / kStep;         // elements (or pairs) of a thread
+  constexpr int kBcStep = 256 * P / NP;     // likewise for B and C
+  constexpr int kBc = TT / kBcStep;
+  static_assert(kRows >= 1 && kBc >= 1, "the threads cover at most a tile");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int sc = tid % CH, sr = tid / CH; // channel and first row it stages
-  const int sn = tid % NP, st = tid / NP; // state and first token of B and C
+  const int sc = tid % (CH / P) * P, sr = tid / (CH / P); // channel and first row it stages
+  const int sn = tid % (NP / P) * P, st = tid / (NP / P); // state and first token of B and C
   const int rc = wave * 4 + (lane >> 4), ri = lane & 15;
   const bool in = sc < chans;
-  Stage<T, kRows, 16> sx(x, a.xs, sr, sc, in), sd(dl, a.dls, sr, sc, in), sz(z, a.zs, sr, sc, in);
-  Stage<T, kBc, kBcStep> sb(B, a.Bs, st, sn, sn < a.N), scc(C, a.Cs, st, sn, sn < a.N);
+  Stage<T, P, kRows, kStep> sx(x, a.xs, sr, sc, in), sd(dl, a.dls, sr, sc, in),
+      sz(z, a.zs, sr, sc, in);
+  Stage<T, P, kBc, kBcStep> sb(B, a.Bs, st, sn, sn < a.N), scc(C, a.Cs, st, sn, sn < a.N);
   const int yoff = in ? (sr * (int)a.ys + sc) * (int)sizeof(T) : -1;
-  const int ystep = 16 * (int)a.ys * (int)sizeof(T);
-  float xk[kRows];
+  const int ystep = kStep * (int)a.ys * (int)sizeof(T);
+  float xk[kRows][P];
   float sum = 0.f;
 
   const auto fetch = [&](int rows) {
@@ -264,38 +297,50 @@ __device__ __forceinline__ float row_segment(const SsmArgs &a, RowLds<E> &lds, f
   fetch(ntok);
   for (int t0 = 0; t0 < ntok; t0 += TT) {
     const int n = min(TT, ntok - t0);
-    float d[kRows], gate[kRows];
+    float d[kRows][P], gate[kRows][P];
 #pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      xk[k] = widen(sx.r[k]);
-      d[k] = widen(sd.r[k]) + bias;
-      gate[k] = 1.f;
-    }
+    for (int k = 0; k < kRows; ++k)
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        xk[k][j] = sx.at(k, j);
+        d[k][j] = sd.at(k, j) + bias[j];
+        gate[k][j] = 1.f;
+      }
     if (a.softplus) {
 #pragma unroll
       for (int k = 0; k < kRows; ++k)
-        d[k] = softplus(d[k]);
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+          d[k][j] = softplus(d[k][j]);
     }
     if (FULL && z) {
 #pragma unroll
       for (int k = 0; k < kRows; ++k)
-        gate[k] = silu(widen(sz.r[k]));
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+          gate[k][j] = silu(sz.at(k, j));
     }
     // past the segment's end a step of 0 (with x and B 0) leaves h as it is
     if (n < TT) {
 #pragma unroll
       for (int k = 0; k < kRows; ++k)
-        d[k] = sr + 16 * k < n ? d[k] : 0.f;
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+          d[k][j] = sr + kStep * k < n ? d[k][j] : 0.f;
     }
 #pragma unroll
     for (int k = 0; k < kRows; ++k)
-      lds.du[sc][sr + 16 * k] = float2{d[k], d[k] * xk[k]};
 #pragma unroll
-    for (int k = 0; k < kBc; ++k) {
-      lds.bc[0][sn][st + k * kBcStep] = widen(sb.r[k]);
-      if (FULL)
-        lds.bc[1][sn][st + k * kBcStep] = widen(scc.r[k]);
-    }
+      for (int j = 0; j < P; ++j)
+        lds.du[sc + j][sr + kStep * k] = float2{d[k][j], d[k][j] * xk[k][j]};
+#pragma unroll
+    for (int k = 0; k < kBc; ++k)
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        lds.bc[0][sn + j][st + k * kBcStep] = sb.at(k, j);
+        if (FULL)
+          lds.bc[1][sn + j][st + k * kBcStep] = scc.at(k, j);
+      }
     __syncthreads();
     fetch(ntok - t0 - TT); // in flight during the recurrence
 
@@ -331,9 +376,15 @@ __device__ __forceinline__ float row_segment(const SsmArgs &a, RowLds<E> &lds, f
       const __amdgpu_buffer_rsrc_t ry = buffer_rsrc(y, 0x7fffffff);
 #pragma unroll
       for (int k = 0; k < kRows; ++k) {
-        const int row = sr + 16 * k;
-        const float v = fmaf(skip, xk[k], lds.y[sc][row]);
-        buffer_store(ry, from_f32<T>(z ? v * gate[k] : v), row < n ? yoff : -1, k * ystep);
+        const int row = sr + kStep * k;
+        float v[P];
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          v[j] = fmaf(skip[j], xk[k][j], lds.y[sc + j][row]);
+          if (z)
+            v[j] *= gate[k][j];
+        }
+        buffer_put<T, P>(ry, v, row < n ? yoff : -1, k * ystep);
       }
       y += TT * a.ys;
     }
@@ -341,7 +392,7 @@ __device__ __forceinline__ float row_segment(const SsmArgs &a, RowLds<E> &lds, f
   return sum;
 }
 
-template <typename T, int E>
+template <typename T, int E, int P>
 __global__ __launch_bounds__(256) void ssm_row_kernel(SeqTable tab, SsmArgs a, int pass,
                                                           int64_t grid,
                                                           const T *__restrict__ x,
@@ -406,19 +457,23 @@ __global__ __launch_bounds__(256) void ssm_row_kernel(SeqTable tab, SsmArgs a, i
 
   const int64_t t0 = tok0 + s0, d0 = (int64_t)g * a.Dg + c0;
   const int chans = min(CH, a.Dg - c0);
-  const int sc = tid % CH; // the channel it stages
-  const float bias = a.bias && sc < chans ? a.bias[d0 + sc] : 0.f;
-  const float skip = a.skip && sc < chans ? a.skip[d0 + sc] : 0.f;
+  const int sc = tid % (CH / P) * P; // the channels it stages
+  float bias[P], skip[P];
+#pragma unroll
+  for (int q = 0; q < P; ++q) {
+    bias[q] = a.bias && sc + q < chans ? a.bias[d0 + sc + q] : 0.f;
+    skip[q] = a.skip && sc + q < chans ? a.skip[d0 + sc + q] : 0.f;
+  }
   x += t0 * a.xs + d0;
   dl += t0 * a.dls + d0;
   B += t0 * a.Bs + g * a.N;
   C += t0 * a.Cs + g * a.N;
   float sum = 0.f;
   if (pass == 1 || j == 0)
-    row_segment<T, E, true>(a, lds, h, A2, x, dl, z ? z + t0 * a.zs + d0 : nullptr, B, C,
+    row_segment<T, E, P, true>(a, lds, h, A2, x, dl, z ? z + t0 * a.zs + d0 : nullptr, B, C,
                                 y + t0 * a.ys + d0, ntok, chans, bias, skip);
   else
-    sum = row_segment<T, E, false>(a, lds, h, A2, x, dl, nullptr, B, C, nullptr, ntok, chans,
+    sum = row_segment<T, E, P, false>(a, lds, h, A2, x, dl, nullptr, B, C, nullptr, ntok, chans,
                                        bias, skip);
 
   if (j == nseg - 1) {
@@ -455,7 +510,7 @@ template <int NS> struct LaneBc {
 // row's end, or 0 for a token past the segment) read 0 and write nothing.
 template <typename T>
 __device__ __forceinline__ Raw<T> row_load(const T *p, int bytes, int lane) {
-  return buffer_raw(buffer_rsrc(p, bytes), lane * (int)sizeof(T), 0, p);
+  return buffer_raw<T, 1>(buffer_rsrc(p, bytes), lane * (int)sizeof(T), 0);
 }
 template <typename T>
 __device__ __forceinline__ void row_store(T *p, int bytes, int lane, float v) {
@@ -489,15 +544,15 @@ template <typename T, int NS> struct BcLoader {
     for (int k = 0; k < kPer; ++k) {
       const int t = t0 + k * kStep;
       const bool ok = on && tok + t < ntok;
-      b[k] = buffer_raw(rb, ok ? (t * (int)Bs + i) * (int)sizeof(T) : -1, 0, B);
-      c[k] = buffer_raw(rc, ok ? (t * (int)Cs + i) * (int)sizeof(T) : -1, 0, C);
+      b[k] = buffer_raw<T, 1>(rb, ok ? (t * (int)Bs + i) * (int)sizeof(T) : -1, 0);
+      c[k] = buffer_raw<T, 1>(rc, ok ? (t * (int)Cs + i) * (int)sizeof(T) : -1, 0);
     }
   }
   __device__ __forceinline__ void put(float (*area)[2 * NS]) const {
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      area[t0 + k * kStep][i] = widen(b[k]);
-      area[t0 + k * kStep][NS + i] = widen(c[k]);
+      area[t0 + k * kStep][i] = widen<T, 1>(b[k], 0);
+      area[t0 + k * kStep][NS + i] = widen<T, 1>(c[k], 0);
     }
   }
 };
@@ -541,8 +596,8 @@ __device__ __forceinline__ float lane_segment(const SsmArgs &a, LaneBc<NS> &lds,
       float xk[U], d[U], gate[U], acc[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        xk[k] = widen(xr[k]);
-        d[k] = widen(dr[k]) + bias;
+        xk[k] = widen<T, 1>(xr[k], 0);
+        d[k] = widen<T, 1>(dr[k], 0) + bias;
         gate[k] = 1.f;
       }
       if (a.softplus) {
@@ -553,7 +608,7 @@ __device__ __forceinline__ float lane_segment(const SsmArgs &a, LaneBc<NS> &lds,
       if (FULL && z) {
 #pragma unroll
         for (int k = 0; k < U; ++k)
-          gate[k] = silu(widen(zr[k]));
+          gate[k] = silu(widen<T, 1>(zr[k], 0));
       }
       // past the segment's end a step of 0 (with x and B 0) leaves h as it is
       if (ntok - t0 < U) {
@@ -928,13 +983,15 @@ template <typename F> hipError_t with_lane(int NS, F &&f) {
   return f(integral_constant<int, 16>());
 }
 
-template <typename F> hipError_t with_row(int E, F &&f) {
+template <typename F> hipError_t with_row(int E, bool pairs, F &&f) {
   using std::integral_constant;
+  using one = integral_constant<int, 1>;
+  using two = integral_constant<int, 2>;
   switch (E) {
-  case 1: return f(integral_constant<int, 1>());
-  case 2: return f(integral_constant<int, 2>());
-  case 4: return f(integral_constant<int, 4>());
-  default: return f(integral_constant<int, 8>());
+  case 1: return pairs ? f(one(), two()) : f(one(), one());
+  case 2: return pairs ? f(two(), two()) : f(two(), one());
+  case 4: return f(integral_constant<int, 4>(), one());
+  default: return f(integral_constant<int, 8>(), one());
   }
 }
 
@@ -1061,6 +1118,15 @@ hipError_t launch_ssm(int elt, const SsmCall &c, int32_t num_seqs, const int64_t
   if (e != hipSuccess)
     return e;
 
+  // the row kernel stages two neighbouring elements at a time where every
+  // pair is one aligned load (8192 x 8192 bf16: 391 us against 415)
+  const auto paired = [elt](const void *p, int64_t stride) {
+    return ((uintptr_t)p & (elt == 1 ? 3u : 7u)) == 0 && stride % 2 == 0;
+  };
+  const bool pairs = a.Dg % 2 == 0 && c.N % 2 == 0 && paired(c.x, c.x_stride) &&
+                     paired(c.delta, c.delta_stride) && paired(c.z, c.z ? c.z_stride : 0) &&
+                     paired(c.y, c.y_stride) && paired(c.B, c.B_stride) && paired(c.C, c.C_stride);
+
   const auto typed = [&](auto tag) {
     using T = decltype(tag);
     const T *x = (const T *)c.x, *dl = (const T *)c.delta, *z = (const T *)c.z;
@@ -1080,9 +1146,9 @@ hipError_t launch_ssm(int elt, const SsmCall &c, int32_t num_seqs, const int64_t
           ssm_lane_kernel<T, decltype(ns)::value><<<n, 256, 0, s>>>(tab, a, pass, x, dl, z, B, C, y);
         });
       });
-    return with_row(plan.states, [&](auto e) {
+    return with_row(plan.states, pairs, [&](auto e, auto p2) {
       return passes([&](int pass, unsigned n) {
-        ssm_row_kernel<T, decltype(e)::value>
+        ssm_row_kernel<T, decltype(e)::value, decltype(p2)::value>
             <<<n, 256, 0, s>>>(tab, a, pass, total[pass] * per, x, dl, z, B, C, y);
       });
     });
