@@ -162,16 +162,17 @@ def load():
         lib.kda_short_conv_workspace_size.restype = sz
         lib.kda_short_conv_workspace_size.argtypes = [i32]
         lib.kda_short_conv.restype = i32
-        lib.kda_short_conv.argtypes = [i32, lp, i32, i32, i32, vp, i64, vp, vp, i32, vp, vp, vp,
+        # (host bounds as a plain address: cheaper to pass than a pointer object)
+        lib.kda_short_conv.argtypes = [i32, vp, i32, i32, i32, vp, i64, vp, vp, i32, vp, vp, vp,
                                        i32, vp, i64, vp, sz, vp]
         lib.kda_short_conv_step.restype = i32
         lib.kda_short_conv_step.argtypes = [i32, i32, i32, i32, vp, i64, vp, vp, i32, vp, vp,
                                             i32, vp, i64, vp]
         sp = ctypes.POINTER(SsmIo)
         lib.kda_selective_scan_workspace_size.restype = sz
-        lib.kda_selective_scan_workspace_size.argtypes = [i32, lp, i32, i32, i32, i32]
+        lib.kda_selective_scan_workspace_size.argtypes = [i32, vp, i32, i32, i32, i32]
         lib.kda_selective_scan.restype = i32
-        lib.kda_selective_scan.argtypes = [i32, lp, i32, i32, i32, i32, sp, vp, vp, vp, i32, i32,
+        lib.kda_selective_scan.argtypes = [i32, vp, i32, i32, i32, i32, sp, vp, vp, vp, i32, i32,
                                            vp, sz, vp]
         lib.kda_selective_scan_step.restype = i32
         lib.kda_selective_scan_step.argtypes = [i32, i32, i32, i32, i32, sp, vp, vp, i32, vp]

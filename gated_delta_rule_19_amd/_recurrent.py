@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from ._native import (KDA_BF16, KDA_F32, KDA_OK, KdaError, SsmIo, _cu_ptr, _host_cu, load)
+from ._native import KDA_BF16, KDA_F32, KDA_OK, KdaError, SsmIo, _host_cu, load
 
 _ACTS = {None: 0, "none": 0, "silu": 1}
 _FORMATS = {torch.int8: 0, torch.float8_e4m3fn: 1}
@@ -38,12 +38,13 @@ def _rows(t, shape, dtype, name):
         raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
     if t.dtype != dtype:
         raise ValueError("%s must be %s (got %s)" % (name, dtype, t.dtype))
+    width = shape[1] if len(shape) == 2 else shape[1] * shape[2]
+    if t.is_contiguous():
+        return width
     st = t.stride()
-    width = 1
-    for n, s in zip(reversed(shape[1:]), reversed(st[1:])):
-        if s != width and n != 1:
-            raise ValueError("%s must have dense rows (strides %s)" % (name, st))
-        width *= n
+    if (shape[-1] != 1 and st[-1] != 1) or \
+            (len(shape) == 3 and shape[1] != 1 and st[1] != shape[2]):
+        raise ValueError("%s must have dense rows (strides %s)" % (name, st))
     # (a single row's stride is whatever torch left there)
     return st[0] if shape[0] > 1 else max(width, st[0])
 
@@ -161,7 +162,7 @@ def short_conv(x, weight, bias=None, cu_seqlens=None, initial_state=None,
         final_state = torch.empty((n, W - 1, D), dtype=dt, device=dev)
     lib = load()
     ws = _workspace(workspace, lib.kda_short_conv_workspace_size(n), dev)
-    _call("kda_short_conv", dev, n, _cu_ptr(cu), D, W, code, _p(x), xs, _p(weight), _p(bias), act,
+    _call("kda_short_conv", dev, n, cu.ctypes.data, D, W, code, _p(x), xs, _p(weight), _p(bias), act,
           _p(initial_state), _p(final_state), _p(slots), pool, _p(y), ys,
           _p(ws), 0 if ws is None else ws.numel())
     return y, final_state
@@ -247,7 +248,7 @@ def selective_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None,
     if final_state is None and output_final_state and slots is None:
         final_state = torch.empty((n, ch, N), dtype=torch.float32, device=dev)
     lib = load()
-    cup = _cu_ptr(cu)
+    cup = cu.ctypes.data
     split = int(split_hint)
     ws = _workspace(workspace, lib.kda_selective_scan_workspace_size(n, cup, ch, N, G, split), dev)
     _call("kda_selective_scan", dev, n, cup, ch, N, G, code, ctypes.byref(io), _p(initial_state),
