@@ -322,7 +322,7 @@ hipError_t launch_conv(int elt, const ConvCall &c, int32_t num_seqs, const int64
   const auto tiles = [](int64_t len, int w) -> int64_t {
     return w ? 0 : (len > kConvTile ? (len + kConvTile - 1) / kConvTile : 1);
   };
-  int64_t total[2];
+  int64_t total[kCounts];
   if (!seq_totals(num_seqs, cu, tiles, total))
     return hipErrorInvalidConfiguration;
   a.waves = total[0] * a.cw;

@@ -16,20 +16,22 @@
 
 namespace kda {
 
-constexpr int kInlineSeqs = 48;  // 49 entries of 24 bytes: 1176 of the 4096 argument bytes
-constexpr int kTablePart = 128;  // entries per table-writing launch (3 of the 4 KB)
+constexpr int kInlineSeqs = 48;  // 49 entries of 32 bytes: 1568 of the 4096 argument bytes
+constexpr int kTablePart = 100;  // entries per table-writing launch: 3200 bytes
+constexpr int kCounts = 3;
 
 // One sequence: its first token, length and number, and the blocks of the
-// entries before it in each of a call's (at most two) launches.  The entry
+// entries before it in each of a call's (at most three) launches.  The entry
 // past the last holds the totals.  Inline tables put the longest sequences
 // first, so that the longest serial work starts first and the short ones
 // fill in behind it; longer tables keep the sequences' order.
 struct SeqEntry {
   int64_t tok0;
   int32_t len, seq;
-  int32_t blk[2];
+  int32_t blk[kCounts];
+  int32_t pad;
 };
-static_assert(sizeof(SeqEntry) == 24, "SeqEntry layout");
+static_assert(sizeof(SeqEntry) == 32, "SeqEntry layout");
 
 struct SeqTable {
   const SeqEntry *ws; // null: the entries are `in`
@@ -51,15 +53,16 @@ inline size_t seq_table_bytes(int32_t num_seqs) {
 // Fills `t` from the host bounds and the tiles of each sequence
 // (tiles(n, length, which) blocks in launch `which`), and for long tables
 // enqueues the launches that write it to `ws` (seq_table_bytes of it).  The
-// totals come back in total[2]; false when one passes 2^31 - 1.
+// totals come back in total; false when one passes 2^31 - 1.
 hipError_t launch_table_part(const TablePart &part, int count, SeqEntry *dst, hipStream_t s);
 
 // (the closing-entry totals of a table that is only counted, not written)
 template <typename F>
-bool seq_totals(int32_t num_seqs, const int64_t *cu, F &&tiles, int64_t total[2]) {
-  total[0] = total[1] = 0;
+bool seq_totals(int32_t num_seqs, const int64_t *cu, F &&tiles, int64_t (&total)[kCounts]) {
+  for (int w = 0; w < kCounts; ++w)
+    total[w] = 0;
   for (int32_t n = 0; n < num_seqs; ++n)
-    for (int w = 0; w < 2; ++w) {
+    for (int w = 0; w < kCounts; ++w) {
       total[w] += tiles(cu[n + 1] - cu[n], w);
       if (total[w] > INT32_MAX)
         return false;
@@ -82,7 +85,7 @@ hipError_t make_seq_table(SeqTable &t, int32_t num_seqs, const int64_t *cu, F &&
         order[i] = order[i - 1];
       order[i] = n;
     }
-  int64_t at[2] = {0, 0};
+  int64_t at[kCounts] = {};
   TablePart part;
   for (int32_t i = 0; i <= num_seqs; ++i) {
     SeqEntry &e = t.ws ? part.e[i % kTablePart] : t.in[i];
@@ -90,7 +93,8 @@ hipError_t make_seq_table(SeqTable &t, int32_t num_seqs, const int64_t *cu, F &&
     e.tok0 = cu[n];
     e.seq = n;
     e.len = i < num_seqs ? (int32_t)(cu[n + 1] - cu[n]) : 0;
-    for (int w = 0; w < 2; ++w) {
+    e.pad = 0;
+    for (int w = 0; w < kCounts; ++w) {
       e.blk[w] = (int32_t)at[w];
       at[w] += i < num_seqs ? tiles(cu[n + 1] - cu[n], w) : 0;
     }

@@ -5,28 +5,31 @@
 //   h[d, n] <- exp(delta A[d, n]) h[d, n] + delta x[d] B[n]
 //   y[d]    = sum_n C[n] h[d, n] + Dskip[d] x[d],   then y *= silu(z)
 //
-// Bound.  Per (token, channel) four elements move, but N states each take a
-// product, an exponential and three more products and sums: with N = 16 the
-// vector ALU is the limit, not HBM, and the kernel is built to issue nothing
-// per state but those five instructions.
-//   - A lane owns one channel, so delta, delta x, x, z and y need no
-//     broadcast, and B and C are the same for the whole wave: they come as
-//     scalar loads from an fp32 table that bc_kernel lays out first (per
-//     wave: consecutive tokens, its states' B then C) and enter the products
-//     as scalar operands.
-//   - The states of a channel are dealt to the S waves of a workgroup, NS
-//     each, in registers.  The waves share delta and delta x through LDS (one
-//     of them evaluates the softplus of a token) and leave their partial
-//     sums of y there, which one wave per token then adds up.
+// Bound.  Per (token, channel) four elements move, but each of the N states
+// takes two products, an exponential and two more products and sums: 24
+// cycles of a SIMD for 64 of them (the exponential 8, the others 4 each; no
+// fp32 pairs are used).  With N = 16 the vector ALU is the limit, not HBM:
+// 8192 tokens x 8192 channels are 164 us of those instructions alone,
+// against 88 us of traffic.  All arithmetic is fp32; y is the only rounding
+// to fewer bits.
 //
-// Few chains.  The recurrence is serial in the tokens.  When the sequences'
-// channels do not fill the chip, a sequence is cut into segments: the decay
-// over a segment is exp(A sum(delta)), so a segment's effect on the state
-// that enters it is known from its end state from zero and its sum of delta.
-// The first launch runs every first segment (from the true initial state)
-// beside the end states of the middle ones; the second runs all others, each
-// folding the pairs before it into its entry state.  The middle segments'
-// exponentials are evaluated twice, which is what the cut costs.
+// The recurrence is serial in the tokens, so what fills the chip are channels
+// and states, and when those do not suffice, pieces of the sequence.  Two
+// kernels, chosen by ssm_plan from the times of both:
+//   row kernel   a channel's states across 16 lanes: 16 times the waves of
+//                the other, for one reduction across lanes a token (some 43
+//                cycles a state and token in all);
+//   lane kernel  all states of a channel in one lane (some 34 cycles), where
+//                there are sequences and channels enough, and for long
+//                sequences cut into segments.
+// The cut: the decay over a segment is exp(A sum(delta)), so a segment's
+// effect on the state that enters it is known from its end state from zero
+// and its sum of delta.  The first launch runs every first segment (from the
+// true initial state) beside the end states of the middle ones (some 25
+// cycles: no read-out), a second folds those pairs into entry states, the
+// third runs all segments but the first.  The middle segments' exponentials
+// are evaluated twice, which is what the cut costs: 131072 tokens x 1536
+// channels take 1.33 ms (65 cycles a state and token), 4.5 ms uncut.
 #include "kda_device.h"
 #include "kda_recurrent.h"
 #include "kda_seqtab.h"
@@ -133,6 +136,15 @@ __device__ __forceinline__ void buffer_put(__amdgpu_buffer_rsrc_t r, const float
 // cost.  The read-out leaves 16 partial products a lane, one for each token,
 // and row_reduce16 adds them across the row so that token i's sum ends in
 // lane i: 33 instructions for 16 tokens instead of 64.
+//
+// A workgroup's four waves stage tiles of TT tokens for their 16 channels
+// through LDS, because a wave's own loads would be 16 rows of 8 bytes (620 us
+// instead of 415 at 8192 x 8192 bf16): the threads go down the channels of a
+// row, evaluate softplus and gate there, and take the read-outs back the same
+// way for skip, gate and store.  391 us at that size, with two waves a SIMD:
+// 9.5 instructions a state and token, the vector ALU busy 70% of the time.
+// Tiles of 32 and 128 tokens: 417 and 406 us; eight waves (32 channels): 388;
+// one barrier a tile with both buffers doubled: 430.
 
 // Token I's value of every row, in all of the row's lanes.
 template <int I> __device__ __forceinline__ float row_bcast(float x) {
@@ -499,7 +511,12 @@ __global__ __launch_bounds__(256) void ssm_row_kernel(SeqTable tab, SsmArgs a, i
 // No exchange between waves and no barrier: a wave streams its 64 channels'
 // tokens, U at a time with the next U tokens' inputs in flight.  B and C come
 // through an LDS area of the wave's own: kBcTokens tokens' values, widened,
-// loaded a whole area ahead; every lane then reads the same 16 bytes.
+// loaded a whole area ahead; every lane then reads the same 16 bytes.  (As
+// scalar operands from a table of scalar loads they saved the LDS reads, but
+// a wave then stood still for every miss: 567 us against 467 at 8192 x 8192,
+// 138 against 67 us at 256 x 1536.)  131072 x 1536 bf16, cut into 171
+// segments: 1.33 ms, 65 cycles a state and token where the instructions of
+// both passes come to 59.
 constexpr int kBcTokens = 16;
 
 template <int NS> struct LaneBc {
@@ -745,21 +762,23 @@ __global__ __launch_bounds__(256, 4) void ssm_lane_kernel(SeqTable tab, SsmArgs 
 // pend[j] + exp(A sum_j) pend[j - 1], the state after segment j.  One wave per
 // (cut sequence, 64 channels, state); the pairs of 16 segments are in flight
 // together.
-__global__ __launch_bounds__(256) void ssm_fold_kernel(SeqTable tab, SsmArgs a, int SN) {
+__global__ __launch_bounds__(256) void ssm_fold_kernel(SeqTable tab, SsmArgs a, int SN,
+                                                       int64_t folds) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int blocks = a.G * a.cb;
   const int64_t wv = (int64_t)blockIdx.x * 4 + wave;
-  const int n = (int)(wv / ((int64_t)blocks * SN));
-  if (n >= tab.num_seqs)
+  const int64_t f = wv / ((int64_t)blocks * SN);
+  if (f >= folds)
     return;
-  const int rest = (int)(wv - (int64_t)n * blocks * SN);
+  const int rest = (int)(wv - f * blocks * SN);
   const int gc = rest / SN, i = rest - gc * SN;
+  if (i >= a.N)
+    return;
   const SeqView seqs(tab);
+  const int n = seqs.find((int)f, 2);
   const int64_t pair0 = seqs.blk(n, 1);
   const int pairs = (int)(seqs.blk(n + 1, 1) - pair0);
-  if (pairs <= 1 || i >= a.N)
-    return;
   const int g = gc / a.cb, dg = (gc - g * a.cb) * 64 + lane;
   const float A2 = dg < a.Dg ? a.A[((int64_t)g * a.Dg + dg) * a.N + i] * kLog2e : 0.f;
   float *pe = a.pend + ((pair0 * blocks + gc) * SN + i) * 64 + lane;
@@ -1093,11 +1112,12 @@ hipError_t launch_ssm(int elt, const SsmCall &c, int32_t num_seqs, const int64_t
   a.pend = (float *)(w + plan.off_end);
   a.psum = (float *)(w + plan.off_sum);
 
-  const auto tiles = [&](int64_t len, int pass) -> int64_t {
+  // segments in each pass, and (2) whether there are pairs to fold
+  const auto tiles = [&](int64_t len, int w) -> int64_t {
     const int64_t nseg = ssm_num_segments(len, plan);
-    return pass ? nseg - 1 : std::max<int64_t>(1, nseg - 1);
+    return w == 0 ? std::max<int64_t>(1, nseg - 1) : (w == 1 ? nseg - 1 : nseg > 2);
   };
-  int64_t total[2];
+  int64_t total[kCounts];
   if (!seq_totals(num_seqs, cu, tiles, total))
     return hipErrorInvalidConfiguration;
   // workgroups per (segment, all channels); the row kernel's grid is rounded
@@ -1110,7 +1130,7 @@ hipError_t launch_ssm(int elt, const SsmCall &c, int32_t num_seqs, const int64_t
     if (grid[pass] * 256 > UINT32_MAX)
       return hipErrorInvalidConfiguration;
   }
-  const int64_t fold = plan.pairs > 0 ? ((int64_t)num_seqs * blocks * SN + 3) / 4 : 0;
+  const int64_t fold = (total[2] * blocks * SN + 3) / 4;
   if (fold * 256 > UINT32_MAX)
     return hipErrorInvalidConfiguration;
   SeqTable tab;
@@ -1134,10 +1154,10 @@ hipError_t launch_ssm(int elt, const SsmCall &c, int32_t num_seqs, const int64_t
     T *y = (T *)c.y;
     const auto passes = [&](auto &&run) {
       run(0, (unsigned)grid[0]);
-      if (total[1] > 0) {
-        ssm_fold_kernel<<<(unsigned)fold, 256, 0, s>>>(tab, a, SN);
+      if (fold > 0)
+        ssm_fold_kernel<<<(unsigned)fold, 256, 0, s>>>(tab, a, SN, total[2]);
+      if (total[1] > 0)
         run(1, (unsigned)grid[1]);
-      }
       return hipGetLastError();
     };
     if (plan.lane)

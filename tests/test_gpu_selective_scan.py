@@ -327,3 +327,11 @@ def test_automatic_choice_at_its_edges(name, lengths, D, N, G):
     for dtype in (F32, BF16):
         c = case(lengths, D, N, G, dtype, 180)
         compare(c, *run(c))
+
+
+@pytest.mark.parametrize("N", [16, 20])
+def test_many_cut_sequences(N):
+    """More sequences than the inline table, several of them cut, others not."""
+    print("scan many cut sequences", N, flush=True)
+    c = case([(i * 53) % 300 for i in range(60)], 66, N, 1, F32, 190)
+    compare(c, *run(c, split_hint=6))

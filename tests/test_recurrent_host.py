@@ -77,7 +77,7 @@ def test_short_conv_of_no_sequences_is_a_no_op(lib):
 def test_short_conv_workspace(lib):
     assert lib.kda_short_conv_workspace_size(0) == 0
     assert lib.kda_short_conv_workspace_size(48) == 0
-    assert lib.kda_short_conv_workspace_size(49) >= 50 * 24
+    assert lib.kda_short_conv_workspace_size(49) >= 50 * 32
     assert lib.kda_short_conv_workspace_size(-1) == 0
 
 
