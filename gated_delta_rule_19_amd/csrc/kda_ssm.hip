@@ -1020,17 +1020,20 @@ int64_t ssm_num_segments(int64_t len, const SsmPlan &p) {
   return len > p.seg ? (len + p.seg - 1) / p.seg : 1;
 }
 
-// Which kernel, and the cut.  Times in us from runs over D = 1536 .. 12288,
-// 1 .. 64 sequences and 1024 .. 16384 tokens, N = 16 (measured / chosen over):
+// Which kernel, and the cut.  Times in us, fitted to runs over D = 1536 ..
+// 12288, 1 .. 128 sequences and 1024 .. 32768 tokens with N = 16:
 //   row kernel, uncut: 36 ns a token of the longest sequence where its waves
 //     have a SIMD each to themselves; a wave more on the SIMD adds 16.5 ns.
 //     A sequence costs some 80 tokens to begin (tiles of 64).
-//   lane kernel, uncut: 0.25 ns per token and 64 channels at full occupancy,
-//     0.45 us a token of the longest sequence for a wave alone.
-//   lane kernel, cut into segments for four waves a SIMD: 0.43 ns per token
-//     and 64 channels (the middle segments run twice) plus 55 us.
-// 8192 tokens x 8192 channels: row 419, lane cut 463.  131072 x 1536: row
-// 4700, lane cut 1331.  64 sequences of 16 tokens x 8192: row 189, lane 110.
+//   lane kernel, uncut: 0.24 ns per token and 64 channels at full occupancy
+//     (a sequence costs some 24 tokens to begin), 0.4 us a token of the
+//     longest sequence for a wave alone.
+//   lane kernel, cut into segments for four waves a SIMD: two such runs, the
+//     middle segments' first one at 0.18 ns per token and 64 channels, and
+//     25 us for the launches between.
+// Both sides: 8192 tokens x 8192 channels: row 391, lane cut 463.  131072 x
+// 1536: row 4500, lane cut 1330.  64 sequences of 16 tokens x 8192: row 189,
+// lane 81.  128 sequences of 64 x 12288: row 742, lane 513.
 SsmPlan ssm_plan(int32_t num_seqs, const int64_t *cu, int32_t D, int32_t N, int32_t G,
                  int32_t split_hint) {
   SsmPlan p{};
@@ -1043,21 +1046,34 @@ SsmPlan ssm_plan(int32_t num_seqs, const int64_t *cu, int32_t D, int32_t N, int3
   p.seg = whole(longest);
   const int NS = lane_states(N), E = row_states(N);
   const double T = (double)tokens, L = (double)longest, W = (double)blocks, n = num_seqs;
-  // (states beside 16: the states' share of each kernel's instructions)
-  const double row_scale = (33. * E + 15.) / 48., full = (24. * NS + 150.) / 534. * 0.25e-3,
+  // (the states' share of each kernel's instructions, beside N = 16)
+  const double row_scale = (33. * E + 15.) / 48., full = (24. * NS + 150.) / 534. * 0.24e-3,
                half = (20. * NS + 90.) / 410. * 0.18e-3;
   const double per_simd = W * 16. / 1024.; // row waves a SIMD, one sequence
   const double row = row_scale * std::max(0.036 * L, 0.020 * L + 0.0165 * per_simd * (T + 80. * n));
-  const double lane = 0.45 * L * NS / 16. + W * (T + 24. * n) * full;
+  const auto lane_time = [&](double longest_run, double work) {
+    const double alone = 0.40 * longest_run * NS / 16.;
+    return std::max(alone, work) + 0.15 * std::min(alone, work);
+  };
+  const double lane = lane_time(L, W * (T + 24. * n) * full);
   const int64_t lane_seg = std::max<int64_t>(64, whole(tokens * blocks / 4096));
-  const double cut = 55. + W * T * (full + half);
+  int64_t first = 0, middle = 0; // tokens of first and of middle segments
+  for (int32_t i = 0; i < num_seqs; ++i) {
+    const int64_t len = cu[i + 1] - cu[i];
+    first += std::min(len, lane_seg);
+    middle += std::max<int64_t>(0, len - 2 * lane_seg);
+  }
+  const double cut = 25. +
+                     lane_time((double)lane_seg, W * (((double)first + 24. * n) * full +
+                                                      (double)middle * half)) +
+                     lane_time((double)lane_seg, W * (T - (double)first) * full);
   p.lane = false;
   if (split_hint > 1) {
     p.lane = N <= kLaneMaxStates;
     p.seg = whole((longest + split_hint - 1) / split_hint);
   } else if (N <= kLaneMaxStates) {
     p.lane = lane < row;
-    if (split_hint == 0 && cut < std::min(lane, row) && lane_seg * 3 <= longest) {
+    if (split_hint == 0 && cut < 0.85 * std::min(lane, row) && lane_seg * 3 <= longest) {
       p.lane = true;
       p.seg = lane_seg;
     }
