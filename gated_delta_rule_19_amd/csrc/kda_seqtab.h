@@ -16,7 +16,7 @@
 
 namespace kda {
 
-constexpr int kInlineSeqs = 48;  // 49 entries of 32 bytes: 1568 of the 4096 argument bytes
+constexpr int kInlineSeqs = 64;  // 65 entries of 32 bytes: 2080 of the 4096 argument bytes
 constexpr int kTablePart = 100;  // entries per table-writing launch: 3200 bytes
 constexpr int kCounts = 3;
 

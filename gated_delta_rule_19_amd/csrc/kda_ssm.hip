@@ -66,6 +66,14 @@ __device__ __forceinline__ float silu(float x) {
   return x * __builtin_amdgcn_rcpf(1.f + exp2_hw(-x * kLog2e));
 }
 
+// A in log2 units.  An infinite A is taken as the largest finite one: its
+// decay is the same, and a step of 0 (which the kernels take past a segment's
+// end) leaves the state as it is instead of making 0 * inf.
+__device__ __forceinline__ float log2_rate(float a) {
+  const float r = a * kLog2e;
+  return fabsf(r) == __builtin_inff() ? copysignf(3.4028235e38f, r) : r;
+}
+
 struct SsmArgs {
   int32_t D, N, G, softplus, num_slots;
   int32_t Dg;      // channels per group
@@ -442,7 +450,7 @@ __global__ __launch_bounds__(256) void ssm_row_kernel(SeqTable tab, SsmArgs a, i
   float A2[E], h[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    A2[e] = in && 16 * e + ri < a.N ? a.A[d * a.N + 16 * e + ri] * kLog2e : 0.f;
+    A2[e] = in && 16 * e + ri < a.N ? log2_rate(a.A[d * a.N + 16 * e + ri]) : 0.f;
     h[e] = 0.f;
   }
   int64_t slot = seqs.seq(n);
@@ -698,7 +706,7 @@ __global__ __launch_bounds__(256, 4) void ssm_lane_kernel(SeqTable tab, SsmArgs 
   float A2[NS], h[NS];
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
-    A2[i] = in && i < a.N ? a.A[d * a.N + i] * kLog2e : 0.f;
+    A2[i] = in && i < a.N ? log2_rate(a.A[d * a.N + i]) : 0.f;
     h[i] = 0.f;
   }
   int64_t slot = seqs.seq(n);
@@ -780,7 +788,7 @@ __global__ __launch_bounds__(256) void ssm_fold_kernel(SeqTable tab, SsmArgs a, 
   const int64_t pair0 = seqs.blk(n, 1);
   const int pairs = (int)(seqs.blk(n + 1, 1) - pair0);
   const int g = gc / a.cb, dg = (gc - g * a.cb) * 64 + lane;
-  const float A2 = dg < a.Dg ? a.A[((int64_t)g * a.Dg + dg) * a.N + i] * kLog2e : 0.f;
+  const float A2 = dg < a.Dg ? log2_rate(a.A[((int64_t)g * a.Dg + dg) * a.N + i]) : 0.f;
   float *pe = a.pend + ((pair0 * blocks + gc) * SN + i) * 64 + lane;
   const float *ps = a.psum + (pair0 * blocks + gc) * 64 + lane;
   const int64_t pstep = (int64_t)blocks * SN * 64, sstep = (int64_t)blocks * 64;

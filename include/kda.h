@@ -521,7 +521,7 @@ kda_status kda_segment_scan(int32_t num_segs, int32_t H, int32_t dk, int32_t dv,
  *                     (with rows of its initial state in front when it is
  *                     shorter), copied without rounding.  final_state ==
  *                     initial_state is allowed; other overlaps are not.
- *   workspace       : DEVICE, of the queried size (0 up to 48 sequences:
+ *   workspace       : DEVICE, of the queried size (0 up to 64 sequences:
  *                     then it may be NULL), 256-byte aligned.
  * The sums are fp32; y is rounded once.
  */
@@ -565,7 +565,9 @@ kda_status kda_short_conv_step(int32_t N, int32_t D, int32_t W, kda_dtype dt, co
  *                alone leave the device idle; 1: never; n > 1: about n
  *                segments for the longest sequence, others in segments of
  *                that length.  The result is the same up to fp32 rounding.
- *   workspace  : DEVICE, of the queried size, 256-byte aligned.
+ *   workspace  : DEVICE, of the queried size, 256-byte aligned (the query
+ *                answers 0 where none is needed, and for a call that will be
+ *                refused: then it may be NULL).
  * States, decays and sums are fp32; y is rounded once.
  */
 #define KDA_SSM_MAX_STATES 128

@@ -173,7 +173,7 @@ def test_kda_layer_with_convolutions_and_parked_states(kind, step):
     assert np.max(np.abs(ref.f64(state) - s_ref)) <= 1e-4 * np.max(np.abs(s_ref))
 
 
-@pytest.mark.parametrize("nseq", [3, 60, 200])
+@pytest.mark.parametrize("nseq", [3, 64, 200])
 def test_captured_prompts_replay_equal_eager(nseq):
     """Prompt calls in a graph, inline and workspace tables, cut sequences:
     each replay on new inputs equals the eager call, with eager calls of other
@@ -242,7 +242,7 @@ def test_two_streams_at_once():
     together, equal the calls run alone."""
     print("two streams", flush=True)
     m = Mixer(256, 16, 1, 4, BF16, 80)
-    cu = np.concatenate([[0], np.cumsum([700] * 2 + [9] * 60)])
+    cu = np.concatenate([[0], np.cumsum([700] * 2 + [9] * 70)])
     T = int(cu[-1])
     n = len(cu) - 1
     ps = [f(gen(81 + i), T, m.width).to(BF16) for i in range(2)]

@@ -63,7 +63,7 @@ def run(c, **kw):
 LENGTHS = {
     "one": [1], "two": [2], "tile": [32], "past": [33], "odd": [131], "long": [1000],
     "mixed": [0, 1, 2, 3, 0, 64, 65, 7, 200, 0], "many": [(i * 7) % 13 for i in range(120)],
-    "edge": [3] * 49, "none": [0, 0],
+    "edge": [3] * 65, "none": [0, 0],
 }
 
 
@@ -333,5 +333,66 @@ def test_automatic_choice_at_its_edges(name, lengths, D, N, G):
 def test_many_cut_sequences(N):
     """More sequences than the inline table, several of them cut, others not."""
     print("scan many cut sequences", N, flush=True)
-    c = case([(i * 53) % 300 for i in range(60)], 66, N, 1, F32, 190)
+    c = case([(i * 53) % 300 for i in range(90)], 66, N, 1, F32, 190)
     compare(c, *run(c, split_hint=6))
+
+
+@pytest.mark.parametrize("lens", [[37], [100, 3, 70]])
+@pytest.mark.parametrize("split", [1, 3])
+def test_infinite_rates_forget(lens, split):
+    """A = -inf drops the state at every token, as any very large rate does,
+    also at lengths that end inside a tile."""
+    print("scan infinite rates", lens, split, flush=True)
+    c = case(lens, 66, 16, 1, F32, 200)
+    c["A"][:, 3] = -1e30
+    c["A"][5] = -1e30
+    y, fin = run(c, split_hint=split)
+    c["A"][:, 3] = -float("inf")
+    c["A"][5] = -float("inf")
+    y2, fin2 = run(c, split_hint=split)
+    assert torch.isfinite(y).all() and torch.equal(y, y2) and torch.equal(fin, fin2)
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+def test_nonfinite_states_stay_in_their_slice(value):
+    """An infinite or NaN initial state spoils its own channel of its own
+    sequence, whose final state keeps it, and nothing else."""
+    print("scan nonfinite state", value, flush=True)
+    for split in (1, 3):
+        c = case([90, 41, 130], 66, 16, 1, F32, 210)
+        clean, cfin = run(c, split_hint=split)
+        c["s"] = c["s"].clone()
+        c["s"][1, 7, 2] = value
+        y, fin = run(c, split_hint=split)
+        hit = torch.zeros_like(y, dtype=torch.bool)
+        hit[90:131, 7] = True
+        assert torch.equal(y[~hit], clean[~hit]) and not torch.isfinite(y[hit]).any()
+        assert not torch.isfinite(fin[1, 7, 2])
+        fin[1, 7, 2] = cfin[1, 7, 2]
+        assert torch.equal(fin, cfin)
+
+
+def test_rows_past_the_last_sequence_are_left_alone():
+    """Through the C ABI: buffers longer than the packed tokens."""
+    print("scan rows past the end", flush=True)
+    import ctypes
+    from gated_delta_rule_19_amd import _native as nat
+    c = case([45, 20], 70, 16, 1, BF16, 220)
+    a = args(c)
+    want, _ = run(c, split_hint=1)
+    y = torch.full((80, 70), 7.0, dtype=BF16, device=DEV)
+    io = nat.SsmIo()
+    for k, t, w in (("x", a["x"], 70), ("delta", a["delta"], 70), ("z", a["z"], 70), ("y", y, 70),
+                    ("B", a["B"], 16), ("C", a["C"], 16)):
+        setattr(io, k, t.data_ptr())
+        setattr(io, k + "_stride", w)
+    io.A, io.D_skip, io.delta_bias = (a[k].data_ptr() for k in ("A", "D", "delta_bias"))
+    io.delta_softplus = 1
+    cu = np.ascontiguousarray(c["cu"])
+    s = on(c["s"])
+    st = nat.load().kda_selective_scan(2, cu.ctypes.data, 70, 16, 1, nat.KDA_BF16, ctypes.byref(io),
+                                       s.data_ptr(), None, None, 2, 1, None, 0,
+                                       torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == nat.KDA_OK
+    assert torch.equal(y[:65], want) and (y[65:] == 7).all()

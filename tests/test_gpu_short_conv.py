@@ -44,7 +44,7 @@ LENGTHS = {
     "one": [1], "short": [2], "tile": [64], "odd": [131],
     "mixed": [0, 1, 2, 3, 0, 64, 65, 7, 200, 0],
     "many": [(i * 7) % 13 for i in range(120)],       # past the inline table
-    "table_edge": [3] * 48, "table_edge1": [3] * 49, "parts": [2] * 321,
+    "table_edge": [3] * 64, "table_edge1": [3] * 65, "parts": [2] * 321,
     "none": [0, 0],
 }
 

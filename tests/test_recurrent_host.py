@@ -62,9 +62,9 @@ def conv(lib, cu=(0, 5), D=64, W=4, dt=BF16, x=PTR, xs=64, w=PTR + (1 << 20), b=
     (INVALID, dict(slots=PTR + 2)),
     (INVALID, dict(cu=(0, 2, 5), fin=PTR + (1 << 28), num_slots=1)),
     (INVALID, dict(init=PTR + (1 << 28), fin=PTR + (1 << 28) + 16)),
-    (WORKSPACE, dict(cu=tuple(range(60)))),
-    (WORKSPACE, dict(cu=tuple(range(60)), ws=PTR, wsb=64)),
-    (INVALID, dict(cu=tuple(range(60)), ws=PTR + 16, wsb=1 << 20)),
+    (WORKSPACE, dict(cu=tuple(range(80)))),
+    (WORKSPACE, dict(cu=tuple(range(80)), ws=PTR, wsb=64)),
+    (INVALID, dict(cu=tuple(range(80)), ws=PTR + 16, wsb=1 << 20)),
 ])
 def test_short_conv_refuses(lib, status, kw):
     assert conv(lib, **kw) == status
@@ -76,8 +76,8 @@ def test_short_conv_of_no_sequences_is_a_no_op(lib):
 
 def test_short_conv_workspace(lib):
     assert lib.kda_short_conv_workspace_size(0) == 0
-    assert lib.kda_short_conv_workspace_size(48) == 0
-    assert lib.kda_short_conv_workspace_size(49) >= 50 * 32
+    assert lib.kda_short_conv_workspace_size(64) == 0
+    assert lib.kda_short_conv_workspace_size(65) >= 66 * 32
     assert lib.kda_short_conv_workspace_size(-1) == 0
 
 
