@@ -60,18 +60,23 @@ def _dense(t, shape, dtype, name):
         raise ValueError("%s must be contiguous" % name)
 
 
-def _device(*ts):
-    dev = None
+def _device(first, *ts):
+    """The device of all tensors (None among `ts` left out)."""
+    at = first.get_device()
+    if at < 0:
+        raise ValueError("KDA tensors must live on a HIP device")
     for t in ts:
-        if t is None:
-            continue
-        if dev is None:
-            dev = t.device
-            if dev.type != "cuda":
+        if t is not None and t.get_device() != at:
+            if t.get_device() < 0:
                 raise ValueError("KDA tensors must live on a HIP device")
-        elif t.device != dev:
             raise ValueError("all KDA tensors must be on one device")
-    return dev
+    return first.device
+
+
+def _like(x):
+    """A dense output of x's shape, type and device."""
+    return torch.empty_like(x) if x.is_contiguous() else \
+        torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
 def _p(t):
@@ -157,7 +162,7 @@ def short_conv(x, weight, bias=None, cu_seqlens=None, initial_state=None,
     ys = D if y is None else _rows(y, (T, D), dt, "y")
     dev = _device(x, weight, bias, initial_state, final_state, slots, y, workspace)
     if y is None:
-        y = torch.empty((T, D), dtype=dt, device=dev)
+        y = _like(x)
     if final_state is None and output_final_state and slots is None:
         final_state = torch.empty((n, W - 1, D), dtype=dt, device=dev)
     lib = load()
@@ -187,7 +192,7 @@ def short_conv_step(state, x, weight, bias=None, activation="silu", slots=None, 
     ys = D if y is None else _rows(y, (N, D), dt, "y")
     dev = _device(x, weight, bias, state, slots, y)
     if y is None:
-        y = torch.empty((N, D), dtype=dt, device=dev)
+        y = _like(x)
     _call("kda_short_conv_step", dev, N, D, W, code, _p(x), xs, _p(weight), _p(bias), act,
           _p(state), _p(slots), pool, _p(y), ys)
     return y
@@ -243,7 +248,7 @@ def selective_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None,
     dev = _device(x, delta, A, B, C, D, z, delta_bias, initial_state, final_state, slots, y,
                   workspace)
     if y is None:
-        y = torch.empty((T, ch), dtype=x.dtype, device=dev)
+        y = _like(x)
     io.y = _p(y)
     if final_state is None and output_final_state and slots is None:
         final_state = torch.empty((n, ch, N), dtype=torch.float32, device=dev)
@@ -270,7 +275,7 @@ def selective_scan_step(state, x, delta, A, B, C, D=None, z=None, delta_bias=Non
     _dense(state, (pool, ch, N), torch.float32, "state")
     dev = _device(x, delta, A, B, C, D, z, delta_bias, state, slots, y)
     if y is None:
-        y = torch.empty((rows, ch), dtype=x.dtype, device=dev)
+        y = _like(x)
     io.y = _p(y)
     _call("kda_selective_scan_step", dev, rows, ch, N, G, code, ctypes.byref(io), _p(state),
           _p(slots), pool)
