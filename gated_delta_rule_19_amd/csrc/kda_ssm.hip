@@ -20,8 +20,8 @@
 //                the other, for one reduction across lanes a token (some 43
 //                cycles a state and token in all);
 //   lane kernel  all states of a channel in one lane (some 34 cycles), where
-//                there are sequences and channels enough, and for long
-//                sequences cut into segments.
+//                there are sequences and channels enough.
+// Either runs long sequences of few channels cut into segments.
 // The cut: the decay over a segment is exp(A sum(delta)), so a segment's
 // effect on the state that enters it is known from its end state from zero
 // and its sum of delta.  The first launch runs every first segment (from the
@@ -29,7 +29,7 @@
 // cycles: no read-out), a second folds those pairs into entry states, the
 // third runs all segments but the first.  The middle segments' exponentials
 // are evaluated twice, which is what the cut costs: 131072 tokens x 1536
-// channels take 1.33 ms (65 cycles a state and token), 4.5 ms uncut.
+// channels take 1.32 ms (65 cycles a state and token), 4.5 ms uncut.
 #include "kda_device.h"
 #include "kda_recurrent.h"
 #include "kda_seqtab.h"
@@ -523,7 +523,7 @@ __global__ __launch_bounds__(256) void ssm_row_kernel(SeqTable tab, SsmArgs a, i
 // scalar operands from a table of scalar loads they saved the LDS reads, but
 // a wave then stood still for every miss: 567 us against 467 at 8192 x 8192,
 // 138 against 67 us at 256 x 1536.)  131072 x 1536 bf16, cut into 171
-// segments: 1.33 ms, 65 cycles a state and token where the instructions of
+// segments: 1.32 ms, 65 cycles a state and token where the instructions of
 // both passes come to 59.
 constexpr int kBcTokens = 16;
 
@@ -767,24 +767,26 @@ __global__ __launch_bounds__(256, 4) void ssm_lane_kernel(SeqTable tab, SsmArgs 
 
 // ---- the segments' entry states -------------------------------------------------------
 // pend[0] is the state after the first segment; pend[j] becomes
-// pend[j] + exp(A sum_j) pend[j - 1], the state after segment j.  One wave per
-// (cut sequence, 64 channels, state); the pairs of 16 segments are in flight
-// together.
-__global__ __launch_bounds__(256) void ssm_fold_kernel(SeqTable tab, SsmArgs a, int SN,
-                                                       int64_t folds) {
+// pend[j] + exp(A sum_j) pend[j - 1], the state after segment j.  A workgroup
+// folds one state of 64 channels: its waves take a run of the pairs each,
+// first from zero; the runs' ends and sums of delta (again a pair each) give
+// every run its entry state, from which it is folded once more and written.
+// (One wave over all pairs took 45 us for 490 of them, the loads of 16 in
+// flight at a time.)
+constexpr int kFoldWaves = 8;
+
+__global__ __launch_bounds__(64 * kFoldWaves) void ssm_fold_kernel(SeqTable tab, SsmArgs a,
+                                                                   int SN) {
+  __shared__ float s_end[kFoldWaves][64], s_sum[kFoldWaves][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int blocks = a.G * a.cb;
-  const int64_t wv = (int64_t)blockIdx.x * 4 + wave;
-  const int64_t f = wv / ((int64_t)blocks * SN);
-  if (f >= folds)
-    return;
-  const int rest = (int)(wv - f * blocks * SN);
+  const int blocks = a.G * a.cb, per = blocks * SN;
+  const int f = blockIdx.x / per, rest = blockIdx.x - f * per;
   const int gc = rest / SN, i = rest - gc * SN;
   if (i >= a.N)
     return;
   const SeqView seqs(tab);
-  const int n = seqs.find((int)f, 2);
+  const int n = seqs.find(f, 2);
   const int64_t pair0 = seqs.blk(n, 1);
   const int pairs = (int)(seqs.blk(n + 1, 1) - pair0);
   const int g = gc / a.cb, dg = (gc - g * a.cb) * 64 + lane;
@@ -792,22 +794,37 @@ __global__ __launch_bounds__(256) void ssm_fold_kernel(SeqTable tab, SsmArgs a, 
   float *pe = a.pend + ((pair0 * blocks + gc) * SN + i) * 64 + lane;
   const float *ps = a.psum + (pair0 * blocks + gc) * 64 + lane;
   const int64_t pstep = (int64_t)blocks * SN * 64, sstep = (int64_t)blocks * 64;
-  float h = pe[0];
-  for (int j = 1; j < pairs; j += 16) {
-    float e[16], sd[16];
+  const int run = (pairs - 1 + kFoldWaves - 1) / kFoldWaves;
+  const int j0 = 1 + wave * run, j1 = min(pairs, j0 + run);
+  float sum = 0.f;
+  const auto fold = [&](float h, bool write) {
+    for (int j = j0; j < j1; j += 8) {
+      float e[8], sd[8];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int q = min(j + k, pairs - 1);
-      e[k] = pe[q * pstep];
-      sd[k] = ps[q * sstep];
-    }
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-      if (j + k < pairs) {
-        h = fmaf(exp2_hw(sd[k] * A2), h, e[k]);
-        pe[(j + k) * pstep] = h;
+      for (int k = 0; k < 8; ++k) {
+        const int q = min(j + k, j1 - 1);
+        e[k] = pe[q * pstep];
+        sd[k] = ps[q * sstep];
       }
-  }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (j + k < j1) {
+          h = fmaf(exp2_hw(sd[k] * A2), h, e[k]);
+          if (write)
+            pe[(j + k) * pstep] = h;
+          else
+            sum += sd[k];
+        }
+    }
+    return h;
+  };
+  s_end[wave][lane] = fold(0.f, false);
+  s_sum[wave][lane] = sum;
+  __syncthreads();
+  float h = pe[0];
+  for (int w = 0; w < wave; ++w)
+    h = fmaf(exp2_hw(s_sum[w][lane] * A2), h, s_end[w][lane]);
+  fold(h, true);
 }
 
 // ---- single tokens ------------------------------------------------------------------
@@ -1036,12 +1053,14 @@ int64_t ssm_num_segments(int64_t len, const SsmPlan &p) {
 //   lane kernel, uncut: 0.24 ns per token and 64 channels at full occupancy
 //     (a sequence costs some 24 tokens to begin), 0.4 us a token of the
 //     longest sequence for a wave alone.
-//   lane kernel, cut into segments for four waves a SIMD: two such runs, the
-//     middle segments' first one at 0.18 ns per token and 64 channels, and
-//     25 us for the launches between.
+//   either one, cut into segments (six row waves a SIMD, four lane waves):
+//     two such runs, the middle segments' first one without read-outs (row:
+//     0.7 of a run; lane: 0.18 ns per token and 64 channels), and 15 or 25 us
+//     for the launches between.
 // Both sides: 8192 tokens x 8192 channels: row 391, lane cut 463.  131072 x
-// 1536: row 4500, lane cut 1330.  64 sequences of 16 tokens x 8192: row 189,
-// lane 81.  128 sequences of 64 x 12288: row 742, lane 513.
+// 1536: row 4500, lane cut 1320.  4096 x 1536: row 139, row cut 66, lane cut
+// 92.  64 sequences of 16 tokens x 8192: row 189, lane 81.  128 sequences of
+// 64 x 12288: row 742, lane 513.
 SsmPlan ssm_plan(int32_t num_seqs, const int64_t *cu, int32_t D, int32_t N, int32_t G,
                  int32_t split_hint) {
   SsmPlan p{};
@@ -1057,40 +1076,46 @@ SsmPlan ssm_plan(int32_t num_seqs, const int64_t *cu, int32_t D, int32_t N, int3
   // (the states' share of each kernel's instructions, beside N = 16)
   const double row_scale = (33. * E + 15.) / 48., full = (24. * NS + 150.) / 534. * 0.24e-3,
                half = (20. * NS + 90.) / 410. * 0.18e-3;
-  const double per_simd = W * 16. / 1024.; // row waves a SIMD, one sequence
-  const double row = row_scale * std::max(0.036 * L, 0.020 * L + 0.0165 * per_simd * (T + 80. * n));
+  // row waves a SIMD, one sequence
+  const double per_simd = (double)G * ((D / G + kRowChans - 1) / kRowChans) * 4. / 1024.;
+  const auto row_time = [&](double longest_run, double tokens_run) {
+    return row_scale * std::max(0.036 * longest_run,
+                                0.020 * longest_run + 0.0165 * per_simd * tokens_run);
+  };
   const auto lane_time = [&](double longest_run, double work) {
     const double alone = 0.40 * longest_run * NS / 16.;
     return std::max(alone, work) + 0.15 * std::min(alone, work);
   };
-  const double lane = lane_time(L, W * (T + 24. * n) * full);
-  const int64_t lane_seg = std::max<int64_t>(64, whole(tokens * blocks / 4096));
-  int64_t first = 0, middle = 0; // tokens of first and of middle segments
-  for (int32_t i = 0; i < num_seqs; ++i) {
-    const int64_t len = cu[i + 1] - cu[i];
-    first += std::min(len, lane_seg);
-    middle += std::max<int64_t>(0, len - 2 * lane_seg);
-  }
-  const double cut = 25. +
-                     lane_time((double)lane_seg, W * (((double)first + 24. * n) * full +
-                                                      (double)middle * half)) +
-                     lane_time((double)lane_seg, W * (T - (double)first) * full);
-  p.lane = false;
+  const bool lane_fits = N <= kLaneMaxStates;
+  const double row = row_time(L, T + 80. * n);
+  const double lane = lane_fits ? lane_time(L, W * (T + 24. * n) * full) : 1e30;
+  const double uncut = std::min(row, lane);
+  p.lane = lane < row;
   if (split_hint > 1) {
-    p.lane = N <= kLaneMaxStates;
+    p.lane = lane_fits;
     p.seg = whole((longest + split_hint - 1) / split_hint);
-  } else if (N <= kLaneMaxStates) {
-    p.lane = lane < row;
-    if (split_hint == 0 && cut < 0.85 * std::min(lane, row) && lane_seg * 3 <= longest) {
-      p.lane = true;
-      p.seg = lane_seg;
-    }
   } else if (split_hint == 0) {
-    // more states than the lane kernel holds: cut for two row waves a SIMD,
-    // where that leaves at least four segments (their middle ones run twice)
-    const int64_t seg = std::max<int64_t>(128, whole(tokens * blocks * 16 / 2048));
-    if (seg * 4 <= longest)
+    const int64_t row_seg = std::max<int64_t>(128, whole((int64_t)(T * per_simd / 6.)));
+    const int64_t lane_seg = std::max<int64_t>(64, whole(tokens * blocks / 4096));
+    int64_t first = 0, middle = 0; // tokens of first and of middle segments
+    for (int32_t i = 0; i < num_seqs; ++i) {
+      const int64_t len = cu[i + 1] - cu[i];
+      first += std::min(len, lane_seg);
+      middle += std::max<int64_t>(0, len - 2 * lane_seg);
+    }
+    const double row_cut = 15. + 1.7 * row_time((double)row_seg, T + 80. * n);
+    const double lane_cut =
+        lane_fits ? 25. +
+                        lane_time((double)lane_seg, W * (((double)first + 24. * n) * full +
+                                                         (double)middle * half)) +
+                        lane_time((double)lane_seg, W * (T - (double)first) * full)
+                  : 1e30;
+    const bool cut_lane = lane_cut < row_cut;
+    const int64_t seg = cut_lane ? lane_seg : row_seg;
+    if (std::min(lane_cut, row_cut) < 0.85 * uncut && seg * 3 <= longest) {
+      p.lane = cut_lane;
       p.seg = seg;
+    }
   }
   p.states = p.lane ? NS : E;
   for (int32_t n = 0; n < num_seqs; ++n)
@@ -1154,8 +1179,8 @@ hipError_t launch_ssm(int elt, const SsmCall &c, int32_t num_seqs, const int64_t
     if (grid[pass] * 256 > UINT32_MAX)
       return hipErrorInvalidConfiguration;
   }
-  const int64_t fold = (total[2] * blocks * SN + 3) / 4;
-  if (fold * 256 > UINT32_MAX)
+  const int64_t fold = total[2] * blocks * SN;
+  if (fold * 64 * kFoldWaves > UINT32_MAX)
     return hipErrorInvalidConfiguration;
   SeqTable tab;
   hipError_t e = make_seq_table(tab, num_seqs, cu, tiles, ws, s);
@@ -1179,7 +1204,7 @@ hipError_t launch_ssm(int elt, const SsmCall &c, int32_t num_seqs, const int64_t
     const auto passes = [&](auto &&run) {
       run(0, (unsigned)grid[0]);
       if (fold > 0)
-        ssm_fold_kernel<<<(unsigned)fold, 256, 0, s>>>(tab, a, SN, total[2]);
+        ssm_fold_kernel<<<(unsigned)fold, 64 * kFoldWaves, 0, s>>>(tab, a, SN);
       if (total[1] > 0)
         run(1, (unsigned)grid[1]);
       return hipGetLastError();
