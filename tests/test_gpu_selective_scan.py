@@ -396,3 +396,37 @@ def test_rows_past_the_last_sequence_are_left_alone():
     torch.cuda.synchronize()
     assert st == nat.KDA_OK
     assert torch.equal(y[:65], want) and (y[65:] == 7).all()
+
+
+def test_long_prompt_of_few_channels():
+    """20000 tokens of 1536 channels, which the call cuts on its own; the
+    recurrence and its bound (as in recurrent_ref.scan) in 64 bits on the
+    device."""
+    print("scan long prompt", flush=True)
+    T, D, N = 20000, 1536, 16
+    c = case([T], D, N, 1, F32, 230, gate=False, skip=False)
+    a = args(c)
+    y, fin = kda.selective_scan(**a, initial_state=on(c["s"]))
+    U = ref.U
+    x, A, B, C = (a[k].double() for k in ("x", "A", "B", "C"))
+    lin = a["delta"].double() + a["delta_bias"].double()
+    d = torch.logaddexp(lin, torch.zeros_like(lin))
+    rd = torch.where(lin > 0, torch.full_like(lin, 16 * U), U * (3 * lin.abs() + 12))
+    h = on(c["s"])[0].double()
+    E = torch.zeros_like(h)
+    worst = torch.zeros((), dtype=torch.float64, device=DEV)
+    for t in range(T):
+        dt_, r = d[t][:, None], rd[t][:, None]
+        arg = dt_ * A
+        decay = torch.exp(arg)
+        hold, inp = decay * h, (d[t] * x[t])[:, None] * B[t]
+        E = decay * E + hold.abs() * (arg.abs() * (r + 3 * U) + 2 * U) + inp.abs() * (r + 2 * U)
+        h = hold + inp
+        E = E + U * h.abs()
+        term = C[t] * h
+        v = term.sum(1)
+        # (2 E: the cut; N + 3 roundings of the sum; the output's own)
+        tol = (C[t].abs() * E * 2).sum(1) + (N + 3) * U * term.abs().sum(1) + U * v.abs() + 1e-37
+        worst = torch.maximum(worst, ((y[t].double() - v).abs() / tol).max())
+    assert worst.item() <= 1
+    assert ((fin[0].double() - h).abs() <= 2 * E + 1e-37).all()
