@@ -50,13 +50,10 @@ inline size_t seq_table_bytes(int32_t num_seqs) {
              : (((size_t)num_seqs + 1) * sizeof(SeqEntry) + 255) / 256 * 256;
 }
 
-// Fills `t` from the host bounds and the tiles of each sequence
-// (tiles(n, length, which) blocks in launch `which`), and for long tables
-// enqueues the launches that write it to `ws` (seq_table_bytes of it).  The
-// totals come back in total; false when one passes 2^31 - 1.
 hipError_t launch_table_part(const TablePart &part, int count, SeqEntry *dst, hipStream_t s);
 
-// (the closing-entry totals of a table that is only counted, not written)
+// The table's totals: tiles(length, w) is how many blocks a sequence has in
+// launch w.  False when a total passes 2^31 - 1.
 template <typename F>
 bool seq_totals(int32_t num_seqs, const int64_t *cu, F &&tiles, int64_t (&total)[kCounts]) {
   for (int w = 0; w < kCounts; ++w)
@@ -70,6 +67,8 @@ bool seq_totals(int32_t num_seqs, const int64_t *cu, F &&tiles, int64_t (&total)
   return true;
 }
 
+// Fills `t` from the host bounds; a long table's launches to `ws`
+// (seq_table_bytes of it) are enqueued.
 template <typename F>
 hipError_t make_seq_table(SeqTable &t, int32_t num_seqs, const int64_t *cu, F &&tiles, void *ws,
                           hipStream_t s) {

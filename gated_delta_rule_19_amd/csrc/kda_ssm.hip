@@ -527,7 +527,7 @@ __global__ __launch_bounds__(256) void ssm_row_kernel(SeqTable tab, SsmArgs a, i
 // both passes come to 59.
 constexpr int kBcTokens = 16;
 
-template <int NS> struct LaneBc {
+template <int NS> struct __align__(16) LaneBc {
   float v[2][kBcTokens][2 * NS]; // B then C of each token, two areas in turn
 };
 
