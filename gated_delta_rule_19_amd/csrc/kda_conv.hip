@@ -32,9 +32,14 @@ hipError_t launch_table_part(const TablePart &part, int count, SeqEntry *dst, hi
 }
 
 // ---- element vectors ------------------------------------------------------------
+// A 16-byte vector with its elements' alignment only: rows may start anywhere
+// (this target's unaligned access mode serves such loads).  8192 tokens of
+// 12289 bf16 channels take 84 us, 108 with one element a lane; 12288: 75.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
 template <typename T, int VEC> struct Pack;
-template <> struct Pack<bf16, 8> { u32x4 r; };
-template <> struct Pack<float, 4> { f32x4 r; };
+template <> struct Pack<bf16, 8> { u32x4_any r; };
+template <> struct Pack<float, 4> { f32x4_any r; };
 template <> struct Pack<bf16, 1> { bf16 r; };
 template <> struct Pack<float, 1> { float r; };
 
@@ -67,9 +72,10 @@ template <typename T, int VEC> __device__ __forceinline__ void store_f32(T *p, c
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       v[i] = static_cast<bf16>(x[i]);
-    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4 *>(p));
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4_any *>(p));
   } else if constexpr (VEC == 4) {
-    __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, reinterpret_cast<f32x4 *>(p));
+    __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]},
+                                reinterpret_cast<f32x4_any *>(p));
   } else {
     *p = from_f32<T>(x[0]);
   }
@@ -130,6 +136,7 @@ static_assert(kConvTile >= 7, "a tile's run-in lies within the tile before");
 
 struct ConvArgs {
   int32_t D, cw;      // channels; waves per row of channels
+  int32_t full;       // lanes with VEC channels; the D % VEC others have a lane each
   int32_t act;        // 1: silu
   int32_t num_slots;
   int32_t rows;       // step: rows
@@ -138,38 +145,15 @@ struct ConvArgs {
   const int32_t *slots;
 };
 
-// One wave per (tile of one sequence, 64 VEC channels).  The wave of a
-// sequence's first tile also reads the initial state and writes the final
-// one, so the two may be the same buffer.
+// One tile of one sequence, VEC channels from d.
 template <typename T, int VEC, int W>
-__global__ __launch_bounds__(256) void conv_kernel(SeqTable tab, ConvArgs a,
-                                                   const T *__restrict__ x,
-                                                   const T *__restrict__ weight,
-                                                   const T *__restrict__ bias, const T *init,
-                                                   T *fin, T *__restrict__ y) {
-  const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (wave >= a.waves)
-    return;
-  const int blk = (int)(wave / a.cw);
-  const int64_t d = ((wave - (int64_t)blk * a.cw) * 64 + (threadIdx.x & 63)) * VEC;
-  const SeqView seqs(tab);
-  const int n = seqs.find(blk, 0);
-  const int t0 = (blk - seqs.blk(n, 0)) * kConvTile;
-  const int len = seqs.len(n);
-  const int64_t tok0 = seqs.tok0(n);
-  int64_t slot = seqs.seq(n);
-  bool kept = true;
-  if (a.slots) {
-    slot = a.slots[slot];
-    kept = slot >= 0 && slot < a.num_slots;
-  }
-  if (d >= a.D)
-    return;
-  x += tok0 * a.xs + d;
-  y += tok0 * a.ys + d;
-
+__device__ __forceinline__ void conv_tile(const ConvArgs &a, const T *x, const T *weight,
+                                          const T *bias, const T *init, T *fin, T *y, int64_t d,
+                                          int t0, int len, int64_t slot, bool kept) {
   constexpr int kW1 = W - 1;
   using P = Pack<T, VEC>;
+  x += d;
+  y += d;
   float win[kW1][VEC];
   if (t0 > 0) {
     // (a tile is at least W - 1 tokens)
@@ -229,29 +213,64 @@ __global__ __launch_bounds__(256) void conv_kernel(SeqTable tab, ConvArgs a,
   }
 }
 
-// Single tokens: one wave per (row, 64 VEC channels); reads the W - 1 rows of
-// the row's state and the input, writes the output and the shifted state.
-template <typename T, int VEC, int W>
-__global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, const T *x,
-                                                        const T *__restrict__ weight,
-                                                        const T *__restrict__ bias,
-                                                        T *__restrict__ state, T *y) {
+// Lane l of a row of channels: the VEC channels from l VEC, or (REST, past
+// the `full` lanes with VEC of them) one of the D % VEC others.  run(vec, d).
+template <int VEC, bool REST, typename F>
+__device__ __forceinline__ void by_channels(const ConvArgs &a, int64_t l, F &&run) {
+  if (l < a.full) {
+    run(std::integral_constant<int, VEC>(), l * VEC);
+  } else if constexpr (REST) {
+    const int64_t d = (int64_t)a.full * VEC + (l - a.full);
+    if (d < a.D)
+      run(std::integral_constant<int, 1>(), d);
+  }
+}
+
+// One wave per (tile of one sequence, 64 lanes of channels).  The wave of a
+// sequence's first tile also reads the initial state and writes the final
+// one, so the two may be the same buffer.
+template <typename T, int VEC, int W, bool REST>
+__global__ __launch_bounds__(256) void conv_kernel(SeqTable tab, ConvArgs a,
+                                                   const T *__restrict__ x,
+                                                   const T *__restrict__ weight,
+                                                   const T *__restrict__ bias, const T *init,
+                                                   T *fin, T *__restrict__ y) {
   const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (wave >= a.waves)
     return;
-  const int row = (int)(wave / a.cw);
-  const int64_t d = ((wave - (int64_t)row * a.cw) * 64 + (threadIdx.x & 63)) * VEC;
-  int64_t slot = a.slots ? a.slots[row] : row;
-  if (slot < 0 || slot >= a.num_slots || d >= a.D)
-    return; // a padding row: nothing is read or written
+  const int blk = (int)(wave / a.cw);
+  const int64_t l = (wave - (int64_t)blk * a.cw) * 64 + (threadIdx.x & 63);
+  const SeqView seqs(tab);
+  const int n = seqs.find(blk, 0);
+  const int t0 = (blk - seqs.blk(n, 0)) * kConvTile;
+  const int len = seqs.len(n);
+  const int64_t tok0 = seqs.tok0(n);
+  int64_t slot = seqs.seq(n);
+  bool kept = true;
+  if (a.slots) {
+    slot = a.slots[slot];
+    kept = slot >= 0 && slot < a.num_slots;
+  }
+  by_channels<VEC, REST>(a, l, [&](auto vec, int64_t d) {
+    conv_tile<T, decltype(vec)::value, W>(a, x + tok0 * a.xs, weight, bias, init, fin,
+                                          y + tok0 * a.ys, d, t0, len, slot, kept);
+  });
+}
+
+// Single tokens: one wave per (row, 64 lanes of channels); reads the W - 1
+// rows of the row's state and the input, writes the output and the shifted
+// state.
+template <typename T, int VEC, int W>
+__device__ __forceinline__ void conv_token(const ConvArgs &a, const T *x, const T *weight,
+                                           const T *bias, T *st, T *y, int64_t d) {
   constexpr int kW1 = W - 1;
   using P = Pack<T, VEC>;
-  T *st = state + slot * kW1 * a.D + d;
+  st += d;
   P old[kW1];
 #pragma unroll
   for (int j = 0; j < kW1; ++j)
     old[j] = load_pack<T, VEC>(st + (int64_t)j * a.D);
-  const P xin = load_pack<T, VEC>(x + row * a.xs + d);
+  const P xin = load_pack<T, VEC>(x + d);
   Taps<T, VEC, W> taps;
   taps.load(weight, bias, d);
   float win[kW1][VEC], xv[VEC], yv[VEC];
@@ -260,11 +279,30 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, const T *x,
     unpack(old[j], win[j]);
   unpack(xin, xv);
   taps.apply(win, xv, a.act != 0, yv);
-  store_f32<T, VEC>(y + row * a.ys + d, yv);
+  store_f32<T, VEC>(y + d, yv);
 #pragma unroll
   for (int j = 0; j + 1 < kW1; ++j)
     store_pack<T, VEC>(st + (int64_t)j * a.D, old[j + 1]);
   store_pack<T, VEC>(st + (int64_t)(kW1 - 1) * a.D, xin);
+}
+
+template <typename T, int VEC, int W, bool REST>
+__global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, const T *x,
+                                                        const T *__restrict__ weight,
+                                                        const T *__restrict__ bias,
+                                                        T *__restrict__ state, T *y) {
+  const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (wave >= a.waves)
+    return;
+  const int row = (int)(wave / a.cw);
+  const int64_t l = (wave - (int64_t)row * a.cw) * 64 + (threadIdx.x & 63);
+  const int64_t slot = a.slots ? a.slots[row] : row;
+  if (slot < 0 || slot >= a.num_slots)
+    return; // a padding row: nothing is read or written
+  by_channels<VEC, REST>(a, l, [&](auto vec, int64_t d) {
+    conv_token<T, decltype(vec)::value, W>(a, x + row * a.xs, weight, bias,
+                                           state + slot * (W - 1) * a.D, y + row * a.ys, d);
+  });
 }
 
 // ---- launches -------------------------------------------------------------------
@@ -283,28 +321,20 @@ template <typename F> hipError_t with_width(int W, F &&f) {
   }
 }
 
-// Element type and vector width: 16-byte vectors where every row starts on a
-// 16-byte boundary, single elements otherwise.
-template <typename F> hipError_t with_type(int elt, bool wide, F &&f) {
+template <typename F> hipError_t with_type(int elt, bool rest, F &&f) {
+  using std::integral_constant;
   if (elt == 1)
-    return wide ? f(bf16(), std::integral_constant<int, 8>())
-                : f(bf16(), std::integral_constant<int, 1>());
-  return wide ? f(float(), std::integral_constant<int, 4>())
-              : f(float(), std::integral_constant<int, 1>());
-}
-
-int conv_vec(int elt, const ConvCall &c) {
-  const int vec = elt == 1 ? 8 : 4;
-  const auto bad = [](const void *p) { return ((uintptr_t)p & 15u) != 0; };
-  const bool wide = c.D % vec == 0 && c.x_stride % vec == 0 && c.y_stride % vec == 0 &&
-                    !bad(c.x) && !bad(c.y) && !bad(c.init) && !bad(c.fin);
-  return wide ? vec : 1;
+    return rest ? f(bf16(), integral_constant<int, 8>(), std::true_type())
+                : f(bf16(), integral_constant<int, 8>(), std::false_type());
+  return rest ? f(float(), integral_constant<int, 4>(), std::true_type())
+              : f(float(), integral_constant<int, 4>(), std::false_type());
 }
 
 ConvArgs conv_args(const ConvCall &c, int vec) {
   ConvArgs a{};
   a.D = c.D;
-  a.cw = (c.D + 64 * vec - 1) / (64 * vec);
+  a.full = c.D / vec;
+  a.cw = (a.full + c.D % vec + 63) / 64;
   a.act = c.act;
   a.num_slots = c.num_slots;
   a.xs = c.x_stride;
@@ -317,7 +347,7 @@ ConvArgs conv_args(const ConvCall &c, int vec) {
 
 hipError_t launch_conv(int elt, const ConvCall &c, int32_t num_seqs, const int64_t *cu, void *ws,
                        hipStream_t s) {
-  const int vec = conv_vec(elt, c);
+  const int vec = elt == 1 ? 8 : 4;
   ConvArgs a = conv_args(c, vec);
   const auto tiles = [](int64_t len, int w) -> int64_t {
     return w ? 0 : (len > kConvTile ? (len + kConvTile - 1) / kConvTile : 1);
@@ -332,10 +362,10 @@ hipError_t launch_conv(int elt, const ConvCall &c, int32_t num_seqs, const int64
   const hipError_t e = make_seq_table(tab, num_seqs, cu, tiles, ws, s);
   if (e != hipSuccess)
     return e;
-  return with_type(elt, vec > 1, [&](auto tag, auto v) {
+  return with_type(elt, c.D % vec != 0, [&](auto tag, auto v, auto rest) {
     return with_width(c.W, [&](auto w) {
       using T = decltype(tag);
-      conv_kernel<T, decltype(v)::value, decltype(w)::value>
+      conv_kernel<T, decltype(v)::value, decltype(w)::value, decltype(rest)::value>
           <<<(unsigned)((a.waves + 3) / 4), 256, 0, s>>>(
               tab, a, (const T *)c.x, (const T *)c.weight, (const T *)c.bias, (const T *)c.init,
               (T *)c.fin, (T *)c.y);
@@ -345,16 +375,16 @@ hipError_t launch_conv(int elt, const ConvCall &c, int32_t num_seqs, const int64
 }
 
 hipError_t launch_conv_step(int elt, const ConvCall &c, int32_t rows, hipStream_t s) {
-  const int vec = conv_vec(elt, c);
+  const int vec = elt == 1 ? 8 : 4;
   ConvArgs a = conv_args(c, vec);
   a.rows = rows;
   a.waves = (int64_t)rows * a.cw;
   if ((a.waves + 3) / 4 * 256 > UINT32_MAX)
     return hipErrorInvalidConfiguration;
-  return with_type(elt, vec > 1, [&](auto tag, auto v) {
+  return with_type(elt, c.D % vec != 0, [&](auto tag, auto v, auto rest) {
     return with_width(c.W, [&](auto w) {
       using T = decltype(tag);
-      conv_step_kernel<T, decltype(v)::value, decltype(w)::value>
+      conv_step_kernel<T, decltype(v)::value, decltype(w)::value, decltype(rest)::value>
           <<<(unsigned)((a.waves + 3) / 4), 256, 0, s>>>(a, (const T *)c.x, (const T *)c.weight,
                                                          (const T *)c.bias, (T *)c.fin,
                                                          (T *)c.y);

@@ -480,8 +480,8 @@ kda_status kda_segment_scan(int32_t num_segs, int32_t H, int32_t dk, int32_t dv,
  * Conventions of these calls, beside those above
  * - Token matrices ([T, D]) may be column ranges of a wider one: each has a
  *   row stride in elements, at least its row length and at most 2^22, and
- *   needs only its element type's alignment (16-byte-aligned rows run the
- *   vector loads).
+ *   needs only its element type's alignment (aligned rows run somewhat
+ *   faster).
  *   Weights, biases, A and states are dense and 16-byte aligned.
  * - slots: DEVICE int32, one entry per sequence (or row), the slice of the
  *   state buffers it uses; NULL means entry n uses slice n.  The state
