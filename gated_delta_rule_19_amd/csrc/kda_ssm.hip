@@ -74,6 +74,23 @@ __device__ __forceinline__ float log2_rate(float a) {
   return fabsf(r) == __builtin_inff() ? copysignf(3.4028235e38f, r) : r;
 }
 
+// A sum of finite steps as a finite number: its decay is the same, and a rate
+// of 0 keeps its state.  (A step that is not finite itself shows in the state
+// that the sum goes with.)
+__device__ __forceinline__ float finite_sum(float x) {
+  return fmaxf(fminf(x, 3.4028235e38f), -3.4028235e38f);
+}
+
+// x, or 0 without a thought of what x is (mask: all ones or 0).
+__device__ __forceinline__ float masked(float x, int mask) {
+  return __builtin_bit_cast(float, __builtin_bit_cast(int, x) & mask);
+}
+
+// Infinity or NaN in any lane.
+__device__ __forceinline__ bool any_nonfinite(float x) {
+  return __builtin_amdgcn_ballot_w64(__builtin_amdgcn_classf(x, 0x207)) != 0;
+}
+
 struct SsmArgs {
   int32_t D, N, G, softplus, num_slots;
   int32_t Dg;      // channels per group
@@ -153,6 +170,9 @@ __device__ __forceinline__ void buffer_put(__amdgpu_buffer_rsrc_t r, const float
 // 9.5 instructions a state and token, the vector ALU busy 70% of the time.
 // Tiles of 32 and 128 tokens: 417 and 406 us; eight waves (32 channels): 388;
 // one barrier a tile with both buffers doubled: 430.
+// Where N fills no 16 E, a tile with an infinite delta x goes through a copy
+// of the loop that keeps the states that are not there 0 (PAD; the test and
+// the copy cost 2% at N = 20 and 13).
 
 // Token I's value of every row, in all of the row's lanes.
 template <int I> __device__ __forceinline__ float row_bcast(float x) {
@@ -216,14 +236,19 @@ __device__ __forceinline__ float row_reduce16(float (&p)[16], int lane) {
 }
 
 // One token of the recurrence in all rows: I-th of its 16, k-th of its 4.
-template <int I, int E, bool FULL>
-__device__ __forceinline__ void row_token(float delta, float u, const float (&A2)[E],
+// The lane's states from `states` on are not there: rate, B and C are 0 and so
+// is the state, without a thought until delta x is infinite or NaN; MASK then
+// keeps them 0.
+template <int I, int E, bool FULL, bool MASK>
+__device__ __forceinline__ void row_token(float delta, float u, int states, const float (&A2)[E],
                                           float (&h)[E], const f32x4 (&b)[E], const f32x4 (&c)[E],
                                           float &p) {
   const float d = row_bcast<I>(delta), ui = row_bcast<I>(u);
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     h[e] = fmaf(exp2_hw(d * A2[e]), h[e], ui * b[e][I & 3]);
+    if (MASK)
+      h[e] = 16 * e < states ? h[e] : 0.f;
     if (FULL)
       p = e == 0 ? c[e][I & 3] * h[e] : fmaf(c[e][I & 3], h[e], p);
   }
@@ -241,6 +266,7 @@ template <int E> struct __align__(16) RowLds {
   float bc[2][16 * E][TT + 4];       // B, C by state
   float2 du[CH][TT + 32 / CH];       // (delta, delta x)
   float y[CH][TT + 64 / CH];         // read-outs
+  alignas(16) int odd[4];                  // a wave staged a delta x that is not finite
 };
 
 // Values a thread stages from a matrix: rows r0, r0 + kStep, ... of a tile, P
@@ -273,7 +299,7 @@ template <typename T, int P, int kN, int kStep> struct Stage {
   __device__ __forceinline__ void next(int rows) { p += rows * stride; }
 };
 
-template <typename T, int E, int P, bool FULL>
+template <typename T, int E, int P, bool PAD, bool FULL>
 __device__ __forceinline__ float row_segment(const SsmArgs &a, RowLds<E> &lds, float (&h)[E],
                                              const float (&A2)[E], const T *x, const T *dl,
                                              const T *z, const T *B, const T *C, T *y, int ntok,
@@ -289,6 +315,7 @@ __device__ __forceinline__ float row_segment(const SsmArgs &a, RowLds<E> &lds, f
   const int sc = tid % (CH / P) * P, sr = tid / (CH / P); // channel and first row it stages
   const int sn = tid % (NP / P) * P, st = tid / (NP / P); // state and first token of B and C
   const int rc = wave * 4 + (lane >> 4), ri = lane & 15;
+  const int states = a.N - ri, has_skip = a.skip ? -1 : 0;
   const bool in = sc < chans;
   Stage<T, P, kRows, kStep> sx(x, a.xs, sr, sc, in), sd(dl, a.dls, sr, sc, in),
       sz(z, a.zs, sr, sc, in);
@@ -348,11 +375,20 @@ __device__ __forceinline__ float row_segment(const SsmArgs &a, RowLds<E> &lds, f
         for (int j = 0; j < P; ++j)
           d[k][j] = sr + kStep * k < n ? d[k][j] : 0.f;
     }
+    float worst = 0.f; // not finite where one of its products is not
 #pragma unroll
     for (int k = 0; k < kRows; ++k)
 #pragma unroll
-      for (int j = 0; j < P; ++j)
-        lds.du[sc + j][sr + kStep * k] = float2{d[k][j], d[k][j] * xk[k][j]};
+      for (int j = 0; j < P; ++j) {
+        const float u = d[k][j] * xk[k][j];
+        lds.du[sc + j][sr + kStep * k] = float2{d[k][j], u};
+        worst = fmaf(0.f, u, worst);
+      }
+    if (PAD) {
+      const int odd = any_nonfinite(worst);
+      if (lane == 0)
+        lds.odd[wave] = odd;
+    }
 #pragma unroll
     for (int k = 0; k < kBc; ++k)
 #pragma unroll
@@ -364,11 +400,18 @@ __device__ __forceinline__ float row_segment(const SsmArgs &a, RowLds<E> &lds, f
     __syncthreads();
     fetch(ntok - t0 - TT); // in flight during the recurrence
 
-    for (int s0 = 0; s0 < n; s0 += 16) {
+    // (a step that is not finite makes delta x not finite)
+    bool odd = false;
+    if (PAD) {
+      const int4 o = *reinterpret_cast<const int4 *>(lds.odd);
+      odd = __builtin_amdgcn_readfirstlane(o.x | o.y | o.z | o.w) != 0;
+    }
+    const auto tokens16 = [&](int s0, auto mask) {
       const float2 du = lds.du[rc][s0 + ri];
       float p[16];
       const auto quad = [&](auto q) {
         constexpr int Q = decltype(q)::value;
+        constexpr bool M = decltype(mask)::value;
         f32x4 b[E], c[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -376,10 +419,10 @@ __device__ __forceinline__ float row_segment(const SsmArgs &a, RowLds<E> &lds, f
           if (FULL)
             c[e] = *reinterpret_cast<const f32x4 *>(&lds.bc[1][16 * e + ri][s0 + 4 * Q]);
         }
-        row_token<4 * Q, E, FULL>(du.x, du.y, A2, h, b, c, p[4 * Q]);
-        row_token<4 * Q + 1, E, FULL>(du.x, du.y, A2, h, b, c, p[4 * Q + 1]);
-        row_token<4 * Q + 2, E, FULL>(du.x, du.y, A2, h, b, c, p[4 * Q + 2]);
-        row_token<4 * Q + 3, E, FULL>(du.x, du.y, A2, h, b, c, p[4 * Q + 3]);
+        row_token<4 * Q, E, FULL, M>(du.x, du.y, states, A2, h, b, c, p[4 * Q]);
+        row_token<4 * Q + 1, E, FULL, M>(du.x, du.y, states, A2, h, b, c, p[4 * Q + 1]);
+        row_token<4 * Q + 2, E, FULL, M>(du.x, du.y, states, A2, h, b, c, p[4 * Q + 2]);
+        row_token<4 * Q + 3, E, FULL, M>(du.x, du.y, states, A2, h, b, c, p[4 * Q + 3]);
       };
       quad(std::integral_constant<int, 0>());
       quad(std::integral_constant<int, 1>());
@@ -389,7 +432,13 @@ __device__ __forceinline__ float row_segment(const SsmArgs &a, RowLds<E> &lds, f
         lds.y[rc][s0 + ri] = row_reduce16(p, lane);
       else
         sum += du.x; // (lane i: the tokens i of every 16)
-    }
+    };
+    if (PAD && odd)
+      for (int s0 = 0; s0 < n; s0 += 16)
+        tokens16(s0, std::true_type());
+    else
+      for (int s0 = 0; s0 < n; s0 += 16)
+        tokens16(s0, std::false_type());
     __syncthreads();
 
     if (FULL) {
@@ -400,7 +449,8 @@ __device__ __forceinline__ float row_segment(const SsmArgs &a, RowLds<E> &lds, f
         float v[P];
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-          v[j] = fmaf(skip[j], xk[k][j], lds.y[sc + j][row]);
+          v[j] = lds.y[sc + j][row];
+          v[j] = fmaf(skip[j], masked(xk[k][j], has_skip), v[j]);
           if (z)
             v[j] *= gate[k][j];
         }
@@ -412,7 +462,8 @@ __device__ __forceinline__ float row_segment(const SsmArgs &a, RowLds<E> &lds, f
   return sum;
 }
 
-template <typename T, int E, int P>
+// PAD: fewer than 16 E states.
+template <typename T, int E, int P, bool PAD>
 __global__ __launch_bounds__(256) void ssm_row_kernel(SeqTable tab, SsmArgs a, int pass,
                                                           int64_t grid,
                                                           const T *__restrict__ x,
@@ -490,10 +541,10 @@ __global__ __launch_bounds__(256) void ssm_row_kernel(SeqTable tab, SsmArgs a, i
   C += t0 * a.Cs + g * a.N;
   float sum = 0.f;
   if (pass == 1 || j == 0)
-    row_segment<T, E, P, true>(a, lds, h, A2, x, dl, z ? z + t0 * a.zs + d0 : nullptr, B, C,
+    row_segment<T, E, P, PAD, true>(a, lds, h, A2, x, dl, z ? z + t0 * a.zs + d0 : nullptr, B, C,
                                 y + t0 * a.ys + d0, ntok, chans, bias, skip);
   else
-    sum = row_segment<T, E, P, false>(a, lds, h, A2, x, dl, nullptr, B, C, nullptr, ntok, chans,
+    sum = row_segment<T, E, P, PAD, false>(a, lds, h, A2, x, dl, nullptr, B, C, nullptr, ntok, chans,
                                        bias, skip);
 
   if (j == nseg - 1) {
@@ -510,7 +561,7 @@ __global__ __launch_bounds__(256) void ssm_row_kernel(SeqTable tab, SsmArgs a, i
       for (int e = 0; e < E; ++e)
         a.pend[(pair0 + j) * pstep + at + e * 16 * 64] = h[e];
       if (j > 0 && ri == 15)
-        a.psum[((pair0 + j) * a.G * a.cb + g * a.cb + dg / 64) * 64 + dg % 64] = sum;
+        a.psum[((pair0 + j) * a.G * a.cb + g * a.cb + dg / 64) * 64 + dg % 64] = finite_sum(sum);
     }
   }
 }
@@ -525,10 +576,17 @@ __global__ __launch_bounds__(256) void ssm_row_kernel(SeqTable tab, SsmArgs a, i
 // 138 against 67 us at 256 x 1536.)  131072 x 1536 bf16, cut into 171
 // segments: 1.32 ms, 65 cycles a state and token where the instructions of
 // both passes come to 59.
+// There is a kernel for every N up to 16: a state too many would cost its
+// instructions (8192 tokens of 64 sequences x 1536 with N = 5: 84 us, 96 with
+// 8 states), and would have to be kept from making 0 * inf of an infinite
+// input.
 constexpr int kBcTokens = 16;
 
-template <int NS> struct __align__(16) LaneBc {
-  float v[2][kBcTokens][2 * NS]; // B then C of each token, two areas in turn
+// Places for the N values of B or C of a token: 4, 8 or 16.
+constexpr int lane_places(int N) { return N <= 4 ? 4 : (N <= 8 ? 8 : 16); }
+
+template <int NP> struct __align__(16) LaneBc {
+  float v[2][kBcTokens][2 * NP]; // B then C of each token, two areas in turn
 };
 
 // One element per lane of a row of channels; lanes at or past `bytes` (the
@@ -544,8 +602,8 @@ __device__ __forceinline__ void row_store(T *p, int bytes, int lane, float v) {
 
 // The values of B and C a lane brings in per area: state i of every kStep-th
 // token.  Tokens past the segment and states past N read 0.
-template <typename T, int NS> struct BcLoader {
-  static constexpr int kStep = 64 / NS;
+template <typename T, int NP> struct BcLoader {
+  static constexpr int kStep = 64 / NP;
   static constexpr int kPer = kBcTokens / kStep;
   const T *B, *C;
   int64_t Bs, Cs;
@@ -556,8 +614,8 @@ template <typename T, int NS> struct BcLoader {
   __device__ __forceinline__ BcLoader(const T *B_, const T *C_, int64_t Bs_, int64_t Cs_, int N,
                                       int lane)
       : B(B_), C(C_), Bs(Bs_), Cs(Cs_) {
-    t0 = lane / NS;
-    i = lane % NS;
+    t0 = lane / NP;
+    i = lane % NP;
     on = i < N;
   }
   __device__ __forceinline__ void fetch(int tok, int ntok) {
@@ -573,21 +631,22 @@ template <typename T, int NS> struct BcLoader {
       c[k] = buffer_raw<T, 1>(rc, ok ? (t * (int)Cs + i) * (int)sizeof(T) : -1, 0);
     }
   }
-  __device__ __forceinline__ void put(float (*area)[2 * NS]) const {
+  __device__ __forceinline__ void put(float (*area)[2 * NP]) const {
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       area[t0 + k * kStep][i] = widen<T, 1>(b[k], 0);
-      area[t0 + k * kStep][NS + i] = widen<T, 1>(c[k], 0);
+      area[t0 + k * kStep][NP + i] = widen<T, 1>(c[k], 0);
     }
   }
 };
 
 template <typename T, int NS, bool FULL>
-__device__ __forceinline__ float lane_segment(const SsmArgs &a, LaneBc<NS> &lds, float (&h)[NS],
-                                              const float (&A2)[NS], BcLoader<T, NS> bc,
+__device__ __forceinline__ float lane_segment(const SsmArgs &a, LaneBc<lane_places(NS)> &lds,
+                                              float (&h)[NS], const float (&A2)[NS],
+                                              BcLoader<T, lane_places(NS)> bc,
                                               const T *x, const T *dl, const T *z, T *y, int ntok,
                                               int row_bytes, int lane, float bias, float skip) {
-  constexpr int U = 4;
+  constexpr int U = 4, NP = lane_places(NS);
   Raw<T> xr[U], dr[U], zr[U];
   float sum = 0.f;
   const auto bytes = [&](int t) { return t < ntok ? row_bytes : 0; };
@@ -609,7 +668,7 @@ __device__ __forceinline__ float lane_segment(const SsmArgs &a, LaneBc<NS> &lds,
   for (int b0 = 0; b0 < ntok; b0 += kBcTokens) {
     // this wave's reads of the area two before are done: its LDS
     // instructions run in order
-    float(*area)[2 * NS] = lds.v[(b0 / kBcTokens) & 1];
+    float(*area)[2 * NP] = lds.v[(b0 / kBcTokens) & 1];
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     __builtin_amdgcn_wave_barrier();
     bc.put(area);
@@ -652,20 +711,23 @@ __device__ __forceinline__ float lane_segment(const SsmArgs &a, LaneBc<NS> &lds,
           const f32x4 bv = *reinterpret_cast<const f32x4 *>(row + q);
           f32x4 cv;
           if (FULL)
-            cv = *reinterpret_cast<const f32x4 *>(row + NS + q);
+            cv = *reinterpret_cast<const f32x4 *>(row + NP + q);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 4 && q + i < NS; ++i) {
             h[q + i] = fmaf(exp2_hw(d[k] * A2[q + i]), h[q + i], u * bv[i]);
             if (FULL)
               acc[k] = fmaf(cv[i], h[q + i], acc[k]);
           }
         }
-        if (FULL)
-          acc[k] = fmaf(skip, xk[k], acc[k]);
-        else
+        if (!FULL)
           sum += d[k];
       }
       if (FULL) {
+        if (a.skip) { // (without one, an infinite x adds no 0 * inf)
+#pragma unroll
+          for (int k = 0; k < U; ++k)
+            acc[k] = fmaf(skip, xk[k], acc[k]);
+        }
 #pragma unroll
         for (int k = 0; k < U; ++k)
           row_store(y + (t0 + k) * a.ys, bytes(t0 + k), lane, z ? acc[k] * gate[k] : acc[k]);
@@ -683,7 +745,7 @@ __global__ __launch_bounds__(256, 4) void ssm_lane_kernel(SeqTable tab, SsmArgs 
                                                        const T *__restrict__ B,
                                                        const T *__restrict__ C,
                                                        T *__restrict__ y) {
-  __shared__ LaneBc<NS> lds[4];
+  __shared__ LaneBc<lane_places(NS)> lds[4];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int blocks = a.G * a.cb, quads = (blocks + 3) / 4;
@@ -706,7 +768,7 @@ __global__ __launch_bounds__(256, 4) void ssm_lane_kernel(SeqTable tab, SsmArgs 
   float A2[NS], h[NS];
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
-    A2[i] = in && i < a.N ? log2_rate(a.A[d * a.N + i]) : 0.f;
+    A2[i] = in ? log2_rate(a.A[d * NS + i]) : 0.f;
     h[i] = 0.f;
   }
   int64_t slot = seqs.seq(n);
@@ -717,11 +779,10 @@ __global__ __launch_bounds__(256, 4) void ssm_lane_kernel(SeqTable tab, SsmArgs 
   }
   if (j == 0) {
     if (a.init && kept && in) {
-      const float *p = a.init + (slot * a.D + d) * a.N;
+      const float *p = a.init + (slot * a.D + d) * NS;
 #pragma unroll
       for (int i = 0; i < NS; ++i)
-        if (i < a.N)
-          h[i] = p[i];
+        h[i] = p[i];
     }
   } else if (pass == 1) {
     const float *pe = a.pend + ((pair0 + j - 1) * blocks + gc) * NS * 64 + lane;
@@ -731,8 +792,8 @@ __global__ __launch_bounds__(256, 4) void ssm_lane_kernel(SeqTable tab, SsmArgs 
   }
 
   const int64_t t0 = tok0 + s0;
-  const BcLoader<T, NS> bc(B + t0 * a.Bs + g * a.N, C + t0 * a.Cs + g * a.N, a.Bs, a.Cs, a.N,
-                           lane);
+  const BcLoader<T, lane_places(NS)> bc(B + t0 * a.Bs + g * NS, C + t0 * a.Cs + g * NS, a.Bs,
+                                        a.Cs, NS, lane);
   const float bias = in && a.bias ? a.bias[d] : 0.f;
   const float skip = in && a.skip ? a.skip[d] : 0.f;
   const int64_t d0 = (int64_t)g * a.Dg + cbi * 64; // the wave's first channel
@@ -749,11 +810,10 @@ __global__ __launch_bounds__(256, 4) void ssm_lane_kernel(SeqTable tab, SsmArgs 
 
   if (j == nseg - 1) {
     if (a.fin && kept && in) {
-      float *p = a.fin + (slot * a.D + d) * a.N;
+      float *p = a.fin + (slot * a.D + d) * NS;
 #pragma unroll
       for (int i = 0; i < NS; ++i)
-        if (i < a.N)
-          p[i] = h[i];
+        p[i] = h[i];
     }
   } else if (pass == 0) {
     float *pe = a.pend + ((pair0 + j) * blocks + gc) * NS * 64 + lane;
@@ -761,7 +821,7 @@ __global__ __launch_bounds__(256, 4) void ssm_lane_kernel(SeqTable tab, SsmArgs 
     for (int i = 0; i < NS; ++i)
       pe[i * 64] = h[i];
     if (j > 0)
-      a.psum[((pair0 + j) * blocks + gc) * 64 + lane] = sum;
+      a.psum[((pair0 + j) * blocks + gc) * 64 + lane] = finite_sum(sum);
   }
 }
 
@@ -819,7 +879,7 @@ __global__ __launch_bounds__(64 * kFoldWaves) void ssm_fold_kernel(SeqTable tab,
     return h;
   };
   s_end[wave][lane] = fold(0.f, false);
-  s_sum[wave][lane] = sum;
+  s_sum[wave][lane] = finite_sum(sum);
   __syncthreads();
   float h = pe[0];
   for (int w = 0; w < wave; ++w)
@@ -983,7 +1043,8 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(StepArgs a, const T *__re
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           h[j][k][i] = fmaf(exp2_hw(dj * A[j][k][i]), h[j][k][i], uj * b[k][i]);
-          acc = fmaf(c[k][i], h[j][k][i], acc);
+          // (a state that is not there adds no 0 * inf)
+          acc = n < a.N ? fmaf(c[k][i], h[j][k][i], acc) : acc;
         }
         if (ch < chans && n < a.N) {
           if constexpr (VEC == 4)
@@ -1000,7 +1061,7 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(StepArgs a, const T *__re
     }
   }
   if (lane < chans) {
-    float v = fmaf(skip, xv, out);
+    float v = a.skip ? fmaf(skip, xv, out) : out;
     if (z)
       v *= silu(zv);
     y[row * a.ys + d0 + lane] = from_f32<T>(v);
@@ -1008,8 +1069,7 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(StepArgs a, const T *__re
 }
 
 // ---- host ---------------------------------------------------------------------------
-// States a lane holds in the lane kernel, and in the row kernel.
-int lane_states(int N) { return N <= 4 ? 4 : (N <= 8 ? 8 : 16); }
+// States a lane of the row kernel holds.
 int row_states(int N) { return N <= 16 ? 1 : (N <= 32 ? 2 : (N <= 64 ? 4 : 8)); }
 constexpr int kLaneMaxStates = 16;
 
@@ -1018,24 +1078,25 @@ size_t up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 int64_t chan_blocks(int32_t D, int32_t G) { return (int64_t)G * ((D / G + 63) / 64); }
 
-template <typename F> hipError_t with_lane(int NS, F &&f) {
-  using std::integral_constant;
-  if (NS == 4)
-    return f(integral_constant<int, 4>());
-  if (NS == 8)
-    return f(integral_constant<int, 8>());
-  return f(integral_constant<int, 16>());
+template <int N = 1, typename F> hipError_t with_lane(int states, F &&f) {
+  if constexpr (N < kLaneMaxStates)
+    if (states != N)
+      return with_lane<N + 1>(states, f);
+  return f(std::integral_constant<int, N>());
 }
 
-template <typename F> hipError_t with_row(int E, bool pairs, F &&f) {
+template <typename F> hipError_t with_row(int E, bool pairs, bool pad, F &&f) {
   using std::integral_constant;
+  const auto padded = [&](auto e, auto p) {
+    return pad ? f(e, p, std::true_type()) : f(e, p, std::false_type());
+  };
   using one = integral_constant<int, 1>;
   using two = integral_constant<int, 2>;
   switch (E) {
-  case 1: return pairs ? f(one(), two()) : f(one(), one());
-  case 2: return pairs ? f(two(), two()) : f(two(), one());
-  case 4: return f(integral_constant<int, 4>(), one());
-  default: return f(integral_constant<int, 8>(), one());
+  case 1: return pairs ? padded(one(), two()) : padded(one(), one());
+  case 2: return pairs ? padded(two(), two()) : padded(two(), one());
+  case 4: return padded(integral_constant<int, 4>(), one());
+  default: return padded(integral_constant<int, 8>(), one());
   }
 }
 
@@ -1071,11 +1132,11 @@ SsmPlan ssm_plan(int32_t num_seqs, const int64_t *cu, int32_t D, int32_t N, int3
   // multiples of 32 tokens: whole tiles
   const auto whole = [](int64_t x) { return std::max<int64_t>(32, (x + 31) / 32 * 32); };
   p.seg = whole(longest);
-  const int NS = lane_states(N), E = row_states(N);
+  const int E = row_states(N);
   const double T = (double)tokens, L = (double)longest, W = (double)blocks, n = num_seqs;
   // (the states' share of each kernel's instructions, beside N = 16)
-  const double row_scale = (33. * E + 15.) / 48., full = (24. * NS + 150.) / 534. * 0.24e-3,
-               half = (20. * NS + 90.) / 410. * 0.18e-3;
+  const double row_scale = (33. * E + 15.) / 48., full = (24. * N + 150.) / 534. * 0.24e-3,
+               half = (20. * N + 90.) / 410. * 0.18e-3;
   // row waves a SIMD, one sequence
   const double per_simd = (double)G * ((D / G + kRowChans - 1) / kRowChans) * 4. / 1024.;
   const auto row_time = [&](double longest_run, double tokens_run) {
@@ -1083,7 +1144,7 @@ SsmPlan ssm_plan(int32_t num_seqs, const int64_t *cu, int32_t D, int32_t N, int3
                                 0.020 * longest_run + 0.0165 * per_simd * tokens_run);
   };
   const auto lane_time = [&](double longest_run, double work) {
-    const double alone = 0.40 * longest_run * NS / 16.;
+    const double alone = 0.40 * longest_run * N / 16.;
     return std::max(alone, work) + 0.15 * std::min(alone, work);
   };
   const bool lane_fits = N <= kLaneMaxStates;
@@ -1117,7 +1178,7 @@ SsmPlan ssm_plan(int32_t num_seqs, const int64_t *cu, int32_t D, int32_t N, int3
       p.seg = seg;
     }
   }
-  p.states = p.lane ? NS : E;
+  p.states = p.lane ? N : E;
   for (int32_t n = 0; n < num_seqs; ++n)
     p.pairs += ssm_num_segments(cu[n + 1] - cu[n], p) - 1;
   const size_t SN = (size_t)p.states * (p.lane ? 1 : 16);
@@ -1215,9 +1276,9 @@ hipError_t launch_ssm(int elt, const SsmCall &c, int32_t num_seqs, const int64_t
           ssm_lane_kernel<T, decltype(ns)::value><<<n, 256, 0, s>>>(tab, a, pass, x, dl, z, B, C, y);
         });
       });
-    return with_row(plan.states, pairs, [&](auto e, auto p2) {
+    return with_row(plan.states, pairs, c.N < SN, [&](auto e, auto p2, auto pad) {
       return passes([&](int pass, unsigned n) {
-        ssm_row_kernel<T, decltype(e)::value, decltype(p2)::value>
+        ssm_row_kernel<T, decltype(e)::value, decltype(p2)::value, decltype(pad)::value>
             <<<n, 256, 0, s>>>(tab, a, pass, total[pass] * per, x, dl, z, B, C, y);
       });
     });

@@ -430,3 +430,79 @@ def test_long_prompt_of_few_channels():
         worst = torch.maximum(worst, ((y[t].double() - v).abs() / tol).max())
     assert worst.item() <= 1
     assert ((fin[0].double() - h).abs() <= 2 * E + 1e-37).all()
+
+
+def infinite(lens, N, seed, skip, what, at):
+    """A case of positive terms with one infinite input: every sum that it
+    enters is infinite, none is the difference of two."""
+    c = case(lens, 66, N, 1, F32, seed, skip=skip)
+    for k in ("x", "B", "C", "s", "D"):
+        if c[k] is not None:
+            c[k] = c[k].abs()
+    c["z"] = c["z"].abs() + 0.1
+    c[what] = c[what].clone()
+    c[what][at, 5] = float("inf")
+    return c
+
+
+def same_classes(name, got, want, tol):
+    """Infinities where the reference has them, the others within the bound."""
+    got = ref.f64(got)
+    inf = np.isinf(want)
+    assert inf.any() and not np.isnan(want).any()
+    assert np.array_equal(got[inf], want[inf]), name
+    ref.check(name, np.where(inf, 0.0, got), np.where(inf, 0.0, want), np.where(inf, 0.0, tol))
+
+
+@pytest.mark.parametrize("what", ["x", "delta"])
+@pytest.mark.parametrize("skip", [False, True])
+@pytest.mark.parametrize("N", [1, 3, 5, 8, 12, 16, 20, 40, 65, 128])
+def test_infinite_inputs_stay_infinite(N, skip, what):
+    """Without a skip, and with state counts that fill no register, lane or
+    tile: what is not there adds no 0 * inf."""
+    print("scan infinite inputs", N, skip, what, flush=True)
+    for lens, at in (([90, 41, 130], 100), ([230], 17), ([230], 100)):
+        c = infinite(lens, N, 240 + N, skip, what, at)
+        ry, yt, rf, ft = reference(c)
+        for split in (1, 4):
+            y, fin = run(c, split_hint=split)
+            same_classes("y", y, ry, yt)
+            same_classes("final state", fin, rf, ft)
+
+
+@pytest.mark.parametrize("what", ["x", "delta"])
+@pytest.mark.parametrize("N", [1, 3, 5, 12, 16, 20, 65, 67, 127, 128])
+def test_infinite_inputs_of_a_step(N, what):
+    print("scan step infinite inputs", N, what, flush=True)
+    for skip in (False, True):
+        c = infinite([1] * 5, N, 260 + N, skip, what, 3)
+        ry, yt, rf, ft = reference(c, fold=1.0)
+        state = on(c["s"]).clone()
+        y = kda.selective_scan_step(state, **args(c))
+        torch.cuda.synchronize()
+        same_classes("y", y, ry, yt)
+        same_classes("state", state, rf, ft)
+
+
+@pytest.mark.parametrize("N", [16, 20])
+@pytest.mark.parametrize("split", [1, 4])
+def test_steps_whose_sum_passes_the_largest_number(N, split):
+    """A rate of 0 keeps its state over any finite step, also over a segment
+    whose steps add up to more than an fp32 holds."""
+    print("scan large steps", N, split, flush=True)
+    c = case([300], 66, N, 1, F32, 280, softplus=False, bias=False)
+    c["A"][:, 2] = 0.0
+    for t in (100, 110, 200):
+        c["delta"][t, 5] = 2e38
+        c["x"][t, 5] = 0.0
+    compare(c, *run(c, split_hint=split))
+
+
+@pytest.mark.parametrize("N", range(1, 17))
+def test_every_state_count_of_one_lane(N):
+    """split_hint > 1 and many sequences: all states of a channel in a lane,
+    in a kernel of their own for each count."""
+    print("scan lane states", N, flush=True)
+    for dtype in (F32, BF16):
+        c = case([70, 150, 33], 66, N, 2, dtype, 290 + N)
+        compare(c, *run(c, split_hint=2))
