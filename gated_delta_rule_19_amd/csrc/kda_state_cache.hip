@@ -230,7 +230,7 @@ hipError_t cache_launch(const CacheCall &c, const float *state, const void *code
   const int64_t rows = (int64_t)kRows * (64 >> a.lanes_log2);
   a.per = (c.R + rows - 1) / rows;
   a.waves = a.per * c.n;
-  if ((a.waves + 3) / 4 * 256 > UINT32_MAX)
+  if (a.waves > (int64_t)(UINT32_MAX / 256) * 4) // (the threads' count may pass 64 bits)
     return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)((a.waves + 3) / 4));
   auto k = [&](auto vec, auto kk) {

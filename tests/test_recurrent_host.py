@@ -202,6 +202,15 @@ def test_state_cache_refuses(lib, status, kw):
                               a["num_a"], a["a"], a["dst"], a["num_b"], None) == status
 
 
+def test_state_cache_refuses_a_grid_that_passes_64_bits(lib):
+    n, R, L = (1 << 31) - 1, 1 << 31, 255
+    for fmt in (0, 1):
+        assert lib.kda_state_store(n, R, L, fmt, PTR, None, n, PTR + (1 << 24), PTR + (2 << 24),
+                                   None, n, None) == INVALID
+        assert lib.kda_state_load(n, R, L, fmt, PTR + (1 << 24), PTR + (2 << 24), None, n, PTR,
+                                  None, n, None) == INVALID
+
+
 def test_state_cache_of_no_items_is_a_no_op(lib):
     assert lib.kda_state_store(0, 8, 16, 0, None, None, 0, None, None, None, 0, None) == OK
     assert lib.kda_state_load(0, 8, 16, 1, None, None, None, 0, None, None, 0, None) == OK
