@@ -835,6 +835,17 @@ __global__ __launch_bounds__(256, 4) void ssm_lane_kernel(SeqTable tab, SsmArgs 
 // flight at a time.)
 constexpr int kFoldWaves = 8;
 
+// The state after a segment, from the one before it, its sum of steps and its
+// end state from zero.  An infinite state stays infinite over it: its steps'
+// decays are not 0, but their product may be.  (Over an infinite step, and at
+// an infinite rate, the decay is 0 and the product NaN.)
+__device__ __forceinline__ float fold_segment(float sum, float A2, float h, float end) {
+  constexpr float kMax = 3.4028235e38f;
+  const float decayed = fmaf(exp2_hw(sum * A2), h, end);
+  const bool stays = fabsf(h) == __builtin_inff() && fabsf(sum) < kMax && fabsf(A2) < kMax;
+  return stays ? h + end : decayed;
+}
+
 __global__ __launch_bounds__(64 * kFoldWaves) void ssm_fold_kernel(SeqTable tab, SsmArgs a,
                                                                    int SN) {
   __shared__ float s_end[kFoldWaves][64], s_sum[kFoldWaves][64];
@@ -869,7 +880,7 @@ __global__ __launch_bounds__(64 * kFoldWaves) void ssm_fold_kernel(SeqTable tab,
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (j + k < j1) {
-          h = fmaf(exp2_hw(sd[k] * A2), h, e[k]);
+          h = fold_segment(sd[k], A2, h, e[k]);
           if (write)
             pe[(j + k) * pstep] = h;
           else
@@ -883,7 +894,7 @@ __global__ __launch_bounds__(64 * kFoldWaves) void ssm_fold_kernel(SeqTable tab,
   __syncthreads();
   float h = pe[0];
   for (int w = 0; w < wave; ++w)
-    h = fmaf(exp2_hw(s_sum[w][lane] * A2), h, s_end[w][lane]);
+    h = fold_segment(s_sum[w][lane], A2, h, s_end[w][lane]);
   fold(h, true);
 }
 

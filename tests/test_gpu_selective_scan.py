@@ -506,3 +506,19 @@ def test_every_state_count_of_one_lane(N):
     for dtype in (F32, BF16):
         c = case([70, 150, 33], 66, N, 2, dtype, 290 + N)
         compare(c, *run(c, split_hint=2))
+
+
+@pytest.mark.parametrize("N", [4, 16])
+def test_infinite_states_outlast_a_segment(N):
+    """The decay over a segment, not that of a step, underflows: what is
+    infinite before it is infinite after it, cut or not."""
+    print("scan infinite states over segments", N, flush=True)
+    for at in (17, 100):
+        c = infinite([700], N, 320, False, "x", at)
+        c["bias"] = None
+        c["A"] = -1.0 - 3.0 * torch.rand((66, N), generator=torch.Generator().manual_seed(321))
+        ry, yt, rf, ft = reference(c)
+        for split in (1, 5, 21):
+            y, fin = run(c, split_hint=split)
+            same_classes("y", y, ry, yt)
+            same_classes("final state", fin, rf, ft)
