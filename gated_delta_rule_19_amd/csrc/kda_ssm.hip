@@ -167,7 +167,7 @@ __device__ __forceinline__ void buffer_put(__amdgpu_buffer_rsrc_t r, const float
 // instead of 415 at 8192 x 8192 bf16): the threads go down the channels of a
 // row, evaluate softplus and gate there, and take the read-outs back the same
 // way for skip, gate and store.  391 us at that size, with two waves a SIMD:
-// 9.5 instructions a state and token, the vector ALU busy 70% of the time.
+// 9.5 instructions a state and token, the vector ALU busy 75% of the time.
 // Tiles of 32 and 128 tokens: 417 and 406 us; eight waves (32 channels): 388;
 // one barrier a tile with both buffers doubled: 430.
 // Where N fills no 16 E, a tile with an infinite delta x goes through a copy
