@@ -836,14 +836,22 @@ __global__ __launch_bounds__(256, 4) void ssm_lane_kernel(SeqTable tab, SsmArgs 
 constexpr int kFoldWaves = 8;
 
 // The state after a segment, from the one before it, its sum of steps and its
-// end state from zero.  An infinite state stays infinite over it: its steps'
-// decays are not 0, but their product may be.  (Over an infinite step, and at
-// an infinite rate, the decay is 0 and the product NaN.)
+// end state from zero.  The decay 2^e, e = sum A2, is the product of the
+// steps' decays and may lie outside fp32 where the state does not: with A > 0
+// or negative steps a state of 0 or 1e-30 may grow by e^100, and an infinite
+// one outlasts a decay of e^-100.  So only 2^(e - ceil(e)), in (1/2, 1], is
+// multiplied, and the rest moves the state's exponent.  (512 passes the way
+// from the largest fp32 number to the smallest.  Over an infinite step, and
+// at an infinite rate, both of which stand here as the largest number, the
+// decay is what that of a step would be: 0, or infinite, with the NaN that
+// they make.)
 __device__ __forceinline__ float fold_segment(float sum, float A2, float h, float end) {
   constexpr float kMax = 3.4028235e38f;
-  const float decayed = fmaf(exp2_hw(sum * A2), h, end);
-  const bool stays = fabsf(h) == __builtin_inff() && fabsf(sum) < kMax && fabsf(A2) < kMax;
-  return stays ? h + end : decayed;
+  if (fabsf(sum) < kMax && fabsf(A2) < kMax) {
+    const float e = fminf(fmaxf(sum * A2, -512.f), 512.f), whole = ceilf(e);
+    return ldexpf(exp2_hw(e - whole) * h, (int)whole) + end;
+  }
+  return fmaf(exp2_hw(sum * A2), h, end);
 }
 
 __global__ __launch_bounds__(64 * kFoldWaves) void ssm_fold_kernel(SeqTable tab, SsmArgs a,
