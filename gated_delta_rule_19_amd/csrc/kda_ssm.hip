@@ -66,13 +66,14 @@ __device__ __forceinline__ float silu(float x) {
   return x * __builtin_amdgcn_rcpf(1.f + exp2_hw(-x * kLog2e));
 }
 
-// A in log2 units.  An infinite A is taken as the largest finite one: its
-// decay is the same, and a step of 0 (which the kernels take past a segment's
-// end) leaves the state as it is instead of making 0 * inf.
-__device__ __forceinline__ float log2_rate(float a) {
-  const float r = a * kLog2e;
+// A in log2 units.  An infinite A is taken as the largest finite one, by
+// prompts and single tokens alike: its decay is the same, and a step of 0
+// (which the prompt kernels take past a segment's end) leaves the state as it
+// is instead of making 0 * inf.
+__device__ __forceinline__ float finite_rate(float r) {
   return fabsf(r) == __builtin_inff() ? copysignf(3.4028235e38f, r) : r;
 }
+__device__ __forceinline__ float log2_rate(float a) { return finite_rate(a * kLog2e); }
 
 // A sum of finite steps as a finite number: its decay is the same, and a rate
 // of 0 keeps its state.  (A step that is not finite itself shows in the state
@@ -1016,6 +1017,12 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(StepArgs a, const T *__re
   if (a.softplus)
     delta = softplus(delta);
   const float u = delta * xv;
+  // An infinite rate counts as the largest finite one, as in the prompt
+  // kernels.  That shows in steps of (nearly) 0 alone, so only waves with one
+  // replace it (in all of them: 256 x 12288, N = 16 takes 74 us, not 68; 64 x
+  // 8192, N = 65 114, not 78).
+  const bool still =
+      __builtin_amdgcn_ballot_w64(lane < chans && fabsf(delta) < 1e-35f) != 0;
 
   float *st = a.state + (slot * a.D + d0) * a.N;
   const float *Ad = a.A + d0 * a.N;
@@ -1048,6 +1055,15 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(StepArgs a, const T *__re
           }
         }
       }
+    }
+    if (still) {
+#pragma unroll
+      for (int j = 0; j < kU; ++j)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i)
+            A[j][k][i] = finite_rate(A[j][k][i]);
     }
 #pragma unroll
     for (int j = 0; j < kU; ++j) {

@@ -522,3 +522,32 @@ def test_infinite_states_outlast_a_segment(N):
             y, fin = run(c, split_hint=split)
             same_classes("y", y, ry, yt)
             same_classes("final state", fin, rf, ft)
+
+
+@pytest.mark.parametrize("softplus", [False, True])
+@pytest.mark.parametrize("N", [5, 16, 65, 67])
+def test_infinite_rates_of_a_step(N, softplus):
+    """A = -inf drops the state at every step but one of 0, which keeps it: as
+    in a prompt of one token, and as any very large rate."""
+    print("scan step infinite rates", N, softplus, flush=True)
+    c = case([1] * 4, 66, N, 1, F32, 360 + N, softplus=softplus, bias=False)
+    c["delta"][1] = -300.0 if softplus else 0.0  # (its softplus underflows)
+    c["delta"][2, ::2] = -300.0 if softplus else 0.0
+    c["A"][:, 3] = -1e30
+    c["A"][5] = -1e30
+    out = []
+    for rate in (-1e30, -float("inf")):
+        c["A"][:, 3] = rate
+        c["A"][5] = rate
+        state = on(c["s"]).clone()
+        y = kda.selective_scan_step(state, **args(c))
+        py, pfin = run(c)
+        out.append((y, state, py, pfin))
+    assert all(torch.isfinite(t).all() for t in out[0])
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+    assert torch.equal(out[1][1][1, 5], on(c["s"])[1, 5])  # a step of 0 keeps the state
+    c["A"][:, 3] = -1e30
+    c["A"][5] = -1e30
+    ry, yt, rf, ft = reference(c, 1.0)
+    ref.check("y", out[1][0], ry, yt)
+    ref.check("state", out[1][1], rf, ft)
