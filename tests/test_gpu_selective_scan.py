@@ -524,6 +524,61 @@ def test_infinite_states_outlast_a_segment(N):
             same_classes("final state", fin, rf, ft)
 
 
+def cut_of_row_kernel(c, D, N, G):
+    """Whether the call by itself runs the row kernel in segments: its
+    workspace holds 16 end states and a sum of steps for every segment pair
+    and channel (the lane kernel's N and one)."""
+    from gated_delta_rule_19_amd import _native as nat
+    cu = np.ascontiguousarray(c["cu"])
+    size = nat.load().kda_selective_scan_workspace_size(len(cu) - 1, cu.ctypes.data, D, N, G, 0)
+    pair = 256 * G * ((D // G + 63) // 64)
+    return size > 0 and size % (17 * pair) == 0 and size % ((N + 1) * pair) != 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N,G", [(5, 1), (5, 2), (13, 1), (13, 2), (12, 1)])
+def test_cut_row_kernel_of_few_states(N, G, dtype):
+    """A long prompt of few channels with states that do not fill 16 lanes."""
+    print("scan cut row kernel", N, G, dtype, flush=True)
+    c = case([3000], 66, N, G, dtype, 330 + N)
+    assert cut_of_row_kernel(c, 66, N, G)
+    compare(c, *run(c))
+    slow = case([3000], 66, N, G, dtype, 331 + N, slow=True, skip=False)
+    compare(slow, *run(slow))
+
+
+@pytest.mark.parametrize("what", ["x", "delta"])
+@pytest.mark.parametrize("N", [5, 12, 13])
+def test_infinite_inputs_of_the_cut_row_kernel(N, what):
+    """In the first segment, a middle one and the last."""
+    print("scan cut row kernel, infinite", N, what, flush=True)
+    for at in (17, 1500, 2990):
+        c = infinite([3000], N, 340 + N, False, what, at)
+        assert cut_of_row_kernel(c, 66, N, 1)
+        ry, yt, rf, ft = reference(c)
+        y, fin = run(c)
+        same_classes("y", y, ry, yt)
+        same_classes("final state", fin, rf, ft)
+
+
+@pytest.mark.parametrize("N", [5, 13])
+def test_nan_of_the_cut_row_kernel_stays_in_its_channel(N):
+    print("scan cut row kernel, NaN", N, flush=True)
+    c = case([3000], 66, N, 1, F32, 350 + N)
+    assert cut_of_row_kernel(c, 66, N, 1)
+    clean, cfin = run(c)
+    for at in (17, 1500, 2990):
+        d = dict(c, x=c["x"].clone())
+        d["x"][at, 5] = float("nan")
+        y, fin = run(d)
+        hit = torch.zeros_like(clean, dtype=torch.bool)
+        hit[at:, 5] = True
+        assert torch.isnan(y[hit]).all() and torch.equal(y[~hit], clean[~hit])
+        assert torch.isnan(fin[0, 5]).all()
+        fin[0, 5] = cfin[0, 5]
+        assert torch.equal(fin, cfin)
+
+
 @pytest.mark.parametrize("softplus", [False, True])
 @pytest.mark.parametrize("N", [5, 16, 65, 67])
 def test_infinite_rates_of_a_step(N, softplus):
