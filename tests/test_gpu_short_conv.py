@@ -227,3 +227,32 @@ def test_offsets_past_32_bits():
     y2 = kda.short_conv_step(last, xt, w)
     torch.cuda.synchronize()
     assert torch.equal(y, y2) and torch.equal(pool[-1:], last)
+
+
+@pytest.mark.parametrize("act", [None, "silu"])
+@pytest.mark.parametrize("dtype,D", [(F32, 7), (BF16, 13)])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+def test_infinities_go_where_the_formula_takes_them(value, dtype, D, act):
+    """An infinite input in a channel of a whole vector and in one of the
+    rest: each sum it enters is infinite with the sign of its weight; silu
+    keeps +inf and makes NaN (-inf * 0) of -inf.  A prompt and its steps."""
+    print("conv infinities", value, dtype, D, act, flush=True)
+    c = case([6, 8, 5], D, 4, dtype, 110, state=False, act=act)
+    c["w"] = torch.where(c["w"] == 0, torch.ones_like(c["w"]), c["w"])
+    clean, cfin = kda.short_conv(on(c["x"]), on(c["w"]), on(c["b"]), cu_seqlens=c["cu"], activation=act)
+    c["x"] = c["x"].clone()
+    for d in (2, D - 1):
+        c["x"][8, d] = value  # sequence 1, token 2
+    y, fin = kda.short_conv(on(c["x"]), on(c["w"]), on(c["b"]), cu_seqlens=c["cu"], activation=act)
+    torch.cuda.synchronize()
+    want = ref.f64(clean).copy()
+    for d in (2, D - 1):
+        for j in range(4):  # the input is the weight's of the token j later
+            s = np.sign(ref.f64(c["w"])[d, 3 - j]) * value
+            want[8 + j, d] = s if act is None or s > 0 else np.nan
+    assert np.array_equal(ref.f64(y), want, equal_nan=True)
+    assert np.array_equal(ref.f64(fin), ref.f64(cfin))
+    _, st = kda.short_conv(on(c["x"][6:8]), on(c["w"]), on(c["b"]), activation=act)
+    for t in range(8, 14):
+        y1 = kda.short_conv_step(st, on(c["x"][t:t + 1]), on(c["w"]), on(c["b"]), activation=act)
+        assert np.array_equal(ref.f64(y1)[0], want[t], equal_nan=True)
