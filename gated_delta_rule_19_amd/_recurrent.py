@@ -292,7 +292,11 @@ def _cache_args(state, codes, scales, src, dst, store):
     _dense(codes, codes.shape, codes.dtype, "codes")
     _dense(scales, codes.shape[:-1], torch.float32, "scales")
     n_from, n_to = (state.shape[0], codes.shape[0]) if store else (codes.shape[0], state.shape[0])
-    n = src.numel() if src is not None else dst.numel() if dst is not None else min(n_from, n_to)
+    n = state.shape[0]
+    if src is not None or dst is not None:
+        n = src.numel() if src is not None else dst.numel()
+    elif codes.shape[0] < n:
+        raise ValueError("codes hold %d slots for %d states" % (codes.shape[0], n))
     _slots(src, n, "src")
     _slots(dst, n, "dst")
     L = state.shape[-1]
@@ -310,8 +314,9 @@ def state_store(state, codes, scales, src=None, dst=None):
     state ``[items, ..., L]`` fp32, codes ``[slots, ..., L]`` int8 or
     float8_e4m3fn, scales ``[slots, ...]`` fp32 (one per row of L values).
     Item ``src[i]`` goes to slot ``dst[i]`` (int32 on the device; None: i);
-    pairs with an entry out of range are skipped.  Slots that are not named
-    keep what they hold."""
+    as many items move as the tables have entries, without tables all of
+    ``state``.  Pairs with an entry out of range are skipped.  Slots that are
+    not named keep what they hold."""
     n, R, L, fmt, n_from, n_to = _cache_args(state, codes, scales, src, dst, True)
     dev = _device(state, codes, scales, src, dst)
     _call("kda_state_store", dev, n, R, L, fmt, _p(state), _p(src), n_from, _p(codes),

@@ -314,6 +314,17 @@ def test_state_cache_binding_rejects(name, kw):
         kda.state_load(**a)
 
 
+@pytest.mark.parametrize("items", [4, 100])
+def test_state_cache_without_tables_moves_every_state_or_refuses(items):
+    """Fewer slots than states: no state may be dropped, or left unread."""
+    a = dict(state=z(items, 4, 8, dtype=f32), codes=z(3, 4, 8, dtype=torch.int8),
+             scales=z(3, 4, dtype=f32))
+    with pytest.raises(ValueError, match="3 slots"):
+        kda.state_store(**a)
+    with pytest.raises(ValueError, match="3 slots"):
+        kda.state_load(**a)
+
+
 # ---- the 64-bit forms -------------------------------------------------------------------
 
 def test_conv_form_is_a_correlation():
