@@ -38,29 +38,52 @@ bool good_rows(const void *p, int64_t stride, int64_t width, kda_dtype dt) {
   return p && aligned_elt(p, dt) && stride >= width && stride <= kMaxStride;
 }
 
-// Whether two row-strided matrices of `rows` rows share a byte.  Matrices
-// with one stride may interleave (column ranges of one buffer).
-bool rows_overlap(const void *a, int64_t a_stride, int64_t a_width, const void *b,
-                  int64_t b_stride, int64_t b_width, int64_t rows, int64_t es) {
-  if (!a || !b || rows <= 0)
+// What a call reads or writes, as byte ranges: `rows` rows of `width` bytes,
+// `pitch` bytes apart.  A dense buffer is one row.  Sizes that the arguments
+// merely name may pass 64 bits, so distances are kept in 128.
+typedef __int128 wide;
+struct Region {
+  const void *p;
+  wide rows, pitch, width;
+};
+Region rows_of(const void *p, int64_t rows, int64_t stride, int64_t width, int64_t es) {
+  return {p, rows, (wide)stride * es, (wide)width * es};
+}
+Region dense(const void *p, wide bytes) { return {p, 1, bytes, bytes}; }
+wide bytes_of(int64_t a, int64_t b, int64_t c, int64_t es) { return (wide)a * b * c * es; }
+
+// Whether two regions share a byte.  Matrices with one pitch may interleave
+// (column ranges of one buffer), and a dense buffer may lie between rows; two
+// matrices of different pitch are taken to meet where their extents do.
+bool overlap(const Region &a, const Region &b) {
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0)
     return false;
-  const uint8_t *pa = (const uint8_t *)a, *pb = (const uint8_t *)b;
-  const uint8_t *ea = pa + ((rows - 1) * a_stride + a_width) * es;
-  const uint8_t *eb = pb + ((rows - 1) * b_stride + b_width) * es;
-  if (ea <= pb || eb <= pa)
+  if (a.rows == 1 && b.rows > 1)
+    return overlap(b, a);
+  const wide at = (wide)(uintptr_t)b.p - (wide)(uintptr_t)a.p; // b's start in a
+  const wide a_end = (a.rows - 1) * a.pitch + a.width;
+  const wide end = at + (b.rows - 1) * b.pitch + b.width;
+  if (end <= 0 || at >= a_end)
     return false;
-  if (a_stride != b_stride)
+  if (a.rows == 1)
     return true;
-  const int64_t pitch = a_stride * es;
-  int64_t off = (pb - pa) % pitch; // b's column offset in a's rows
+  if (b.rows == 1) { // in a gap between two rows of a, or not
+    const wide lo = at > 0 ? at : 0, row = lo / a.pitch;
+    return lo - row * a.pitch < a.width || (row + 1) * a.pitch < end;
+  }
+  if (a.pitch != b.pitch)
+    return true;
+  wide off = at % a.pitch; // b's column offset in a's rows
   if (off < 0)
-    off += pitch;
-  return off < a_width * es || off + b_width * es > pitch;
+    off += a.pitch;
+  return off < a.width || off + b.width > a.pitch;
 }
 
-bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
-  const uint8_t *pa = (const uint8_t *)a, *pb = (const uint8_t *)b;
-  return a && b && a_bytes > 0 && b_bytes > 0 && pa < pb + b_bytes && pb < pa + a_bytes;
+template <size_t N> bool overlaps_any(const Region &out, const Region (&in)[N]) {
+  for (const Region &r : in)
+    if (overlap(out, r))
+      return true;
+  return false;
 }
 
 // Slot table: the state buffers' slice count against the batch's.
@@ -118,8 +141,9 @@ kda_status check_ssm_io(int64_t rows, int32_t D, int32_t N, int32_t G, kda_dtype
   if (!io->A || !aligned16(io->A) || !aligned16(io->D_skip) || !aligned16(io->delta_bias))
     return KDA_ERR_INVALID_ARG;
   const int64_t es = elt_size(dt);
+  const Region y = rows_of(io->y, rows, io->y_stride, D, es);
   const auto hits = [&](const void *p, int64_t stride, int64_t width) {
-    return rows_overlap(io->y, io->y_stride, D, p, stride, width, rows, es);
+    return overlap(y, rows_of(p, rows, stride, width, es));
   };
   if (hits(io->x, io->x_stride, D) || hits(io->delta, io->delta_stride, D) ||
       hits(io->B, io->B_stride, gn) || hits(io->C, io->C_stride, gn) ||
@@ -187,18 +211,26 @@ kda_status kda_short_conv(int32_t num_seqs, const int64_t *cu_seqlens_host, int3
   if (num_seqs == 0)
     return KDA_OK;
   const int64_t T = cu_seqlens_host[num_seqs], es = elt_size(dt);
-  if (T > 0 && (!good_rows(x, x_stride, D, dt) || !good_rows(y, y_stride, D, dt) ||
-                rows_overlap(x, x_stride, D, y, y_stride, D, T, es)))
+  if (T > 0 && (!good_rows(x, x_stride, D, dt) || !good_rows(y, y_stride, D, dt)))
     return KDA_ERR_INVALID_ARG;
   if (!weight || !aligned16(weight) || !aligned16(bias) || !aligned16(initial_state) ||
       !aligned16(final_state))
     return KDA_ERR_INVALID_ARG;
-  const int64_t bytes = (int64_t)num_slots * (W - 1) * D * es;
-  if (initial_state != final_state && overlap(initial_state, bytes, final_state, bytes))
+  const size_t need = seq_table_bytes(num_seqs);
+  const wide pool = bytes_of(num_slots, W - 1, D, es);
+  const Region in_x = rows_of(x, T, x_stride, D, es), out_y = rows_of(y, T, y_stride, D, es),
+               in_w = dense(weight, bytes_of(D, W, 1, es)), in_b = dense(bias, (wide)D * es),
+               init = dense(initial_state, pool), fin = dense(final_state, pool),
+               table = dense(slots, (wide)num_seqs * 4);
+  if (overlaps_any(out_y, {in_x, in_w, in_b, init, fin, table}) ||
+      overlaps_any(fin, {in_x, in_w, in_b, table}) ||
+      (initial_state != final_state && overlap(init, fin)))
     return KDA_ERR_INVALID_ARG;
-  st = check_workspace(seq_table_bytes(num_seqs), workspace, workspace_bytes);
+  st = check_workspace(need, workspace, workspace_bytes);
   if (st != KDA_OK)
     return st;
+  if (overlaps_any(dense(workspace, need), {in_x, out_y, in_w, in_b, init, fin, table}))
+    return KDA_ERR_INVALID_ARG;
   ConvCall c{};
   c.D = D;
   c.W = W;
@@ -231,8 +263,14 @@ kda_status kda_short_conv_step(int32_t N, int32_t D, int32_t W, kda_dtype dt, co
   if (!good_rows(x, x_stride, D, dt) || !good_rows(y, y_stride, D, dt) || !weight || !state ||
       !aligned16(weight) || !aligned16(bias) || !aligned16(state))
     return KDA_ERR_INVALID_ARG;
-  if (!(x == y && x_stride == y_stride) &&
-      rows_overlap(x, x_stride, D, y, y_stride, D, N, elt_size(dt)))
+  const int64_t es = elt_size(dt);
+  const Region in_x = rows_of(x, N, x_stride, D, es), out_y = rows_of(y, N, y_stride, D, es),
+               in_w = dense(weight, bytes_of(D, W, 1, es)), in_b = dense(bias, (wide)D * es),
+               pool = dense(state, bytes_of(num_slots, W - 1, D, es)),
+               table = dense(slots, (wide)N * 4);
+  if (overlaps_any(out_y, {in_w, in_b, pool, table}) ||
+      overlaps_any(pool, {in_x, in_w, in_b, table}) ||
+      (!(x == y && x_stride == y_stride) && overlap(out_y, in_x)))
     return KDA_ERR_INVALID_ARG;
   ConvCall c{};
   c.D = D;
@@ -281,8 +319,9 @@ kda_status kda_selective_scan(int32_t num_seqs, const int64_t *cu_seqlens_host, 
   }
   if (!aligned16(initial_state) || !aligned16(final_state))
     return KDA_ERR_INVALID_ARG;
-  const int64_t bytes = (int64_t)num_slots * D * N * (int64_t)sizeof(float);
-  if (initial_state != final_state && overlap(initial_state, bytes, final_state, bytes))
+  const wide bytes = bytes_of(num_slots, D, N, sizeof(float));
+  if (initial_state != final_state &&
+      overlap(dense(initial_state, bytes), dense(final_state, bytes)))
     return KDA_ERR_INVALID_ARG;
   const SsmPlan plan = ssm_plan(num_seqs, cu_seqlens_host, D, N, G, split_hint);
   st = check_workspace(plan.total, workspace, workspace_bytes);

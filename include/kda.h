@@ -490,6 +490,9 @@ kda_status kda_segment_scan(int32_t num_segs, int32_t H, int32_t dk, int32_t dv,
  *   then starts from zeros and its final state is not kept; a single-token
  *   row is skipped whole (its output row is left as it was).  Valid entries
  *   of one call must differ: two sequences that update one slice race.
+ * - What a call writes must not overlap anything else that it is given,
+ *   except where the call says so (KDA_ERR_INVALID_ARG).  Column ranges of
+ *   one buffer, and a dense array between rows, do not overlap.
  * - Every one of these calls may be captured into a HIP graph: sequence
  *   bounds travel in the recorded launches' argument blocks, not in a host
  *   buffer.  A call's workspace is its own until it has finished, replays
@@ -512,8 +515,7 @@ kda_status kda_segment_scan(int32_t num_segs, int32_t H, int32_t dk, int32_t dv,
  *   cu_seqlens_host : HOST, as for kda_chunk_prefill; each sequence shorter
  *                     than 2^30 tokens.
  *   D, W            : channels (>= 1), width (2 .. KDA_CONV_MAX_WIDTH).
- *   x, y            : [T, D] of type dt, row strides x_stride, y_stride;
- *                     y must not overlap x.
+ *   x, y            : [T, D] of type dt, row strides x_stride, y_stride.
  *   weight, bias    : [D, W], [D] (or NULL) of type dt.
  *   act             : KDA_ACT_NONE or KDA_ACT_SILU.
  *   initial_state, final_state : [num_slots, W - 1, D] of type dt, or NULL.

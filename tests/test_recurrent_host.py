@@ -216,6 +216,68 @@ def test_state_cache_of_no_items_is_a_no_op(lib):
     assert lib.kda_state_load(0, 8, 16, 1, None, None, None, 0, None, None, 0, None) == OK
 
 
+# ---- C ABI: what a call writes lies apart from everything else it is given ---------
+# (81 sequences and no workspace: a call whose arguments pass is then refused
+# for that, before anything is enqueued)
+
+CU80 = tuple(range(0, 160, 2)) + (160,)
+FAR = PTR + (1 << 28)
+
+
+@pytest.mark.parametrize("status,kw", [
+    (WORKSPACE, {}),
+    (INVALID, dict(w=PTR + (1 << 24) + 128)),                    # y on the weights
+    (INVALID, dict(w=PTR + (1 << 24) - 64 * 4 * 2 + 16)),        # their end
+    (WORKSPACE, dict(w=PTR + (1 << 24) - 64 * 4 * 2)),           # right in front of y
+    (WORKSPACE, dict(w=PTR + (1 << 24) + 160 * 64 * 2)),         # right behind it
+    (INVALID, dict(w=PTR + (1 << 24) + 160 * 64 * 2 - 16)),
+    (INVALID, dict(b=PTR + (1 << 24) + 256)),
+    (INVALID, dict(init=PTR + (1 << 24) + 256, num_slots=80)),
+    (INVALID, dict(fin=PTR + (1 << 24) - 80 * 3 * 64 * 2 + 16, num_slots=80)),
+    (WORKSPACE, dict(fin=PTR + (1 << 24) - 80 * 3 * 64 * 2, num_slots=80)),
+    (INVALID, dict(slots=PTR + (1 << 24) + 4)),
+    (INVALID, dict(fin=PTR + 256, num_slots=80)),                # final state on x
+    (INVALID, dict(init=PTR + 256, fin=PTR + 256, num_slots=80)),
+    (WORKSPACE, dict(init=PTR + 256, num_slots=80)),             # both only read
+    (INVALID, dict(fin=PTR + (1 << 20), num_slots=80)),          # on the weights
+    (INVALID, dict(b=FAR, fin=FAR, num_slots=80)),
+    (INVALID, dict(slots=FAR + 8, fin=FAR, num_slots=80)),
+    # rows of 64 columns in a buffer of 128: between them there is room for 128 bytes
+    (WORKSPACE, dict(xs=128, ys=128, b=PTR + (1 << 24) + 128)),
+    (WORKSPACE, dict(xs=128, ys=128, b=PTR + (1 << 24) + 256 * 159 - 128)),
+    (INVALID, dict(xs=128, ys=128, b=PTR + (1 << 24) + 128 - 16)),
+    (INVALID, dict(xs=128, ys=128, b=PTR + (1 << 24) + 128 + 16)),
+    (WORKSPACE, dict(xs=128, ys=128, b=PTR + (1 << 24) + 256 * 159 + 128)),
+    (INVALID, dict(b=FAR, ws=FAR, wsb=1 << 20)),                 # workspace on the bias
+    (INVALID, dict(ws=PTR + (1 << 24), wsb=1 << 20)),            # workspace on y
+    (INVALID, dict(ws=PTR, wsb=1 << 20)),                        # on x
+    (INVALID, dict(ws=PTR + (1 << 20), wsb=1 << 20)),            # on the weights
+    (INVALID, dict(ws=FAR, wsb=1 << 20, init=FAR, num_slots=80)),
+    (INVALID, dict(ws=FAR, wsb=1 << 20, fin=FAR, num_slots=80)),
+    # sizes that pass 64 bits: a pool's, and the distance of the last rows
+    (INVALID, dict(cu=(0,) * 81, D=(1 << 31) - 1, fin=FAR, num_slots=(1 << 31) - 1, b=FAR + (1 << 40))),
+    (INVALID, dict(cu=tuple(i * ((1 << 30) - 1) for i in range(1024)), num_slots=1023, dt=F32,
+                   xs=1 << 22, ys=(1 << 22) - 1)),
+])
+def test_short_conv_refuses_overlaps(lib, status, kw):
+    a = dict(cu=CU80, num_slots=80)
+    a.update(kw)
+    assert conv(lib, **a) == status
+
+
+@pytest.mark.parametrize("kw", [
+    dict(y=PTR + (1 << 20)), dict(y=FAR + 64), dict(bias=PTR + (1 << 24)),
+    dict(slots=PTR + (1 << 24)), dict(x=FAR + 128), dict(weight=FAR), dict(bias=FAR + 16),
+    dict(slots=FAR + 4), dict(x=FAR, y=FAR),
+    dict(state=PTR + (1 << 24) - 3 * 3 * 64 * 2 + 16), dict(y=PTR, x=PTR, bias=PTR + 64),
+])
+def test_short_conv_step_refuses_overlaps(lib, kw):
+    a = dict(N=3, D=64, W=4, dt=BF16, x=PTR, xs=64, weight=PTR + (1 << 20), bias=None, act=0,
+             state=FAR, slots=None, num_slots=3, y=PTR + (1 << 24), ys=64, stream=None)
+    a.update(kw)
+    assert lib.kda_short_conv_step(*a.values()) == INVALID
+
+
 # ---- binding ---------------------------------------------------------------------------
 
 bf, f32 = torch.bfloat16, torch.float32
