@@ -129,25 +129,34 @@ kda_status check_ssm(int32_t D, int32_t N, int32_t G, kda_dtype dt, const kda_ss
   return KDA_OK;
 }
 
-// The matrices and parameters of a scan over `rows` >= 1 tokens.
+// What a scan reads beside its initial state, and its y.
+constexpr size_t kScanInputs = 9;
+struct ScanRegions {
+  Region in[kScanInputs], y;
+};
+ScanRegions scan_regions(int64_t rows, int32_t D, int32_t N, int32_t G, kda_dtype dt,
+                         const kda_ssm_io *io, const int32_t *slots, int32_t count) {
+  const int64_t gn = (int64_t)G * N, es = elt_size(dt);
+  return {{rows_of(io->x, rows, io->x_stride, D, es),
+           rows_of(io->delta, rows, io->delta_stride, D, es),
+           rows_of(io->B, rows, io->B_stride, gn, es), rows_of(io->C, rows, io->C_stride, gn, es),
+           rows_of(io->z, rows, io->z_stride, D, es), dense(io->A, bytes_of(D, N, 1, 4)),
+           dense(io->D_skip, (wide)D * 4), dense(io->delta_bias, (wide)D * 4),
+           dense(slots, (wide)count * 4)},
+          rows_of(io->y, rows, io->y_stride, D, es)};
+}
+
+// The matrices and parameters of a scan over `rows` tokens.
 kda_status check_ssm_io(int64_t rows, int32_t D, int32_t N, int32_t G, kda_dtype dt,
                         const kda_ssm_io *io) {
   const int64_t gn = (int64_t)G * N;
-  if (!good_rows(io->x, io->x_stride, D, dt) || !good_rows(io->delta, io->delta_stride, D, dt) ||
-      !good_rows(io->B, io->B_stride, gn, dt) || !good_rows(io->C, io->C_stride, gn, dt) ||
-      !good_rows(io->y, io->y_stride, D, dt) ||
-      (io->z && !good_rows(io->z, io->z_stride, D, dt)))
+  if (rows > 0 &&
+      (!good_rows(io->x, io->x_stride, D, dt) || !good_rows(io->delta, io->delta_stride, D, dt) ||
+       !good_rows(io->B, io->B_stride, gn, dt) || !good_rows(io->C, io->C_stride, gn, dt) ||
+       !good_rows(io->y, io->y_stride, D, dt) ||
+       (io->z && !good_rows(io->z, io->z_stride, D, dt))))
     return KDA_ERR_INVALID_ARG;
   if (!io->A || !aligned16(io->A) || !aligned16(io->D_skip) || !aligned16(io->delta_bias))
-    return KDA_ERR_INVALID_ARG;
-  const int64_t es = elt_size(dt);
-  const Region y = rows_of(io->y, rows, io->y_stride, D, es);
-  const auto hits = [&](const void *p, int64_t stride, int64_t width) {
-    return overlap(y, rows_of(p, rows, stride, width, es));
-  };
-  if (hits(io->x, io->x_stride, D) || hits(io->delta, io->delta_stride, D) ||
-      hits(io->B, io->B_stride, gn) || hits(io->C, io->C_stride, gn) ||
-      hits(io->z, io->z_stride, D))
     return KDA_ERR_INVALID_ARG;
   return KDA_OK;
 }
@@ -310,23 +319,24 @@ kda_status kda_selective_scan(int32_t num_seqs, const int64_t *cu_seqlens_host, 
   if (num_seqs == 0)
     return KDA_OK;
   const int64_t T = cu_seqlens_host[num_seqs];
-  if (T > 0) {
-    st = check_ssm_io(T, D, N, G, dt, io);
-    if (st != KDA_OK)
-      return st;
-  } else if (!io->A || !aligned16(io->A)) {
-    return KDA_ERR_INVALID_ARG;
-  }
+  st = check_ssm_io(T, D, N, G, dt, io);
+  if (st != KDA_OK)
+    return st;
   if (!aligned16(initial_state) || !aligned16(final_state))
     return KDA_ERR_INVALID_ARG;
-  const wide bytes = bytes_of(num_slots, D, N, sizeof(float));
-  if (initial_state != final_state &&
-      overlap(dense(initial_state, bytes), dense(final_state, bytes)))
+  const ScanRegions r = scan_regions(T, D, N, G, dt, io, slots, num_seqs);
+  const wide pool = bytes_of(num_slots, D, N, sizeof(float));
+  const Region init = dense(initial_state, pool), fin = dense(final_state, pool);
+  if (overlaps_any(r.y, r.in) || overlaps_any(fin, r.in) || overlaps_any(r.y, {init, fin}) ||
+      (initial_state != final_state && overlap(init, fin)))
     return KDA_ERR_INVALID_ARG;
   const SsmPlan plan = ssm_plan(num_seqs, cu_seqlens_host, D, N, G, split_hint);
   st = check_workspace(plan.total, workspace, workspace_bytes);
   if (st != KDA_OK)
     return st;
+  const Region ws = dense(workspace, plan.total);
+  if (overlaps_any(ws, r.in) || overlaps_any(ws, {r.y, init, fin}))
+    return KDA_ERR_INVALID_ARG;
   SsmCall c = ssm_call(D, N, G, io);
   c.init = initial_state;
   c.fin = final_state;
@@ -350,6 +360,10 @@ kda_status kda_selective_scan_step(int32_t rows, int32_t D, int32_t N, int32_t G
   if (st != KDA_OK)
     return st;
   if (!state || !aligned16(state))
+    return KDA_ERR_INVALID_ARG;
+  const ScanRegions r = scan_regions(rows, D, N, G, dt, io, slots, rows);
+  const Region pool = dense(state, bytes_of(num_slots, D, N, sizeof(float)));
+  if (overlaps_any(r.y, r.in) || overlaps_any(pool, r.in) || overlap(r.y, pool))
     return KDA_ERR_INVALID_ARG;
   SsmCall c = ssm_call(D, N, G, io);
   c.fin = state;

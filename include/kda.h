@@ -559,10 +559,9 @@ kda_status kda_short_conv_step(int32_t N, int32_t D, int32_t W, kda_dtype dt, co
  *                (rows of G * N) of type dt with their row strides, and the
  *                fp32 parameters A [D, N], D_skip [D], delta_bias [D].  z,
  *                D_skip and delta_bias may be NULL: no gate, no skip, no
- *                bias.  y must not overlap the inputs.
- *                An infinite rate A counts as the largest finite one: a step
- *                delta of 0 keeps its state.  A step's decay is an fp32
- *                number: below 2^-126 it is 0.
+ *                bias.  An infinite rate A counts as the largest finite
+ *                one: a step delta of 0 keeps its state.  A step's decay is
+ *                an fp32 number: below 2^-126 it is 0.
  *   initial_state, final_state : [num_slots, D, N] fp32, or NULL (zeros /
  *                not written).  final_state == initial_state is allowed;
  *                other overlaps are not.

@@ -278,6 +278,64 @@ def test_short_conv_step_refuses_overlaps(lib, kw):
     assert lib.kda_short_conv_step(*a.values()) == INVALID
 
 
+# (a cut of 7 pairs and no workspace: refused for that where the arguments pass)
+POOL, WS, Y = PTR + (7 << 24), PTR + (8 << 24), PTR + (4 << 24)
+
+
+@pytest.mark.parametrize("status,io,kw", [
+    (WORKSPACE, {}, {}),
+    (INVALID, dict(A=Y + 64), {}),
+    (WORKSPACE, dict(A=Y + 4096 * 64 * 2), {}),
+    (INVALID, dict(A=Y - 64 * 16 * 4 + 16), {}),
+    (WORKSPACE, dict(A=Y - 64 * 16 * 4), {}),
+    (INVALID, dict(D_skip=Y + 4096 * 64 * 2 - 16), {}),
+    (INVALID, dict(delta_bias=Y), {}),
+    (INVALID, dict(y_stride=128, delta_bias=Y + 128), {}),       # 256 bytes in a gap of 128
+    (WORKSPACE, dict(y_stride=192, delta_bias=Y + 128), {}),     # in one of 256
+    (INVALID, {}, dict(init=Y)),
+    (INVALID, {}, dict(fin=Y + 4096 * 64 * 2 - 16)),
+    (WORKSPACE, {}, dict(fin=Y + 4096 * 64 * 2)),
+    (INVALID, {}, dict(slots=Y + 8)),
+    (WORKSPACE, {}, dict(init=PTR)),                             # both only read
+    (INVALID, {}, dict(fin=PTR)),                                # final state on x
+    (INVALID, {}, dict(fin=PTR + (1 << 24))),                    # delta
+    (INVALID, {}, dict(fin=PTR + (2 << 24))),                    # B
+    (INVALID, {}, dict(fin=PTR + (3 << 24))),                    # C
+    (INVALID, dict(z=POOL, z_stride=64), dict(fin=POOL)),
+    (INVALID, {}, dict(fin=PTR + (5 << 24))),                    # A
+    (INVALID, dict(D_skip=POOL + 16), dict(fin=POOL)),
+    (INVALID, dict(delta_bias=POOL + 64), dict(init=POOL, fin=POOL)),
+    (INVALID, {}, dict(slots=POOL + 4, fin=POOL)),
+    (INVALID, {}, dict(ws=Y, wsb=1 << 24)),
+    (INVALID, {}, dict(ws=PTR, wsb=1 << 24)),
+    (INVALID, {}, dict(ws=PTR + (2 << 24), wsb=1 << 24)),
+    (INVALID, {}, dict(ws=PTR + (5 << 24), wsb=1 << 24)),
+    (INVALID, {}, dict(ws=POOL, wsb=1 << 24, init=POOL)),
+    (INVALID, {}, dict(ws=POOL, wsb=1 << 24, fin=POOL)),
+])
+def test_selective_scan_refuses_overlaps(lib, status, io, kw):
+    a = dict(init=None, fin=None, slots=None, ws=None, wsb=0)
+    a.update(kw)
+    keep, p = cu_ptr(0, 4096)
+    blk = ssm_io(**io)
+    assert lib.kda_selective_scan(1, p, 64, 16, 1, BF16, ctypes.byref(blk), a["init"], a["fin"],
+                                  a["slots"], 1, 8, a["ws"], a["wsb"], None) == status
+
+
+@pytest.mark.parametrize("io,kw", [
+    (dict(A=Y), {}), (dict(D_skip=Y + 16), {}), (dict(delta_bias=Y), {}), ({}, dict(state=Y)),
+    ({}, dict(slots=Y)), (dict(x=POOL), {}), (dict(delta=POOL + 64), {}), (dict(B=POOL), {}),
+    (dict(C=POOL), {}), (dict(z=POOL, z_stride=64), {}), (dict(A=POOL), {}),
+    (dict(D_skip=POOL), {}), (dict(delta_bias=POOL), {}), ({}, dict(slots=POOL)),
+])
+def test_selective_scan_step_refuses_overlaps(lib, io, kw):
+    a = dict(state=POOL, slots=None)
+    a.update(kw)
+    blk = ssm_io(**io)
+    assert lib.kda_selective_scan_step(3, 64, 16, 1, BF16, ctypes.byref(blk), a["state"],
+                                       a["slots"], 3, None) == INVALID
+
+
 # ---- binding ---------------------------------------------------------------------------
 
 bf, f32 = torch.bfloat16, torch.float32
