@@ -382,6 +382,13 @@ kda_status kda_state_store(int32_t n, int64_t R, int32_t L, int32_t format, cons
     return KDA_OK;
   if (!state || !codes || !scales || !aligned4(state) || !aligned4(scales))
     return KDA_ERR_INVALID_ARG;
+  const Region st_r = dense(state, bytes_of(num_src, R, L, sizeof(float))),
+               codes_r = dense(codes, bytes_of(num_dst, R, L, 1)),
+               scales_r = dense(scales, bytes_of(num_dst, R, 1, sizeof(float))),
+               src_r = dense(src, (wide)n * 4), dst_r = dense(dst, (wide)n * 4);
+  if (overlaps_any(codes_r, {st_r, scales_r, src_r, dst_r}) ||
+      overlaps_any(scales_r, {st_r, src_r, dst_r}))
+    return KDA_ERR_INVALID_ARG;
   CacheCall c{};
   c.n = n;
   c.R = R;
@@ -406,6 +413,12 @@ kda_status kda_state_load(int32_t n, int64_t R, int32_t L, int32_t format, const
   if (n == 0)
     return KDA_OK;
   if (!state || !codes || !scales || !aligned4(state) || !aligned4(scales))
+    return KDA_ERR_INVALID_ARG;
+  const Region st_r = dense(state, bytes_of(num_dst, R, L, sizeof(float))),
+               codes_r = dense(codes, bytes_of(num_src, R, L, 1)),
+               scales_r = dense(scales, bytes_of(num_src, R, 1, sizeof(float))),
+               src_r = dense(src, (wide)n * 4), dst_r = dense(dst, (wide)n * 4);
+  if (overlaps_any(st_r, {codes_r, scales_r, src_r, dst_r}))
     return KDA_ERR_INVALID_ARG;
   CacheCall c{};
   c.n = n;

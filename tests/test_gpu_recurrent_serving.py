@@ -268,3 +268,47 @@ def test_two_streams_at_once():
     for i, got in enumerate(both):
         for a, b in zip(got, alone[i % 2]):
             assert torch.equal(a, b)
+
+
+def test_arrays_side_by_side_in_one_buffer():
+    """States, outputs and parameters that touch without overlapping are
+    accepted, and each call writes its own only."""
+    print("side by side", flush=True)
+    D, N, W, rows = 64, 16, 4, 5
+    m = Mixer(D, N, 1, W, F32, 120)
+    p = f(gen(121), rows, m.width)
+    x, z, dl, B, C = m.parts(p)
+    sizes = dict(conv=rows * 3 * D, xc=rows * D, ssm=rows * D * N, y=rows * D, A=D * N, skip=D,
+                 bias=D, w=D * W, b=D, back=rows * D * N, scales=rows * D, codes=rows * D * N // 4)
+    arena = torch.full((sum(sizes.values()),), 7.0, device=DEV)
+    v, at = {}, 0
+    for k, n in sizes.items():
+        v[k] = arena[at:at + n]
+        at += n
+    shape = dict(conv=(rows, 3, D), xc=(rows, D), ssm=(rows, D, N), y=(rows, D), A=(D, N), w=(D, W),
+                 back=(rows, D, N), scales=(rows, D))
+    v = {k: t.view(shape[k]) if k in shape else t for k, t in v.items()}
+    codes = v["codes"].view(torch.int8).view(rows, D, N)
+    for k, t in (("A", m.A), ("skip", m.skip), ("bias", m.bias), ("w", m.w), ("b", m.b)):
+        v[k].copy_(t)
+    c0, s0 = f(gen(122), rows, 3, D), f(gen(123), rows, D, N)
+    v["conv"].copy_(c0)
+    v["ssm"].copy_(s0)
+    want = m.step(p, c0, s0, None)
+    kda.short_conv_step(v["conv"], x, v["w"], v["b"], y=v["xc"])
+    y = kda.selective_scan_step(v["ssm"], v["xc"], dl, v["A"], B, C, D=v["skip"], z=z,
+                                delta_bias=v["bias"], y=v["y"])
+    kda.state_store(v["ssm"], codes, v["scales"])
+    kda.state_load(codes, v["scales"], v["back"])
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(v["conv"], c0) and torch.equal(v["ssm"], s0)
+    assert torch.equal(v["A"], m.A) and torch.equal(v["bias"], m.bias) and torch.equal(v["w"], m.w)
+    qc, qs = ref.quantise(s0.cpu(), torch.int8)
+    assert torch.equal(codes.cpu(), qc) and torch.equal(v["scales"].cpu(), qs)
+    assert torch.equal(v["back"].cpu(), qc.float() * qs[..., None])
+    kda.short_conv(x, v["w"], v["b"], initial_state=v["conv"][:1], final_state=v["conv"][:1], y=v["xc"])
+    kda.selective_scan(v["xc"], dl, v["A"], B, C, D=v["skip"], delta_bias=v["bias"],
+                       initial_state=v["ssm"][:1], final_state=v["ssm"][:1], y=v["y"])
+    torch.cuda.synchronize()
+    assert torch.equal(v["conv"][1:], c0[1:]) and torch.equal(v["ssm"][1:], s0[1:])
+    assert torch.equal(v["A"], m.A) and torch.equal(v["bias"], m.bias) and torch.equal(v["w"], m.w)

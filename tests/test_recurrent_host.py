@@ -278,6 +278,31 @@ def test_short_conv_step_refuses_overlaps(lib, kw):
     assert lib.kda_short_conv_step(*a.values()) == INVALID
 
 
+@pytest.mark.parametrize("store,load,kw", [
+    (INVALID, INVALID, dict(c=PTR + 2 * 8 * 16 * 4 - 1)),            # codes on the states' end
+    (INVALID, INVALID, dict(a=PTR + (1 << 24) + 2 * 8 * 16 - 4)),    # states on the codes' end
+    (INVALID, INVALID, dict(sc=PTR + 64)),                           # scales on the states
+    (INVALID, None, dict(sc=PTR + (1 << 24) + 128)),                 # scales on the codes
+    (INVALID, None, dict(sc=PTR + (1 << 24) - 60)),
+    (INVALID, None, dict(src=PTR + (1 << 24))),                      # tables on what is written
+    (INVALID, None, dict(dst=PTR + (2 << 24) + 60)),
+    (None, INVALID, dict(src=PTR + 4)),
+    (None, INVALID, dict(dst=PTR)),
+    (INVALID, INVALID, dict(num_a=(1 << 31) - 1, num_b=(1 << 31) - 1, R=1 << 31, n=0x7fffffff,
+                            L=256)),
+])
+def test_state_cache_refuses_overlaps(lib, store, load, kw):
+    a = dict(n=2, R=8, L=16, format=0, a=PTR, src=None, num_a=2, c=PTR + (1 << 24),
+             sc=PTR + (2 << 24), dst=None, num_b=2)
+    a.update(kw)
+    if store is not None:
+        assert lib.kda_state_store(a["n"], a["R"], a["L"], a["format"], a["a"], a["src"],
+                                   a["num_a"], a["c"], a["sc"], a["dst"], a["num_b"], None) == store
+    if load is not None:
+        assert lib.kda_state_load(a["n"], a["R"], a["L"], a["format"], a["c"], a["sc"], a["src"],
+                                  a["num_b"], a["a"], a["dst"], a["num_a"], None) == load
+
+
 # (a cut of 7 pairs and no workspace: refused for that where the arguments pass)
 POOL, WS, Y = PTR + (7 << 24), PTR + (8 << 24), PTR + (4 << 24)
 
