@@ -191,7 +191,8 @@ template <int CTRL> __device__ __forceinline__ float quad_swap(float x) {
 // 0 go on with the lower token of a pair, the others with the upper one, each
 // adding its partner's share.  The first two steps write their two halves by
 // DPP bank masks (4 lanes a bank).  (s_nop 1: a DPP operand must be two
-// instructions old, which the compiler does not see inside or around asm.)
+// instructions old, which the compiler does not see inside or around asm.
+// "+&v": the sums are written before the last operand is read.)
 __device__ __forceinline__ float row_reduce16(float (&p)[16], int lane) {
   asm volatile(
       "s_nop 1\n\t"
@@ -221,8 +222,8 @@ __device__ __forceinline__ float row_reduce16(float (&p)[16], int lane) {
       "v_add_f32_dpp %2, %6, %6 row_shr:4 row_mask:0xf bank_mask:0xa\n\t"
       "v_add_f32_dpp %3, %7, %7 row_shr:4 row_mask:0xf bank_mask:0xa\n\t"
       "s_nop 1"
-      : "+v"(p[0]), "+v"(p[1]), "+v"(p[2]), "+v"(p[3]), "+v"(p[4]), "+v"(p[5]), "+v"(p[6]),
-        "+v"(p[7])
+      : "+&v"(p[0]), "+&v"(p[1]), "+&v"(p[2]), "+&v"(p[3]), "+&v"(p[4]), "+&v"(p[5]), "+&v"(p[6]),
+        "+&v"(p[7])
       : "v"(p[8]), "v"(p[9]), "v"(p[10]), "v"(p[11]), "v"(p[12]), "v"(p[13]), "v"(p[14]),
         "v"(p[15]));
   const bool b1 = lane & 2, b0 = lane & 1;
