@@ -81,10 +81,6 @@ template <typename T, int VEC> __device__ __forceinline__ void store_f32(T *p, c
   }
 }
 
-__device__ __forceinline__ float silu(float x) {
-  return x * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-x * 1.4426950408889634f));
-}
-
 // Weights [D, W] and bias of a lane's VEC channels.
 template <typename T, int VEC, int W> struct Taps {
   float w[W][VEC], b[VEC];
@@ -139,7 +135,6 @@ struct ConvArgs {
   int32_t full;       // lanes with VEC channels; the D % VEC others have a lane each
   int32_t act;        // 1: silu
   int32_t num_slots;
-  int32_t rows;       // step: rows
   int64_t xs, ys;     // row strides
   int64_t waves;      // all waves with work
   const int32_t *slots;
@@ -377,7 +372,6 @@ hipError_t launch_conv(int elt, const ConvCall &c, int32_t num_seqs, const int64
 hipError_t launch_conv_step(int elt, const ConvCall &c, int32_t rows, hipStream_t s) {
   const int vec = elt == 1 ? 8 : 4;
   ConvArgs a = conv_args(c, vec);
-  a.rows = rows;
   a.waves = (int64_t)rows * a.cw;
   if ((a.waves + 3) / 4 * 256 > UINT32_MAX)
     return hipErrorInvalidConfiguration;

@@ -11,6 +11,12 @@
 
 namespace kda {
 
+// x sigmoid(x) with the hardware's exponential and reciprocal: the activation
+// of the convolution and the gate of the scan.  -inf gives NaN (-inf * 0).
+__device__ __forceinline__ float silu(float x) {
+  return x * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-x * 1.4426950408889634f));
+}
+
 // Short convolution, prompts and single tokens.  Strides in elements.
 struct ConvCall {
   int32_t D, W, act, num_slots;

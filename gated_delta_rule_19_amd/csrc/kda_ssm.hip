@@ -62,10 +62,6 @@ __device__ __forceinline__ float softplus(float x) {
   return fmaf(s + s, p, fmaxf(x, 0.f));
 }
 
-__device__ __forceinline__ float silu(float x) {
-  return x * __builtin_amdgcn_rcpf(1.f + exp2_hw(-x * kLog2e));
-}
-
 // A in log2 units.  An infinite A is taken as the largest finite one, by
 // prompts and single tokens alike: its decay is the same, and a step of 0
 // (which the prompt kernels take past a segment's end) leaves the state as it
