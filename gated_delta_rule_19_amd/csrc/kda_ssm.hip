@@ -911,7 +911,9 @@ __global__ __launch_bounds__(64 * kFoldWaves) void ssm_fold_kernel(SeqTable tab,
 // evaluated there), B and C once a wave; the states pass in chunks of 64 / W
 // channels, W lanes a channel with VEC states on each (K times), which get
 // their channel's delta and delta x from its lane and give their sum back to
-// it.
+// it.  256 rows x 12288 bf16, N = 16: 69 to 74 us, 5.6 to 6.0 TB/s.  Where N
+// is no multiple of 4 a lane takes one state at a time: N = 13 83 us (3.9
+// TB/s), N = 5 40 us (3.1).
 struct StepArgs {
   int32_t D, N, G, Dg, cb, rows, softplus, num_slots, wlog, bcvec;
   int64_t xs, dls, zs, ys, Bs, Cs;
@@ -1154,6 +1156,17 @@ int64_t ssm_num_segments(int64_t len, const SsmPlan &p) {
 // 1536: row 4500, lane cut 1320.  4096 x 1536: row 139, row cut 66, lane cut
 // 92.  64 sequences of 16 tokens x 8192: row 189, lane 81.  128 sequences of
 // 64 x 12288: row 742, lane 513.
+// Other N scale these times by their share of the instructions; that was not
+// fitted, but measured on both sides for N = 1 .. 128 (bf16, gate; and fp32 for
+// N = 5 and 8) at 8192 x 8192, 4096 x 1536, 65536 x 1024, 16 sequences of 1024
+// x 2048 and 64 of 128 x 4096.  8192 x 8192, N = 1, 4, 5, 8, 13: row 458, 406,
+// 430, 401, 441, lane cut 234, 247, 273, 315, 481; 65536 x 1024: row cut 604,
+// 599, 615, 611, 633, lane cut 238, 270, 306, 347, 478.  The choice is the
+// faster side, or within a tenth of it, at all but one: 16 sequences of 1024 x
+// 2048 with N = 1 .. 5 run uncut on the lane kernel in 235 .. 300, where the
+// row kernel takes 173 .. 183 and the cut lane kernel 127 .. 178.  (A lane
+// wave alone takes some 0.20 + 0.0125 N us a token, of which the model below
+// leaves out the part without N.)
 SsmPlan ssm_plan(int32_t num_seqs, const int64_t *cu, int32_t D, int32_t N, int32_t G,
                  int32_t split_hint) {
   SsmPlan p{};

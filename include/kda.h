@@ -517,7 +517,8 @@ kda_status kda_segment_scan(int32_t num_segs, int32_t H, int32_t dk, int32_t dv,
  *   D, W            : channels (>= 1), width (2 .. KDA_CONV_MAX_WIDTH).
  *   x, y            : [T, D] of type dt, row strides x_stride, y_stride.
  *   weight, bias    : [D, W], [D] (or NULL) of type dt.
- *   act             : KDA_ACT_NONE or KDA_ACT_SILU.
+ *   act             : KDA_ACT_NONE or KDA_ACT_SILU (s * sigmoid(s), NaN at
+ *                     -inf).
  *   initial_state, final_state : [num_slots, W - 1, D] of type dt, or NULL.
  *                     The final state of a sequence is its last W - 1 inputs
  *                     (with rows of its initial state in front when it is
