@@ -73,6 +73,13 @@ def _device(first, *ts):
     return first.device
 
 
+def _count(n, name):
+    """A count that the library takes in 32 bits (ctypes would wrap it)."""
+    if n > 0x7fffffff:
+        raise ValueError("%s must be below 2^31 (got %d)" % (name, n))
+    return n
+
+
 def _like(x):
     """A dense output of x's shape, type and device."""
     return torch.empty_like(x) if x.is_contiguous() else \
@@ -115,7 +122,7 @@ def _pools(initial, final, count, slots, tail, dtype):
         _dense(t, (num,) + tail, dtype, name)
     if initial is not None and final is not None and initial.shape != final.shape:
         raise ValueError("initial_state and final_state must have one shape")
-    return num
+    return _count(num, "the number of state slices")
 
 
 def _bounds(cu_seqlens, T):
@@ -187,7 +194,9 @@ def short_conv_step(state, x, weight, bias=None, activation="silu", slots=None, 
     _dense(bias, (D,), dt, "bias")
     act = _act(activation)
     _slots(slots, N)
-    pool = N if slots is None else state.shape[0]
+    pool = _count(N, "the number of rows")
+    if slots is not None:
+        pool = _count(state.shape[0], "the number of state slices")
     _dense(state, (pool, W - 1, D), dt, "state")
     ys = D if y is None else _rows(y, (N, D), dt, "y")
     dev = _device(x, weight, bias, state, slots, y)
@@ -243,6 +252,7 @@ def selective_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None,
     io, T, ch, N, G, code = _ssm_io(x, delta, A, B, C, D, z, delta_bias, delta_softplus, y)
     cu = _bounds(cu_seqlens, T)
     n = cu.size - 1
+    split = _count(int(split_hint), "split_hint")
     _slots(slots, n)
     pool = _pools(initial_state, final_state, n, slots, (ch, N), torch.float32)
     dev = _device(x, delta, A, B, C, D, z, delta_bias, initial_state, final_state, slots, y,
@@ -254,7 +264,6 @@ def selective_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None,
         final_state = torch.empty((n, ch, N), dtype=torch.float32, device=dev)
     lib = load()
     cup = cu.ctypes.data
-    split = int(split_hint)
     ws = _workspace(workspace, lib.kda_selective_scan_workspace_size(n, cup, ch, N, G, split), dev)
     _call("kda_selective_scan", dev, n, cup, ch, N, G, code, ctypes.byref(io), _p(initial_state),
           _p(final_state), _p(slots), pool, split, _p(ws),
@@ -271,7 +280,9 @@ def selective_scan_step(state, x, delta, A, B, C, D=None, z=None, delta_bias=Non
     Returns y."""
     io, rows, ch, N, G, code = _ssm_io(x, delta, A, B, C, D, z, delta_bias, delta_softplus, y)
     _slots(slots, rows)
-    pool = rows if slots is None else state.shape[0]
+    pool = _count(rows, "the number of rows")
+    if slots is not None:
+        pool = _count(state.shape[0], "the number of state slices")
     _dense(state, (pool, ch, N), torch.float32, "state")
     dev = _device(x, delta, A, B, C, D, z, delta_bias, state, slots, y)
     if y is None:
@@ -291,15 +302,17 @@ def _cache_args(state, codes, scales, src, dst, store):
     _dense(state, state.shape, torch.float32, "state")
     _dense(codes, codes.shape, codes.dtype, "codes")
     _dense(scales, codes.shape[:-1], torch.float32, "scales")
-    n_from, n_to = (state.shape[0], codes.shape[0]) if store else (codes.shape[0], state.shape[0])
-    n = state.shape[0]
+    items = _count(state.shape[0], "the number of states")
+    held = _count(codes.shape[0], "the number of slots")
+    n_from, n_to = (items, held) if store else (held, items)
+    n = items
     if src is not None or dst is not None:
-        n = src.numel() if src is not None else dst.numel()
-    elif codes.shape[0] < n:
-        raise ValueError("codes hold %d slots for %d states" % (codes.shape[0], n))
+        n = _count(src.numel() if src is not None else dst.numel(), "the number of entries")
+    elif held < n:
+        raise ValueError("codes hold %d slots for %d states" % (held, n))
     _slots(src, n, "src")
     _slots(dst, n, "dst")
-    L = state.shape[-1]
+    L = _count(state.shape[-1], "the row length")
     R = 1
     for v in state.shape[1:-1]:
         R *= v

@@ -470,6 +470,40 @@ def test_state_cache_without_tables_moves_every_state_or_refuses(items):
         kda.state_load(**a)
 
 
+def far(*shape, dtype=bf):
+    """A shape without memory."""
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+@pytest.mark.parametrize("call", [
+    lambda n: kda.state_store(far(n, 1, dtype=f32), far(n, 1, dtype=torch.int8), far(n, dtype=f32)),
+    lambda n: kda.state_load(far(n, 1, dtype=torch.int8), far(n, dtype=f32), far(n, 1, dtype=f32)),
+    lambda n: kda.state_store(far(1, n, dtype=f32), far(1, n, dtype=torch.int8), far(1, dtype=f32)),
+    lambda n: kda.state_store(far(4, 1, dtype=f32), far(n, 1, dtype=torch.int8), far(n, dtype=f32),
+                              dst=far(4, dtype=torch.int32)),
+    lambda n: kda.short_conv_step(far(n, 1, 1), far(n, 1), far(1, 2)),
+    lambda n: kda.short_conv_step(far(n, 1, 1), far(3, 1), far(1, 2), slots=far(3, dtype=torch.int32)),
+    lambda n: kda.short_conv_step(far(3, 1, 1), far(n, 1), far(1, 2), slots=far(n, dtype=torch.int32)),
+    lambda n: kda.short_conv(far(3, 1), far(1, 2), initial_state=far(n, 1, 1),
+                             slots=far(1, dtype=torch.int32)),
+    lambda n: kda.selective_scan_step(far(n, 1, 1, dtype=f32), far(n, 1), far(n, 1),
+                                      far(1, 1, dtype=f32), far(n, 1, 1), far(n, 1, 1)),
+    lambda n: kda.selective_scan_step(far(n, 1, 1, dtype=f32), far(3, 1), far(3, 1),
+                                      far(1, 1, dtype=f32), far(3, 1, 1), far(3, 1, 1),
+                                      slots=far(3, dtype=torch.int32)),
+    lambda n: kda.selective_scan(far(3, 1), far(3, 1), far(1, 1, dtype=f32), far(3, 1, 1),
+                                 far(3, 1, 1), final_state=far(n, 1, 1, dtype=f32),
+                                 slots=far(1, dtype=torch.int32)),
+    lambda n: kda.selective_scan(far(3, 1), far(3, 1), far(1, 1, dtype=f32), far(3, 1, 1),
+                                 far(3, 1, 1), split_hint=n),
+])
+def test_counts_past_31_bits_are_refused(call):
+    """The library counts in 32 bits, and 2^32 + 5 must not pass for 5."""
+    for n in ((1 << 31), (1 << 32) + 5):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call(n)
+
+
 # ---- the 64-bit forms -------------------------------------------------------------------
 
 def test_conv_form_is_a_correlation():
