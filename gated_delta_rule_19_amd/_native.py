@@ -52,6 +52,25 @@ class SsmIo(ctypes.Structure):
         [("delta_softplus", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class DecayIo(ctypes.Structure):
+    """``kda_decay_io`` of include/kda.h, field for field."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "g", "o")] + \
+        [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "g_stride",
+                                       "o_stride")] + \
+        [(n, ctypes.c_int32) for n in ("Hq", "Hk", "Hv", "dk", "dv")] + \
+        [("scale", ctypes.c_float)]
+
+
+class NormIo(ctypes.Structure):
+    """``kda_norm_io`` of include/kda.h, field for field."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "gate", "residual", "residual_out", "y")] + \
+        [(n, ctypes.c_int64) for n in ("x_stride", "gate_stride", "residual_stride",
+                                       "residual_out_stride", "y_stride")] + \
+        [(n, ctypes.c_void_p) for n in ("post_weight", "weight", "scale")] + \
+        [(n, ctypes.c_float) for n in ("post_eps", "eps", "scale_all")] + \
+        [("residual_dt", ctypes.c_int32)]
+
+
 # Every symbol include/kda.h declares.
 EXPORTED = (
     "kda_status_string",
@@ -82,6 +101,13 @@ EXPORTED = (
     "kda_selective_scan_step",
     "kda_state_store",
     "kda_state_load",
+    "kda_decay_attention_workspace_size",
+    "kda_decay_attention",
+    "kda_decay_attention_step",
+    "kda_block_norm",
+    "kda_beam_select_workspace_size",
+    "kda_beam_select",
+    "kda_state_reorder",
 )
 
 _lib = None
@@ -180,6 +206,24 @@ def load():
         lib.kda_state_store.argtypes = [i32, i64, i32, i32, vp, vp, i32, vp, vp, vp, i32, vp]
         lib.kda_state_load.restype = i32
         lib.kda_state_load.argtypes = [i32, i64, i32, i32, vp, vp, vp, i32, vp, vp, i32, vp]
+        dp = ctypes.POINTER(DecayIo)
+        lib.kda_decay_attention_workspace_size.restype = sz
+        lib.kda_decay_attention_workspace_size.argtypes = [i32, vp, i32, i32, i32, i32, i32]
+        lib.kda_decay_attention.restype = i32
+        lib.kda_decay_attention.argtypes = [i32, vp, i32, i32, dp, vp, vp, vp, i32, i32, vp, sz,
+                                            vp]
+        lib.kda_decay_attention_step.restype = i32
+        lib.kda_decay_attention_step.argtypes = [i32, i32, i32, dp, vp, vp, i32, vp]
+        lib.kda_block_norm.restype = i32
+        lib.kda_block_norm.argtypes = [i32, i32, i32, ctypes.POINTER(NormIo), vp]
+        lib.kda_beam_select_workspace_size.restype = sz
+        lib.kda_beam_select_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+        lib.kda_beam_select.restype = i32
+        lib.kda_beam_select.argtypes = [i32, i32, i32, i32, i32, vp, i64, vp, vp, i32, i32, vp,
+                                        vp, vp, vp, vp, sz, vp]
+        lib.kda_state_reorder.restype = i32
+        lib.kda_state_reorder.argtypes = [i32, i32, vp, vp, i32, ctypes.POINTER(vp), lp,
+                                          ctypes.POINTER(i32), vp]
         _lib = lib
         return lib
 

@@ -1,0 +1,632 @@
+// Beam search's selection over beams and vocabulary, and the reordering of the
+// states that the chosen beams continue from.
+//
+// Selection.  Token v of beam w is worth score[w] + x[w, v] - lse[w], with
+// lse[w] = log(sum_u exp(x[w, u])).  Within a beam that is the order of the
+// logits themselves, so each logit is read once, by the first of two kernels:
+//   part kernel: a workgroup holds 16 KB of one beam's logits in registers and
+//     finds their maximum, the sum of exp(x - maximum), and the K largest in
+//     order (larger first, equal ones by the lower token);
+//   merge kernel: a workgroup per batch joins the parts' sums into lse, values
+//     the parts' candidates in 64 bits, and takes the K best of them.
+// The part kernel finds its K largest without sorting them all: the K-th
+// largest of the lanes' own maxima has K elements at or above it, so only what
+// reaches it is collected and ranked.  A logit of -inf is never collected:
+// where fewer than K candidates are above -inf, the lowest (w, v) that are not
+// among them fill up the selection.
+//
+// Sums: exp from fp32 with its argument's rounding put back (about 2^-23
+// relative a term), added in 64 bits; so two beams' candidates change places
+// only if their values are that near.
+//
+// Reordering.  One pass in place: a lane holds the same 16 bytes of all rows
+// of its group that change, loads them all, then stores them, so no order of
+// rows can overwrite what is still to be read, whatever the table.
+#include "kda_block.h"
+#include "kda_device.h"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace kda {
+
+namespace {
+
+// ---- selection: parts ---------------------------------------------------------
+
+constexpr int kPartBytes = 16384; // of logits per workgroup
+template <typename T> constexpr int kPart = kPartBytes / (int)sizeof(T);
+
+struct BeamArgs {
+  int32_t B, W, V, K, eos, order;
+  int32_t parts, groups_log2; // lane groups whose maxima set the threshold
+  int64_t row_stride;
+};
+
+struct Cand { // a candidate of a part: token < 0 marks none
+  float x;
+  int32_t v;
+};
+struct PartSum {
+  double sum;
+  float max;
+  int32_t pad;
+};
+
+// Keys in the order of the selection: the value's order (-0 as 0) above the
+// complement of the place in the part.  Unique, and never 0 for a value above
+// -inf.
+template <typename T> struct KeyOf;
+template <> struct KeyOf<bf16> {
+  typedef uint32_t type; // 16 bits of value, 13 of place
+  static __device__ __forceinline__ uint32_t make(float x, int at) {
+    uint32_t u = __builtin_bit_cast(uint32_t, x + 0.f) >> 16;
+    u ^= u & 0x8000u ? 0xffffu : 0x8000u;
+    return u << 13 | (uint32_t)(kPart<bf16> - 1 - at);
+  }
+  static __device__ __forceinline__ int place(uint32_t k) {
+    return kPart<bf16> - 1 - (int)(k & (kPart<bf16> - 1));
+  }
+  static __device__ __forceinline__ float value(uint32_t k) {
+    uint32_t u = k >> 13;
+    u ^= u & 0x8000u ? 0x8000u : 0xffffu;
+    return __builtin_bit_cast(float, u << 16);
+  }
+};
+template <> struct KeyOf<float> {
+  typedef uint64_t type; // 32 bits of value, 12 of place
+  static __device__ __forceinline__ uint64_t make(float x, int at) {
+    uint32_t u = __builtin_bit_cast(uint32_t, x + 0.f);
+    u ^= u & 0x80000000u ? 0xffffffffu : 0x80000000u;
+    return (uint64_t)u << 12 | (uint64_t)(kPart<float> - 1 - at);
+  }
+  static __device__ __forceinline__ int place(uint64_t k) {
+    return kPart<float> - 1 - (int)(k & (kPart<float> - 1));
+  }
+  static __device__ __forceinline__ float value(uint64_t k) {
+    uint32_t u = (uint32_t)(k >> 12);
+    u ^= u & 0x80000000u ? 0x80000000u : 0xffffffffu;
+    return __builtin_bit_cast(float, u);
+  }
+};
+static_assert(kPart<bf16> == 1 << 13 && kPart<float> == 1 << 12, "key layout");
+
+// eight elements with their type's alignment only
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+__device__ __forceinline__ void load8(const bf16 *p, float *x) {
+  widen8(*reinterpret_cast<const u32x4_any *>(p), x);
+}
+__device__ __forceinline__ void load8(const float *p, float *x) {
+  const f32x4 a = *reinterpret_cast<const f32x4_any *>(p);
+  const f32x4 b = *reinterpret_cast<const f32x4_any *>(p + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = a[i];
+    x[4 + i] = b[i];
+  }
+}
+
+__device__ __forceinline__ float lane_f32(float x, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+}
+__device__ __forceinline__ double lane_f64(double x, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// The K-th largest of the maxima of 2^groups_log2 >= K lane groups: at least K
+// elements of the wave reach it, or it is -inf.
+template <typename F, typename R>
+__device__ __forceinline__ F kth_of_groups(F m, int K, int groups_log2, R &&read_lane) {
+  const int lane = threadIdx.x & 63, width = 64 >> groups_log2;
+  for (int b = 1; b < width; b <<= 1) {
+    const F o = __shfl_xor(m, b);
+    m = o > m ? o : m;
+  }
+  int above = 0;
+  for (int g = 0; g < (1 << groups_log2); ++g) {
+    const F o = read_lane(m, g * width);
+    above += o > m || (o == m && g * width < (lane & -width));
+  }
+  return read_lane(m, __builtin_ctzll(__ballot(above == K - 1)));
+}
+
+// exp(d) for d <= 0: exp2 of the product with log2(e), whose rounding and the
+// constant's are put back to first order.
+__device__ __forceinline__ float exp_neg(float d) {
+  constexpr float c1 = 0x1.715476p+0f, c2 = 0x1.4ae0bep-26f, ln2 = 0x1.62e43p-1f;
+  const float t = d * c1;
+  const float r = fmaf(d, c2, fmaf(d, c1, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return t < -126.f ? e : fmaf(e, r * ln2, e); // (there d may be -inf)
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void beam_part_kernel(BeamArgs a, const T *__restrict__ logits,
+                                                        Cand *__restrict__ cand,
+                                                        PartSum *__restrict__ sums) {
+  typedef KeyOf<T> KO;
+  typedef typename KO::type Key;
+  constexpr int kN = kPart<T> / 256 / 8; // groups of eight a lane
+  __shared__ Key keys[kPart<T>];
+  __shared__ float wave_max[4], wave_kth[4];
+  __shared__ double wave_sum[4];
+  __shared__ int count;
+  const int row = blockIdx.x / a.parts, part = blockIdx.x - row * a.parts;
+  const int tid = threadIdx.x, wv = tid >> 6;
+  const int first = part * kPart<T>;
+  const int left = a.V - first; // elements from the part's start on
+  const T *p = logits + row * a.row_stride + first;
+
+  float x[kN][8];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const int c = (i * 256 + tid) * 8;
+    if (c + 8 <= left) {
+      load8(p + c, x[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        x[i][j] = c + j < left ? to_f32(p[c + j]) : -__builtin_inff();
+    }
+  }
+  float m = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < kN; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      m = fmaxf(m, x[i][j]); // (a NaN is found by the sum)
+  const float kth = kth_of_groups(m, a.K, a.groups_log2, lane_f32);
+  float top = m;
+#pragma unroll
+  for (int b = 1; b < 64; b <<= 1)
+    top = fmaxf(top, __shfl_xor(top, b));
+  if ((tid & 63) == 0) {
+    wave_max[wv] = top;
+    wave_kth[wv] = kth;
+  }
+  if (tid == 0)
+    count = 0;
+  __syncthreads();
+  top = fmaxf(fmaxf(wave_max[0], wave_max[1]), fmaxf(wave_max[2], wave_max[3]));
+  const float bar = fmaxf(fmaxf(wave_kth[0], wave_kth[1]), fmaxf(wave_kth[2], wave_kth[3]));
+
+  // what reaches the threshold, in any order: the keys are ordered below
+#pragma unroll
+  for (int i = 0; i < kN; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (x[i][j] >= bar && x[i][j] > -__builtin_inff())
+        keys[atomicAdd(&count, 1)] = KO::make(x[i][j], (i * 256 + tid) * 8 + j);
+
+  double sum = 0.;
+  if (top > -__builtin_inff()) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        sum += (double)exp_neg(x[i][j] - top);
+  } else {
+    // nothing, unless a NaN hides there
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (x[i][j] != x[i][j])
+          sum = __builtin_nan("");
+  }
+#pragma unroll
+  for (int b = 1; b < 64; b <<= 1)
+    sum += __shfl_xor(sum, b);
+  if ((tid & 63) == 0)
+    wave_sum[wv] = sum;
+  __syncthreads();
+  if (tid == 0)
+    sums[blockIdx.x] = {wave_sum[0] + wave_sum[1] + (wave_sum[2] + wave_sum[3]), top, 0};
+
+  const int n = count;
+  Cand *out = cand + (int64_t)blockIdx.x * a.K;
+  const auto put = [&](int at, Key k) { out[at] = {KO::value(k), first + KO::place(k)}; };
+  if (n <= 256) { // by rank
+    if (tid < n) {
+      const Key k = keys[tid];
+      int above = 0;
+      for (int i = 0; i < n; ++i)
+        above += keys[i] > k;
+      if (above < a.K)
+        put(above, k);
+    }
+  } else { // (many equal logits, or few distinct lanes) sorted whole
+    int size = 512;
+    while (size < n)
+      size <<= 1;
+    for (int i = n + tid; i < size; i += 256)
+      keys[i] = 0;
+    for (int run = 2; run <= size; run <<= 1)
+      for (int d = run >> 1; d > 0; d >>= 1) {
+        __syncthreads();
+        for (int i = tid; i < size / 2; i += 256) {
+          const int lo = (i & ~(d - 1)) << 1 | (i & (d - 1)), hi = lo | d;
+          const Key u = keys[lo], v = keys[hi];
+          if ((u < v) == ((lo & run) == 0)) {
+            keys[lo] = v;
+            keys[hi] = u;
+          }
+        }
+      }
+    __syncthreads();
+    if (tid < a.K)
+      put(tid, keys[tid]); // (n > 256 >= K)
+  }
+  if (n < a.K && tid >= n && tid < a.K)
+    out[tid] = {0.f, -1};
+}
+
+// ---- selection: merge -----------------------------------------------------------
+
+constexpr int kMergeCap = 1024;
+
+// A valued candidate.  Before another one: the larger value, then the lower
+// beam, then (where 64 bits do not tell a beam's values apart) the larger
+// logit, then the lower token.
+struct Valued {
+  double val;
+  float x;
+  int32_t w, v;
+};
+__device__ __forceinline__ bool before(const Valued &p, const Valued &q) {
+  if (p.val != q.val)
+    return p.val > q.val;
+  if (p.w != q.w)
+    return p.w < q.w;
+  if (p.x != q.x)
+    return p.x > q.x;
+  return p.v < q.v;
+}
+
+__global__ __launch_bounds__(256) void beam_merge_kernel(
+    BeamArgs a, const Cand *__restrict__ cand, const PartSum *__restrict__ sums,
+    const float *__restrict__ scores, const uint8_t *__restrict__ finished,
+    float *__restrict__ out_scores, int32_t *__restrict__ out_parents,
+    int32_t *__restrict__ out_tokens, uint8_t *__restrict__ out_finished) {
+  __shared__ double lse[KDA_BEAM_MAX], base[KDA_BEAM_MAX]; // base NaN: beam without value
+  __shared__ bool done[KDA_BEAM_MAX];
+  __shared__ double wave_kth[4];
+  __shared__ Valued buf[kMergeCap];
+  __shared__ Valued sel[KDA_BEAM_MAX];
+  __shared__ Valued wave_best[4];
+  __shared__ int count;
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int K = a.K, W = a.W, P = a.parts;
+  const double inf = __builtin_inf();
+  const PartSum *ps = sums + (int64_t)b * W * P;
+  const Cand *cs = cand + (int64_t)b * W * P * K;
+
+  for (int w = wv; w < W; w += 4) {
+    float top = -__builtin_inff();
+    for (int p = lane; p < P; p += 64)
+      top = fmaxf(top, ps[w * P + p].max);
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1)
+      top = fmaxf(top, __shfl_xor(top, s));
+    double sum = 0.;
+    for (int p = lane; p < P; p += 64) {
+      const PartSum q = ps[w * P + p];
+      // (a part of -inf only has the sum 0, or NaN)
+      sum += q.max > -__builtin_inff() ? q.sum * exp((double)q.max - (double)top) : q.sum;
+    }
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1)
+      sum += __shfl_xor(sum, s);
+    if (lane == 0) {
+      const double l = (double)top + log(sum);
+      const float sc = scores[b * W + w];
+      const bool fin = finished && finished[b * W + w];
+      const bool has = sc - sc == 0.f && (fin || l - l == 0.); // finite
+      done[w] = fin;
+      lse[w] = l;
+      base[w] = has ? (double)sc : __builtin_nan("");
+    }
+  }
+  if (tid == 0)
+    count = 0;
+  __syncthreads();
+
+  // list i: the candidates of part i % P of beam i / P, best first
+  const int lists = W * P;
+  const auto open = [&](int w) { return base[w] == base[w] && !done[w]; };
+  const auto value = [&](int w, const Cand &c) { return base[w] + ((double)c.x - lse[w]); };
+  const auto of_done = [&](int w) { // the one candidate of a finished beam
+    return Valued{base[w], 0.f, w, a.eos};
+  };
+  double best = -inf;
+  for (int i = tid; i < lists; i += 256) {
+    const int w = i / P;
+    const Cand c = cs[(int64_t)i * K];
+    if (open(w) && c.v >= 0)
+      best = fmax(best, value(w, c));
+  }
+  const double kth = kth_of_groups(best, K, a.groups_log2, lane_f64);
+  if (lane == 0)
+    wave_kth[wv] = kth;
+  __syncthreads();
+  const double bar = fmax(fmax(wave_kth[0], wave_kth[1]), fmax(wave_kth[2], wave_kth[3]));
+  const auto push = [&](const Valued &v) {
+    const int at = atomicAdd(&count, 1);
+    if (at < kMergeCap)
+      buf[at] = v;
+  };
+  for (int i = tid; i < lists; i += 256) {
+    const int w = i / P;
+    if (!open(w))
+      continue;
+    for (int k = 0; k < K; ++k) {
+      const Cand c = cs[(int64_t)i * K + k];
+      if (c.v < 0)
+        break;
+      const double v = value(w, c);
+      if (v < bar)
+        break;
+      push({v, c.x, w, c.v});
+    }
+  }
+  if (tid < W && done[tid] && base[tid] == base[tid])
+    push(of_done(tid));
+  __syncthreads();
+
+  const int n = count;
+  if (n <= kMergeCap) {
+    for (int i = tid; i < n; i += 256) {
+      const Valued v = buf[i];
+      int above = 0;
+      for (int j = 0; j < n; ++j)
+        above += before(buf[j], v);
+      if (above < K)
+        sel[above] = v;
+    }
+  } else {
+    // more than the buffer holds (thousands of equal values): one by one, each
+    // time the best of all candidates that come after the last one
+    Valued last{inf, 0.f, -1, -1};
+    for (int k = 0; k < K; ++k) {
+      Valued mine{-inf, 0.f, W, 0};
+      const auto take = [&](const Valued &v) {
+        if (before(last, v) && before(v, mine))
+          mine = v;
+      };
+      for (int i = tid; i < lists; i += 256)
+        if (open(i / P))
+          for (int j = 0; j < K; ++j) {
+            const Cand c = cs[(int64_t)i * K + j];
+            if (c.v < 0)
+              break;
+            take({value(i / P, c), c.x, i / P, c.v});
+          }
+      if (tid < W && done[tid] && base[tid] == base[tid])
+        take(of_done(tid));
+      for (int s = 1; s < 64; s <<= 1) {
+        const Valued o{__shfl_xor(mine.val, s), __shfl_xor(mine.x, s), __shfl_xor(mine.w, s),
+                       __shfl_xor(mine.v, s)};
+        if (before(o, mine))
+          mine = o;
+      }
+      if (lane == 0)
+        wave_best[wv] = mine;
+      __syncthreads();
+      for (int s = 0; s < 4; ++s)
+        if (before(wave_best[s], mine))
+          mine = wave_best[s];
+      last = mine;
+      if (tid == 0)
+        sel[k] = mine;
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+  if (wv != 0)
+    return;
+
+  // one wave from here on: entry `lane` of the selection
+  const int have = min(n, K);
+  Valued v{-inf, 0.f, 0, 0};
+  if (lane < have)
+    v = sel[lane];
+  if (have < K) {
+    // the lowest (w, v) that are not chosen: of the first K places at most
+    // `have` are
+    bool open_place = lane < K;
+    for (int i = 0; i < have; ++i)
+      open_place = open_place && (int64_t)sel[i].w * a.V + sel[i].v != lane;
+    uint64_t places = __ballot(open_place);
+    if (lane >= have && lane < K) {
+      for (int i = lane - have; i > 0; --i)
+        places &= places - 1;
+      const int at = __builtin_ctzll(places);
+      v.w = at / a.V;
+      v.v = at % a.V;
+    }
+  }
+  int to = lane;
+  if (a.order == KDA_BEAM_BY_ROW) {
+    bool stays = lane < K;
+    uint64_t taken = 0;
+    for (int i = 0; i < K; ++i) {
+      const int w = __builtin_amdgcn_readlane(v.w, i);
+      taken |= 1ull << w;
+      stays = stays && !(i < lane && w == v.w);
+    }
+    const uint64_t moves = __ballot(lane < K && !stays);
+    if (stays) {
+      to = v.w;
+    } else {
+      uint64_t spare = ~taken;
+      for (int i = __popcll(moves & ((1ull << lane) - 1)); i > 0; --i)
+        spare &= spare - 1;
+      to = spare ? __builtin_ctzll(spare) : 0;
+    }
+  }
+  if (lane < K) {
+    const int64_t at = (int64_t)b * K + to;
+    out_scores[at] = (float)v.val;
+    out_parents[at] = v.w;
+    out_tokens[at] = v.v;
+    out_finished[at] = done[v.w] || v.v == a.eos;
+  }
+}
+
+// ---- reordering ----------------------------------------------------------------
+
+typedef u32x4 u32x4_byte __attribute__((aligned(1)));
+typedef uint32_t u32_byte __attribute__((aligned(1)));
+constexpr int kReorderCols = 4; // units a lane
+
+// KM: rows that change, at most; U: bytes a lane holds of each.
+template <int KM, typename U>
+__global__ __launch_bounds__(256) void reorder_kernel(ReorderCall c) {
+  __shared__ int64_t from[KDA_BEAM_MAX], to[KDA_BEAM_MAX];
+  __shared__ int moved;
+  // state, group and block of columns
+  int64_t blk = blockIdx.x;
+  int s = 0;
+  int64_t per = 0;
+  for (; s < c.num_states; ++s) {
+    per = (c.bytes[s] + 256 * kReorderCols * (int64_t)sizeof(U) - 1) /
+          (256 * kReorderCols * (int64_t)sizeof(U));
+    if (blk < per * c.groups)
+      break;
+    blk -= per * c.groups;
+  }
+  if (s == c.num_states)
+    return;
+  const int group = (int)(blk / per);
+  const int64_t col0 = (blk - group * per) * (256 * kReorderCols * (int64_t)sizeof(U));
+  const int64_t bytes = c.bytes[s];
+  if (threadIdx.x < 64) {
+    const int r = threadIdx.x;
+    const int64_t row = (int64_t)group * c.K + r;
+    int64_t f = 0, t = 0;
+    bool moves = false;
+    if (r < c.K) {
+      const int p = c.parents[row];
+      if (p >= 0 && p < c.K && p != r) {
+        f = c.slots ? c.slots[row - r + p] : row - r + p;
+        t = c.slots ? c.slots[row] : row;
+        moves = f >= 0 && f < c.num_slots[s] && t >= 0 && t < c.num_slots[s];
+      }
+    }
+    const uint64_t which = __ballot(moves);
+    if (moves) {
+      const int at = __popcll(which & ((1ull << r) - 1));
+      from[at] = f * bytes;
+      to[at] = t * bytes;
+    }
+    if (r == 0)
+      moved = __popcll(which);
+  }
+  __syncthreads();
+  const int n = __builtin_amdgcn_readfirstlane(moved);
+  if (n == 0)
+    return;
+  uint8_t *base = (uint8_t *)c.state[s];
+  for (int k = 0; k < kReorderCols; ++k) {
+    const int64_t col = col0 + ((int64_t)k * 256 + threadIdx.x) * (int64_t)sizeof(U);
+    if (col + (int64_t)sizeof(U) <= bytes) {
+      typedef std::conditional_t<sizeof(U) == 16, u32x4_byte, u32_byte> Any;
+      U v[KM];
+#pragma unroll
+      for (int i = 0; i < KM; ++i)
+        if (i < n)
+          v[i] = *reinterpret_cast<const Any *>(base + from[i] + col);
+#pragma unroll
+      for (int i = 0; i < KM; ++i)
+        if (i < n)
+          *reinterpret_cast<Any *>(base + to[i] + col) = v[i];
+    } else {
+      // the last bytes of a slice whose size is no multiple of the unit
+      for (int64_t at = col; at < bytes; ++at) {
+        uint8_t v[KM];
+#pragma unroll
+        for (int i = 0; i < KM; ++i)
+          if (i < n)
+            v[i] = base[from[i] + at];
+#pragma unroll
+        for (int i = 0; i < KM; ++i)
+          if (i < n)
+            base[to[i] + at] = v[i];
+      }
+    }
+  }
+}
+
+template <typename T> int part_count(int32_t V) { return (V - 1) / kPart<T> + 1; }
+
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+
+} // namespace
+
+size_t beam_workspace(int elt, int32_t B, int32_t W, int32_t V, int32_t K) {
+  const size_t parts = elt == 1 ? part_count<bf16>(V) : part_count<float>(V);
+  const size_t n = (size_t)B * W * parts;
+  return up(n * sizeof(PartSum)) + up(n * K * sizeof(Cand));
+}
+
+hipError_t launch_beam_select(int elt, const BeamCall &c, void *ws, hipStream_t s) {
+  BeamArgs a{};
+  a.B = c.B;
+  a.W = c.W;
+  a.V = c.V;
+  a.K = c.K;
+  a.eos = c.eos;
+  a.order = c.order;
+  a.row_stride = c.row_stride;
+  a.parts = elt == 1 ? part_count<bf16>(c.V) : part_count<float>(c.V);
+  // twice K groups of lanes: their K-th maximum lets through some K elements a
+  // wave
+  while ((1 << a.groups_log2) < 2 * c.K && a.groups_log2 < 6)
+    ++a.groups_log2;
+  const int64_t n = (int64_t)c.B * c.W * a.parts;
+  if (n * 256 > UINT32_MAX)
+    return hipErrorInvalidConfiguration;
+  PartSum *sums = (PartSum *)ws;
+  Cand *cand = (Cand *)((uint8_t *)ws + up((size_t)n * sizeof(PartSum)));
+  if (elt == 1)
+    beam_part_kernel<bf16><<<(unsigned)n, 256, 0, s>>>(a, (const bf16 *)c.logits, cand, sums);
+  else
+    beam_part_kernel<float><<<(unsigned)n, 256, 0, s>>>(a, (const float *)c.logits, cand, sums);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess)
+    return e;
+  beam_merge_kernel<<<(unsigned)c.B, 256, 0, s>>>(a, cand, sums, c.scores, c.finished,
+                                                  c.out_scores, c.out_parents, c.out_tokens,
+                                                  c.out_finished);
+  return hipGetLastError();
+}
+
+hipError_t launch_state_reorder(const ReorderCall &c, hipStream_t s) {
+  const auto run = [&](auto km, auto unit) {
+    typedef decltype(unit) U;
+    const int64_t cols = 256 * kReorderCols * (int64_t)sizeof(U);
+    int64_t grid = 0;
+    for (int i = 0; i < c.num_states; ++i) {
+      const int64_t per = (c.bytes[i] + cols - 1) / cols;
+      if (per * c.groups > UINT32_MAX / 256 - grid)
+        return hipErrorInvalidConfiguration;
+      grid += per * c.groups;
+    }
+    reorder_kernel<decltype(km)::value, U><<<(unsigned)grid, 256, 0, s>>>(c);
+    return hipGetLastError();
+  };
+  using std::integral_constant;
+  if (c.K <= 4)
+    return run(integral_constant<int, 4>(), u32x4());
+  if (c.K <= 8)
+    return run(integral_constant<int, 8>(), u32x4());
+  if (c.K <= 16)
+    return run(integral_constant<int, 16>(), u32x4());
+  return run(integral_constant<int, 64>(), uint32_t());
+}
+
+} // namespace kda

@@ -637,6 +637,173 @@ kda_status kda_state_load(int32_t n, int64_t R, int32_t L, int32_t format, const
                           const float *scales, const int32_t *src, int32_t num_src, float *state,
                           const int32_t *dst, int32_t num_dst, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Calls of a decoder block around and beside the KDA layer: linear attention
+ * with one decay a head, the norms, gate and residual between blocks, and
+ * beam search with the reordering of the states it continues from.  The
+ * conventions of the calls around the recurrence hold here too (row strides,
+ * slots, overlaps, capture, infinities and NaN).
+ */
+
+/*
+ * Linear attention with one decay a head over packed sequences.  Per
+ * sequence and head h, with a dk x dv state S:
+ *     S_t = exp(g[t, h]) S_{t-1} + k_t v_t^T
+ *     o_t = scale S_t^T q_t
+ *
+ *   H, dk, dv    : heads (>= 1) and head sizes (1 .. KDA_DECAY_MAX_DIM each).
+ *   io           : q [T, Hq, dk], k [T, Hk, dk], v [T, Hv, dv], o [T, H, dv]
+ *                  of type dt, with row (token) strides in elements; Hq, Hk
+ *                  and Hv each divide H: head h reads head h / (H / Hq) of q
+ *                  and likewise of k and v.  g [T, H] fp32 with g_stride >= H,
+ *                  or one decay a head for all tokens, g [H], with g_stride
+ *                  0.  g is a natural-log decay, used as given; at or below
+ *                  -150 (fp32's exp is 0 there) it forgets everything.
+ *   initial_state, final_state : [num_slots, H, dk, dv] fp32, or NULL (zeros
+ *                  / not written).  final_state == initial_state is allowed;
+ *                  other overlaps are not.
+ *   split_hint   : 0: long sequences are cut into segments when their heads
+ *                  alone leave the device idle; 1: never; n > 1: about n
+ *                  segments for the longest sequence, others in segments of
+ *                  that length.  The result is the same up to fp32 rounding.
+ *   workspace    : DEVICE, of the queried size, 256-byte aligned (0 where
+ *                  none is needed, and for a call that will be refused: then
+ *                  it may be NULL).
+ * States, decays and sums are fp32.  With KDA_BF16, o is formed from bf16
+ * products (a chunk's scores and the state that enters it, each rounded
+ * once), the state is carried and updated to fp32 accuracy, and o is rounded
+ * once; with KDA_F32 all operands are fp32.
+ */
+#define KDA_DECAY_MAX_DIM 256
+
+typedef struct kda_decay_io {
+  const void *q, *k, *v;
+  const float *g;
+  void *o;
+  int64_t q_stride, k_stride, v_stride, g_stride, o_stride;
+  int32_t Hq, Hk, Hv, dk, dv;
+  float scale;
+} kda_decay_io;
+
+size_t kda_decay_attention_workspace_size(int32_t num_seqs, const int64_t *cu_seqlens_host,
+                                          int32_t H, int32_t dk, int32_t dv, kda_dtype dt,
+                                          int32_t split_hint);
+
+kda_status kda_decay_attention(int32_t num_seqs, const int64_t *cu_seqlens_host, int32_t H,
+                               kda_dtype dt, const kda_decay_io *io, const float *initial_state,
+                               float *final_state, const int32_t *slots, int32_t num_slots,
+                               int32_t split_hint, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/*
+ * The attention for one token of each of `rows` sequences: io's matrices have
+ * `rows` rows, state ([num_slots, H, dk, dv] fp32) is updated in place.  All
+ * arithmetic is fp32.
+ */
+kda_status kda_decay_attention_step(int32_t rows, int32_t H, kda_dtype dt, const kda_decay_io *io,
+                                    float *state, const int32_t *slots, int32_t num_slots,
+                                    void *stream);
+
+/*
+ * Norm after a block, its gate and scaled residual, and the norm before the
+ * next block, row by row over rows of D values:
+ *     u = x * post_weight / sqrt(mean(x^2) + post_eps)   (post_weight NULL: u = x)
+ *     u = u * sigmoid(gate)                              (gate NULL: not gated)
+ *     r = residual + scale * u          (residual NULL: r = scale * u)
+ *     y = r * weight / sqrt(mean(r^2) + eps)             (y NULL: not formed)
+ *
+ *   rows, D      : rows >= 0; D 1 .. KDA_NORM_MAX_WIDTH.
+ *   io           : x, gate and y [rows, D] of type dt; residual and
+ *                  residual_out [rows, D] of type residual_dt; fp32
+ *                  post_weight, weight and scale [D] (scale NULL: the number
+ *                  scale_all).  weight is needed where y is given, and y or
+ *                  residual_out (or both) must be given.  residual_out may be
+ *                  residual itself, and residual_out or y may be x or gate
+ *                  itself, where pointer, stride and type are the same.
+ * Sums and r are fp32; y is formed from r before r is rounded to its type.
+ */
+#define KDA_NORM_MAX_WIDTH 65536
+
+typedef struct kda_norm_io {
+  const void *x, *gate, *residual;
+  void *residual_out, *y;
+  int64_t x_stride, gate_stride, residual_stride, residual_out_stride, y_stride;
+  const float *post_weight, *weight, *scale;
+  float post_eps, eps, scale_all;
+  kda_dtype residual_dt;
+} kda_norm_io;
+
+kda_status kda_block_norm(int32_t rows, int32_t D, kda_dtype dt, const kda_norm_io *io,
+                          void *stream);
+
+/*
+ * Beam search: the K best continuations of W beams over V tokens, for each of
+ * B batches.  Token v of beam w is worth
+ *     scores[b, w] + logits[b, w, v] - log(sum_u exp(logits[b, w, u])),
+ * and a finished beam is worth its score with token eos and -inf with any
+ * other.  A beam without value (its score is not finite; or it is not finished
+ * and its logits hold a NaN or a +inf or are all -inf) counts as -inf
+ * throughout.  Larger values go first, equal ones by the lower w * V + v, so
+ * that the order is total.
+ *
+ *   B, W, V, K    : B >= 0; W and K 1 .. KDA_BEAM_MAX; K <= W * V.
+ *   logits        : [B, W, V] of type dt; row b * W + w starts row_stride
+ *                   elements after the one before (row_stride >= V, at most
+ *                   2^31).
+ *   scores        : fp32 [B, W].
+ *   finished      : bytes [B, W] (0: not finished), or NULL: none is.
+ *   eos           : the token that finishes a beam (0 .. V - 1), or -1: none
+ *                   does (then finished must be NULL).
+ *   order         : KDA_BEAM_BY_SCORE: the chosen, best first;
+ *                   KDA_BEAM_BY_ROW (K >= W): the best continuation of beam
+ *                   w is in row w, the others fill the rows left, best first:
+ *                   what goes on from a row's own state finds it in place.
+ *   out_scores, out_parents, out_tokens, out_finished : [B, K] fp32, int32 w,
+ *                   int32 v, byte (the parent is finished, or v is eos).  They
+ *                   may not overlap the inputs or each other.
+ *   workspace     : DEVICE, of the queried size, 256-byte aligned.
+ * Within a beam candidates are ordered by their logits as they are, across
+ * beams by values in 64 bits; the logarithm's sum is good to some 2^-24.
+ * out_scores are rounded to fp32.
+ */
+#define KDA_BEAM_MAX 64
+#define KDA_BEAM_BY_SCORE 0
+#define KDA_BEAM_BY_ROW 1
+
+size_t kda_beam_select_workspace_size(int32_t B, int32_t W, int32_t V, int32_t K, kda_dtype dt);
+
+kda_status kda_beam_select(int32_t B, int32_t W, int32_t V, int32_t K, kda_dtype dt,
+                           const void *logits, int64_t row_stride, const float *scores,
+                           const uint8_t *finished, int32_t eos, int32_t order,
+                           float *out_scores, int32_t *out_parents, int32_t *out_tokens,
+                           uint8_t *out_finished, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/*
+ * Reordering of states, in place: row r of group b becomes what row
+ * parents[b, r] of the group was before the call.  Any table is allowed (a
+ * row may go to many rows, or two rows change places).
+ *
+ *   groups, K    : groups >= 0 of K rows (1 .. KDA_BEAM_MAX).
+ *   parents      : DEVICE int32 [groups, K]; an entry outside [0, K) leaves
+ *                  its row as it is.
+ *   slots        : DEVICE int32 [groups, K], the slice of row r of group b,
+ *                  or NULL: slice b * K + r.  A row whose slice, or whose
+ *                  parent's slice, is outside a state's slices is left as it
+ *                  is.  The valid entries must differ.
+ *   num_states   : buffers to reorder (0 .. KDA_REORDER_MAX_STATES);
+ *   states_host, slice_bytes_host, num_slots_host : HOST arrays of that many
+ *                  buffers' addresses, bytes per slice (>= 0) and slice
+ *                  counts (>= groups * K where slots is NULL).  No two
+ *                  buffers may overlap.
+ */
+#define KDA_REORDER_MAX_STATES 32
+
+kda_status kda_state_reorder(int32_t groups, int32_t K, const int32_t *parents,
+                             const int32_t *slots, int32_t num_states, void *const *states_host,
+                             const int64_t *slice_bytes_host, const int32_t *num_slots_host,
+                             void *stream);
+
 #ifdef __cplusplus
 }
 #endif
