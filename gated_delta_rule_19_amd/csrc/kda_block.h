@@ -29,7 +29,7 @@ struct DecayPlan {
   size_t off_state, off_decay, total; // workspace layout (the table first)
 };
 DecayPlan decay_plan(int32_t num_seqs, const int64_t *cu, int32_t H, int32_t dk, int32_t dv,
-                     int elt, int32_t split_hint);
+                     int32_t split_hint);
 
 hipError_t launch_decay(int elt, const DecayCall &c, int32_t num_seqs, const int64_t *cu,
                         const DecayPlan &plan, void *ws, hipStream_t s);

@@ -6,26 +6,25 @@
 //   o_i = scale (e^{G_i} S^T q_i + sum_{j <= i} e^{G_i - G_j} (q_i . k_j) v_j)
 //   S'  = e^{G_L} S + sum_j k_j (e^{G_L - G_j} v_j)^T
 // that is four matrix products a chunk.  A workgroup carries the state of one
-// (sequence, head) and 64 value columns through the tokens in registers; wave
-// w owns 16 columns of the state (all dk rows) and the scores and outputs of
-// tokens 16 w .. 16 w + 15.  K and V of a chunk and the state that enters it
-// are shared through LDS; the next chunk's K, V, q and g are requested before
-// a chunk is worked on and wait in registers.
+// (sequence, head) and 64 or 128 value columns through the tokens; each of its
+// waves holds 16 columns of the state (all dk rows) in registers and forms
+// these columns of o.  The scores of a chunk are formed once, 16 tokens by 32
+// a wave, and shared through LDS as operands; q, k and v of a chunk lie in LDS
+// as they come.
 //
-// Layout: every product takes its tokens (the summed index of S' and of the
-// second part of o) in the order 32 s + 16 h + 4 g + r for element 4 h + r of
-// lane group g, which is how two tiles of scores come out of the matrix
-// instruction: the scores go into the next product from the registers they
-// are in, and K and V are read transposed in that order.  Column tiles take
-// the columns 32 (t / 2) + 8 (m / 4) + 4 (t % 2) + m % 4, so that a lane holds
-// eight neighbouring columns of o.
+// Layout: what one product leaves in registers is the next one's operand.  A
+// lane holds eight neighbouring rows of its state column in two accumulators
+// (tiles of rows take the rows 32 (t / 2) + 8 (m / 4) + 4 (t % 2) + m % 4), so
+// the state, rounded, is the operand of S^T q beside rows of q as they are.
+// The scores come out with the tokens 32 s + 16 h + 4 g + r in element 4 h + r
+// of lane group g; K and V are read transposed in that order.
 //
 // Roundings: the state is fp32 and its update takes v e^{G_L - G_j} as the sum
 // of three bf16 numbers (24 bits; one alone would leave the state 2^-9 off),
 // beside k as it is; the scores and the entering state are rounded to bf16
 // once each for o, which is rounded to bf16 itself.  fp32 calls round nothing.
-// G is summed in 64 bits and kept as two fp32 numbers, so that differences
-// within a chunk keep their accuracy beside a decay of e^-150.
+// G is summed and kept as two fp32 numbers, so that differences within a chunk
+// keep their accuracy beside a decay of e^-150.
 //
 // An infinity or NaN in k or v would reach earlier tokens of its chunk as
 // 0 * inf: a chunk is ended in front of such a token, which is then worked on
@@ -48,122 +47,161 @@ struct DecayArgs {
   float *fin;
   const int32_t *slots;
   // prompts
-  int32_t slices, seg; // 64-column slices of dv, tokens per segment
+  int32_t slices, seg; // slices of dv (a workgroup's columns), tokens per segment
   int64_t units;       // (segment, head) pairs of this launch
-  float *pair_state;   // [pairs, H, slices, DK / 16, 256] of four
+  float *pair_state;   // [pairs, H, slices, DK / 16, lanes] of four
   double *pair_decay;  // [pairs, H]: log2 of a segment's decay
 };
 
 constexpr float kMinDecay = -150.f; // fp32's exp is 0 there
-constexpr double kLog2E = 1.4426950408889634074;
-
 // exp(g), 0 from kMinDecay down (and for -inf)
 __device__ __forceinline__ float decay_of(float g) { return expf(fmaxf(g, kMinDecay)); }
 
-// 2^x of a 64-bit exponent, to an fp32 rounding or two
-__device__ __forceinline__ float exp2_of(double x) {
-  x = x < -1000. ? -1000. : x > 1000. ? 1000. : x; // (a NaN stays one)
-  const double n = rint(x);
-  return ldexpf(__builtin_amdgcn_exp2f((float)(x - n)), (int)n);
+// Numbers of some 48 bits as the sum of two fp32 ones, hi the sum rounded.
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair operator+(const Pair &a, const Pair &b) {
+  const float s = a.hi + b.hi, t = s - a.hi;
+  const float e = (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo);
+  const float h = s + e;
+  return {h, e - (h - s)};
+}
+__device__ __forceinline__ Pair operator-(const Pair &a) { return {-a.hi, -a.lo}; }
+// 2^x to an fp32 rounding or two, whatever the size of x
+__device__ __forceinline__ float exp2_of(const Pair &x) {
+  const float e = __builtin_amdgcn_exp2f(x.hi);
+  return fmaf(e, x.lo * 0.693147181f, e);
+}
+// log2 of a token's decay: g log2(e)
+__device__ __forceinline__ Pair log2_decay(float g) {
+  constexpr float c1 = 0x1.715476p+0f, c2 = 0x1.4ae0bep-26f; // log2(e)
+  g = g < kMinDecay ? kMinDecay : g; // (a NaN stays one)
+  const float hi = g * c1;
+  return {hi, fmaf(g, c2, fmaf(g, c1, -hi))};
+}
+// Sum over lanes 0 .. of a wave up to each (DPP: 1, 2, 4 and 8 lanes within
+// rows of 16, then the ends of rows to those behind).
+template <int CTRL, int ROWS> __device__ __forceinline__ Pair dpp_pair(const Pair &x) {
+  return {__builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                        0, __builtin_bit_cast(int, x.hi), CTRL, ROWS, 0xf, true)),
+          __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                        0, __builtin_bit_cast(int, x.lo), CTRL, ROWS, 0xf, true))};
+}
+__device__ __forceinline__ Pair prefix_sum(Pair x) {
+  x = x + dpp_pair<0x111, 0xf>(x);
+  x = x + dpp_pair<0x112, 0xf>(x);
+  x = x + dpp_pair<0x114, 0xf>(x);
+  x = x + dpp_pair<0x118, 0xf>(x);
+  x = x + dpp_pair<0x142, 0xa>(x);
+  return x + dpp_pair<0x143, 0xc>(x);
+}
+__device__ __forceinline__ Pair lane_pair(const Pair &x, int lane) {
+  lane = __builtin_amdgcn_readfirstlane(lane);
+  return {__builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x.hi), lane)),
+          __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x.lo), lane))};
 }
 
 // ---- prompts ----------------------------------------------------------------------
 
-constexpr int kDC = 64;   // tokens per chunk
-constexpr int kDCols = 64; // value columns per workgroup
+constexpr int kDC = 64; // tokens per chunk
 
-// Eight elements of a row, as loaded.
-template <typename T> struct Oct;
-template <> struct Oct<bf16> { u32x4 r; };
-template <> struct Oct<float> { f32x4 lo, hi; };
+// Tiles are staged in pieces of 16 bytes.
+template <typename T> constexpr int kPiece = 16 / (int)sizeof(T);
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
-typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
-// n of eight elements from p (n >= 8: all, n <= 0: none; the others are 0)
-__device__ __forceinline__ Oct<bf16> load_oct(const bf16 *p, int n) {
-  Oct<bf16> o{};
-  if (n >= 8) {
-    o.r = *reinterpret_cast<const u32x4_any *>(p);
-  } else if (n > 0) {
-    bf16x8 v{};
+// n elements of a piece from p (n >= the piece's: all, n <= 0: none; else 0)
+__device__ __forceinline__ u32x4 load_piece(const bf16 *p, int n) {
+  if (n >= 8)
+    return *reinterpret_cast<const u32x4_any *>(p);
+  bf16x8 v{};
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n)
-        v[i] = p[i];
-    o.r = __builtin_bit_cast(u32x4, v);
-  }
-  return o;
+  for (int i = 0; i < 7; ++i)
+    if (i < n)
+      v[i] = p[i];
+  return __builtin_bit_cast(u32x4, v);
 }
-__device__ __forceinline__ Oct<float> load_oct(const float *p, int n) {
-  Oct<float> o{};
-  if (n >= 8) {
-    o.lo = *reinterpret_cast<const f32x4_any *>(p);
-    o.hi = *reinterpret_cast<const f32x4_any *>(p + 4);
-  } else if (n > 0) {
-    float v[8] = {};
+__device__ __forceinline__ u32x4 load_piece(const float *p, int n) {
+  if (n >= 4)
+    return *reinterpret_cast<const u32x4_any *>(p);
+  f32x4 v{};
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n)
-        v[i] = p[i];
-    o.lo = f32x4{v[0], v[1], v[2], v[3]};
-    o.hi = f32x4{v[4], v[5], v[6], v[7]};
-  }
-  return o;
+  for (int i = 0; i < 3; ++i)
+    if (i < n)
+      v[i] = p[i];
+  return __builtin_bit_cast(u32x4, v);
 }
-__device__ __forceinline__ void to_lds(bf16 *p, const Oct<bf16> &o) {
-  *reinterpret_cast<u32x4 *>(p) = o.r;
-}
-__device__ __forceinline__ void to_lds(float *p, const Oct<float> &o) {
-  *reinterpret_cast<f32x4 *>(p) = o.lo;
-  *reinterpret_cast<f32x4 *>(p + 4) = o.hi;
-}
-__device__ __forceinline__ Frag<bf16> as_frag(const Oct<bf16> &o) {
-  return {__builtin_bit_cast(bf16x8, o.r)};
-}
-__device__ __forceinline__ Frag<float> as_frag(const Oct<float> &o) { return {o.lo, o.hi}; }
 
-// Nonzero where an element has an exponent of all ones.
-__device__ __forceinline__ uint32_t non_finite(const Oct<bf16> &o) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) // (the sums of the halves do not carry over)
-    m |= (o.r[i] & 0x7f807f80u) + 0x00800080u;
-  return m & 0x80008000u;
+// The sum of 0 * x over a piece: NaN where an element is not finite.
+__device__ __forceinline__ float zero_sum(const u32x4 &x, bf16) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  const bf16x8 v = __builtin_bit_cast(bf16x8, x);
+  const bf16x2_t z = {static_cast<bf16>(0.f), static_cast<bf16>(0.f)};
+  float a = __builtin_amdgcn_fdot2_f32_bf16(__builtin_shufflevector(v, v, 0, 1), z, 0.f, false);
+  float b = __builtin_amdgcn_fdot2_f32_bf16(__builtin_shufflevector(v, v, 2, 3), z, 0.f, false);
+  a = __builtin_amdgcn_fdot2_f32_bf16(__builtin_shufflevector(v, v, 4, 5), z, a, false);
+  b = __builtin_amdgcn_fdot2_f32_bf16(__builtin_shufflevector(v, v, 6, 7), z, b, false);
+  return a + b;
 }
-__device__ __forceinline__ uint32_t non_finite(const Oct<float> &o) {
-  const u32x4 lo = __builtin_bit_cast(u32x4, o.lo), hi = __builtin_bit_cast(u32x4, o.hi);
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    m |= ((lo[i] & 0x7f800000u) + 0x00800000u) | ((hi[i] & 0x7f800000u) + 0x00800000u);
-  return m & 0x80000000u;
+__device__ __forceinline__ float zero_sum(const u32x4 &x, float) {
+  const f32x4 v = __builtin_bit_cast(f32x4, x) * 0.f;
+  return (v[0] + v[1]) + (v[2] + v[3]);
 }
+
+// LDS matrices.  Rows have no padding; the pieces of a row are permuted by an
+// exclusive-or with bits of the row, so that the reads below meet every one of
+// 64 banks once: rows of fragments (16 rows, one piece), and tokens read
+// transposed (bf16: 8 rows, 2 or 4 pieces; fp32: 4 rows, 4 pieces).  K and q
+// have rows of LD = DK elements, V of the workgroup's columns.
+template <typename T, int LD> __device__ __forceinline__ int row_flip(int row) {
+  if constexpr (sizeof(T) == 4)
+    return row & 15;
+  else if constexpr (LD == 64) // (two rows meet all banks)
+    return ((row >> 1) & 3) << 1 | ((row >> 3) & 1);
+  else
+    return (row & 7) << 1 | ((row >> 3) & 1);
+}
+template <typename T, int LD> __device__ __forceinline__ int lds_at(int row, int col) {
+  constexpr int kP = kPiece<T>;
+  return row * LD + (((col / kP) ^ row_flip<T, LD>(row)) * kP | (col & (kP - 1)));
+}
+// Because only low bits of the row enter the permutation, 16 rows further is a
+// constant distance; and where bits of a column index above those of a lane's
+// own change, the place changes by an exclusive-or with them: with at =
+// lds_at(row, col), fragment s of a row is at ^ 32 s, row tile t of the state
+// (columns of K) at ^ state_tile(t), wave w's columns of V at ^ 16 w.
+__device__ __forceinline__ constexpr int state_tile(int t) { return 32 * (t >> 1) + 4 * (t & 1); }
+// Row m of tile 0 of the state's rows.
+__device__ __forceinline__ int state_row(int m) { return 8 * (m >> 2) + (m & 3); }
 
 // The operand of eight tokens (element 4 h + r: row0 + 16 h + 4 lg + r) and
-// the 16 columns col(m) of a tile, from a token-major LDS matrix.  bf16: two
-// transposed reads; in each 16-lane group, lane 4 a + b of ds_read_b64_tr_b16
-// receives element b of the 4-element reads of lanes a, a + 4, a + 8, a + 12,
-// so lane L reads four columns of row L / 4, from the one of m = 4 (L % 4) on.
-template <typename Col>
-__device__ __forceinline__ Frag<bf16> tr_frag(const bf16 *m, int ld, int row0, int lr, int lg,
-                                              Col &&col) {
+// the 16 columns of a tile; `ld` elements a row.  bf16: two transposed reads;
+// in each 16-lane group, lane 4 a + b of ds_read_b64_tr_b16 receives element b
+// of the 4-element reads of lanes a, a + 4, a + 8, a + 12, so lane L reads
+// four columns of row L / 4, from the one of m = 4 (L % 4) on (tr_row, tr_col).
+// fp32: element by element; at[r]: row 4 lg + r, column lr.
+template <typename T> constexpr int kTrAt = sizeof(T) == 4 ? 4 : 1;
+__device__ __forceinline__ Frag<bf16> tr_frag(const bf16 *m, int ld, const int (&at)[1], int flip) {
   typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
-  const bf16 *p = m + (row0 + 4 * lg + (lr >> 2)) * ld + col(4 * (lr & 3));
+  const bf16 *p = m + (at[0] ^ flip);
   const bf16x4 r0 = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4 *)p);
   const bf16x4 r1 = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4 *)(p + 16 * ld));
   return {__builtin_shufflevector(r0, r1, 0, 1, 2, 3, 4, 5, 6, 7)};
 }
-template <typename Col>
-__device__ __forceinline__ Frag<float> tr_frag(const float *m, int ld, int row0, int lr, int lg,
-                                               Col &&col) {
-  const float *p = m + (row0 + 4 * lg) * ld + col(lr);
+__device__ __forceinline__ Frag<float> tr_frag(const float *m, int ld, const int (&at)[4], int flip) {
   Frag<float> f;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    f.lo[r] = p[r * ld];
-    f.hi[r] = p[(16 + r) * ld];
+    f.lo[r] = m[at[r] ^ flip];
+    f.hi[r] = m[(at[r] ^ flip) + 16 * ld];
   }
   return f;
+}
+
+// Eight neighbouring elements of a row (fp32: two pieces).
+__device__ __forceinline__ Frag<bf16> lds_frag(const bf16 *m, int at) { return load_frag(m + at); }
+__device__ __forceinline__ Frag<float> lds_frag(const float *m, int at) {
+  return {*reinterpret_cast<const f32x4 *>(m + at), *reinterpret_cast<const f32x4 *>(m + (at ^ 4))};
 }
 
 __device__ __forceinline__ Frag<bf16> pack_scores(const f32x4 &lo, const f32x4 &hi, bf16) {
@@ -173,23 +211,47 @@ __device__ __forceinline__ Frag<float> pack_scores(const f32x4 &lo, const f32x4 
   return {lo, hi};
 }
 
+// A fragment kept in LDS as an operand, lane by lane.
+__device__ __forceinline__ void put_frag(bf16 *p, int lane, const Frag<bf16> &f) {
+  *reinterpret_cast<bf16x8 *>(p + lane * 8) = f.v;
+}
+__device__ __forceinline__ void put_frag(float *p, int lane, const Frag<float> &f) {
+  *reinterpret_cast<f32x4 *>(p + lane * 4) = f.lo;
+  *reinterpret_cast<f32x4 *>(p + 256 + lane * 4) = f.hi;
+}
+__device__ __forceinline__ Frag<bf16> get_frag(const bf16 *p, int lane) {
+  return load_frag(p + lane * 8);
+}
+__device__ __forceinline__ Frag<float> get_frag(const float *p, int lane) {
+  return {*reinterpret_cast<const f32x4 *>(p + lane * 4),
+          *reinterpret_cast<const f32x4 *>(p + 256 + lane * 4)};
+}
+
 // An operand times a weight per element, as a sum of operands.
 struct Split3 {
   Frag<bf16> part[3];
 };
 __device__ __forceinline__ Split3 weigh(const Frag<bf16> &v, const f32x4 &w0, const f32x4 &w1) {
-  Split3 s;
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  const u32x4 raw = __builtin_bit_cast(u32x4, v.v);
+  u32x4 out[3];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float x = static_cast<float>(v.v[i]) * (i < 4 ? w0[i & 3] : w1[i & 3]);
+  for (int i = 0; i < 4; ++i) {
+    float x = __builtin_bit_cast(float, raw[i] << 16) * (i < 2 ? w0[2 * i] : w1[2 * i - 4]);
+    float y = __builtin_bit_cast(float, raw[i] & 0xffff0000u) *
+              (i < 2 ? w0[2 * i + 1] : w1[2 * i - 3]);
 #pragma unroll
-    for (int p = 0; p < 3; ++p) {
-      const bf16 b = static_cast<bf16>(x);
-      s.part[p].v[i] = b;
-      x = x == static_cast<float>(b) ? 0.f : x - static_cast<float>(b);
+    for (int p = 0; p < 3; ++p) { // (a pair is rounded by one instruction)
+      const uint32_t b = __builtin_bit_cast(
+          uint32_t, bf16x2_t{static_cast<bf16>(x), static_cast<bf16>(y)});
+      out[p][i] = b;
+      x -= __builtin_bit_cast(float, b << 16);
+      y -= __builtin_bit_cast(float, b & 0xffff0000u);
     }
   }
-  return s;
+  return {{{__builtin_bit_cast(bf16x8, out[0])},
+           {__builtin_bit_cast(bf16x8, out[1])},
+           {__builtin_bit_cast(bf16x8, out[2])}}};
 }
 struct Whole {
   Frag<float> part[1];
@@ -198,28 +260,63 @@ __device__ __forceinline__ Whole weigh(const Frag<float> &v, const f32x4 &w0, co
   return {{{v.lo * w0, v.hi * w1}}};
 }
 
-template <typename T> struct Tiles; // rows of the LDS matrices, padded
-template <> struct Tiles<bf16> { static constexpr int k = 8, v = 8, s = 8; };
-template <> struct Tiles<float> { static constexpr int k = 4, v = 4, s = 4; };
+// A raw buffer's descriptor over `bytes` bytes at p (wave-uniform), in four
+// scalars.
+__device__ __forceinline__ u32x4 raw_rsrc(const void *p, uint32_t bytes) {
+  const uint64_t at = (uint64_t)(uintptr_t)p;
+  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)at),
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(at >> 32) & 0xffffu)),
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
+}
+// 16 bytes per lane from a raw buffer straight into LDS, lane l's to byte 16 l
+// after `to` (wave-uniform).  In assembly because the compiler, which sees such
+// a load as a store to any of LDS, would wait for it before each transposed
+// read; the walk below waits for vmcnt(0) and a barrier before it reads what
+// was loaded.  Nothing is returned in registers, and m0 serves nothing else
+// in these kernels.
+__device__ __forceinline__ void lds_request16(const u32x4 &r, int at, const void *to) {
+  // (the low half of a generic LDS address is the offset in LDS)
+  const uint32_t m0 = (uint32_t)(uintptr_t)to;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(m0)), "v"(at), "s"(r));
+}
+constexpr int kNowhere = 0x7fffffe0; // a byte offset past every buffer's end
+
+// LDS and memory reads in front of and behind this are not exchanged (the
+// scheduler would otherwise raise all of a chunk's, and spill registers).
+__device__ __forceinline__ void reads_stay() { __builtin_amdgcn_sched_barrier(0x000f); }
 
 // Launch `pass` 0: all segments but each sequence's last (all of them where a
 // sequence is not cut): the first segments in full, the others only their
 // state from zero.  Pass 1: the other segments from the states that enter
-// them.
-template <typename T, int DK>
-__global__ __launch_bounds__(256) void decay_chunk_kernel(SeqTable tab, DecayArgs a, int pass,
-                                                          const T *__restrict__ q,
-                                                          const T *__restrict__ k,
-                                                          const T *__restrict__ v,
-                                                          T *__restrict__ o) {
+// them.  NW waves, 16 value columns each.  FAST: dk, dv and the rows'
+// addresses are multiples of 16 bytes: everything moves through raw buffers,
+// whose bounds take the place of branches at a chunk's end, and q, K and V
+// straight into LDS.  AHEAD: a chunk ahead into the other one of two copies;
+// without, the loads of the one copy are waited for.
+template <typename T, int DK, int NW> constexpr int kCopyBytes =
+    kDC * (2 * DK + 16 * NW) * (int)sizeof(T);
+template <typename T, int DK, int NW, bool FAST>
+__global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
+    SeqTable tab, DecayArgs a, int pass, const T *__restrict__ q, const T *__restrict__ k,
+    const T *__restrict__ v, T *__restrict__ o) {
   const SeqView sv(tab);
-  constexpr int kLdK = DK + Tiles<T>::k, kLdV = kDCols + Tiles<T>::v, kLdS = DK + Tiles<T>::s;
-  constexpr int kGK = DK / 32, kGV = 2; // groups of eight of K and V a lane stages
-  constexpr int kTD = DK / 16;          // state tiles of a wave
-  __shared__ alignas(16) T Ks[kDC * kLdK], Vs[kDC * kLdV], Ss[kDCols * kLdS];
-  __shared__ alignas(16) float Ghi[kDC], Glo[kDC], wts[kDC], eG[kDC];
-  __shared__ float total;
-  __shared__ int first_bad[4];
+  constexpr int kEs = (int)sizeof(T), kP = kPiece<T>;
+  constexpr int kCols = 16 * NW;                // value columns
+  constexpr int kGQ = DK / 32;                  // fragments of a row of q or K
+  constexpr int kTD = DK / 16;                  // row tiles of a wave's state
+  constexpr int kNK = DK * kEs / (16 * NW);     // pieces of K (q) a lane stages
+  constexpr int kNV = kEs;                      // pieces of V a lane stages
+  constexpr bool AHEAD = FAST && 2 * kCopyBytes<T, DK, NW> <= 98304;
+  constexpr int kBufs = AHEAD ? 2 : 1;
+  // (bf16 has room for the scores beside q; fp32 puts them in its place)
+  constexpr bool OWN_P = kEs == 2;
+  __shared__ alignas(16) T Qs[kBufs][kDC * DK], Ks[kBufs][kDC * DK], Vs[kBufs][kDC * kCols];
+  __shared__ alignas(16) T Ps[OWN_P ? kDC * kDC : 8];
+  __shared__ alignas(16) float Ghi[2][kDC], Glo[2][kDC], wts[2][kDC], eG[2][kDC];
+  __shared__ float total[2];
+  __shared__ int first_bad[2][NW];
 
   // block b: unit (b / 8 / slices) * 8 + b % 8, slice b / 8 % slices: slices
   // of one unit, which share q and k, are on one die
@@ -233,7 +330,6 @@ __global__ __launch_bounds__(256) void decay_chunk_kernel(SeqTable tab, DecayArg
   const int nseg = sv.blk(n + 1, 1) - sv.blk(n, 1) + 1; // (pairs in front: pass 1's blocks)
   const int seg = blk - sv.blk(n, pass) + pass;
   const int64_t pair0 = sv.blk(n, 1);
-  const bool outputs = pass == 1 || seg == 0;
   int pos = seg * a.seg;
   const int end = min(len, pos + a.seg);
   const int64_t slot = a.slots ? a.slots[seq] : seq;
@@ -241,262 +337,444 @@ __global__ __launch_bounds__(256) void decay_chunk_kernel(SeqTable tab, DecayArg
 
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int col0 = slice * kDCols;
-  const auto row_col = [](int d) { return [d](int m) { return 16 * d + m; }; };
-  const auto val_col = [](int e) {
-    return [e](int m) { return 32 * (e >> 1) + 8 * (m >> 2) + 4 * (e & 1) + (m & 3); };
-  };
-  const int my_col = val_col(w)(lr); // of the state this lane holds
+  const int col0 = slice * kCols;
+  const int cols = min(kCols, a.dv - col0);
+  const int my_col = 16 * w + lr; // of the state this lane holds
 
-  // the state that enters: lane (lr, lg) element r of tile d is row 16 d + 4
-  // lg + r of column my_col
+  // the state that enters: element r of tile d is row state_tile(d) + 8 lg + r
+  // of column my_col
   f32x4 S[kTD];
   const int64_t global = (slot * a.H + h) * a.dk * a.dv + col0 + my_col;
-  float *pairs = a.pair_state + ((pair0 * a.H + h) * a.slices + slice) * (kTD * 1024) + tid * 4;
-  const int64_t pair_step = (int64_t)a.H * a.slices * (kTD * 1024);
+  float *pairs =
+      a.pair_state + ((pair0 * a.H + h) * a.slices + slice) * (kTD * 256 * NW) + tid * 4;
+  const int64_t pair_step = (int64_t)a.H * a.slices * (kTD * 256 * NW);
   if (pass == 1) {
 #pragma unroll
     for (int d = 0; d < kTD; ++d)
-      S[d] = *reinterpret_cast<const f32x4 *>(pairs + (seg - 1) * pair_step + d * 1024);
+      S[d] = *reinterpret_cast<const f32x4 *>(pairs + (seg - 1) * pair_step + d * 256 * NW);
   } else {
-    const bool from = seg == 0 && a.init && kept && col0 + my_col < a.dv;
+    const bool from = seg == 0 && a.init && kept && my_col < cols;
 #pragma unroll
     for (int d = 0; d < kTD; ++d)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int row = 16 * d + 4 * lg + r;
+        const int row = state_tile(d) + 8 * lg + r;
         S[d][r] = from && row < a.dk ? a.init[global + (int64_t)row * a.dv] : 0.f;
       }
   }
 
-  // staging: what a lane loads of a tile of `cnt` tokens from token `at` on
-  Oct<T> kr[kGK], vr[kGV], qn[kGK];
-  float gn = 0.f;
+  // Staging.  Wave w's piece i is the (pieces a lane) * w + i-th kilobyte of
+  // an LDS copy, 16 bytes a lane; where that is in the matrix follows from the
+  // flips.  `at`: the places of the next tile in memory.
+  struct Source {
+    const T *q, *k, *v;
+    const float *g;
+  };
   const int64_t tok0 = sv.tok0(n);
-  const auto load_tile = [&](int at, int cnt) {
-    const T *kb = k + (tok0 + at) * a.ks + (int64_t)(h / a.rk) * a.dk;
-    const T *vb = v + (tok0 + at) * a.vs + (int64_t)(h / a.rv) * a.dv + col0;
-#pragma unroll
-    for (int i = 0; i < kGK; ++i) {
-      const int row = (i * 256 + tid) / (DK / 8), c = (i * 256 + tid) % (DK / 8) * 8;
-      kr[i] = load_oct(kb + row * (int)a.ks + c, row < cnt ? a.dk - c : 0);
-    }
-#pragma unroll
-    for (int i = 0; i < kGV; ++i) {
-      const int row = (i * 256 + tid) / 8, c = (i * 256 + tid) % 8 * 8;
-      vr[i] = load_oct(vb + row * (int)a.vs + c, row < cnt ? a.dv - col0 - c : 0);
-    }
-    if (w == 0)
-      gn = lane < cnt ? a.g[(tok0 + at + lane) * a.gs + h] : 0.f;
-    if (outputs) {
-      const T *qb = q + (tok0 + at) * a.qs + (int64_t)(h / a.rq) * a.dk;
-      const int row = 16 * w + lr;
-#pragma unroll
-      for (int i = 0; i < kGK; ++i)
-        qn[i] = load_oct(qb + row * (int)a.qs + 32 * i + 8 * lg, row < cnt ? a.dk - 32 * i - 8 * lg : 0);
-    }
+  const int ks = (int)a.ks, vs = (int)a.vs, qs = (int)a.qs, os = (int)a.os, gs = (int)a.gs;
+  const auto source = [&](int at) __attribute__((always_inline)) {
+    return Source{q + (tok0 + at) * a.qs + (int64_t)(h / a.rq) * a.dk,
+                  k + (tok0 + at) * a.ks + (int64_t)(h / a.rk) * a.dk,
+                  v + (tok0 + at) * a.vs + (int64_t)(h / a.rv) * a.dv + col0,
+                  a.g + (tok0 + at) * a.gs + h};
   };
-  // wave 0: log2 of the decay from the tile's start to each of its tokens
-  double G = 0.;
-  const auto scan_decays = [&](int cnt) {
-    G = lane < cnt ? (double)fmaxf(gn, kMinDecay) * kLog2E : 0.;
-    if (gn != gn)
-      G = __builtin_nan("");
-#pragma unroll
-    for (int b = 1; b < 64; b <<= 1) {
-      const double up = __shfl_up(G, b);
-      G += lane >= b ? up : 0.;
-    }
+  const auto piece = [&](auto ld, int per_lane, int i, int &row, int &col)
+      __attribute__((always_inline)) {
+    constexpr int LD = decltype(ld)::value, per = LD / kP;
+    const int at = (w * per_lane + i) * 64 + lane;
+    row = at / per;
+    col = ((at % per) ^ row_flip<T, LD>(row)) * kP;
   };
-  const auto put_decays = [&](int cnt) {
-    const double last = __shfl(G, cnt - 1);
-    const float hi = (float)G;
-    Ghi[lane] = hi;
-    Glo[lane] = (float)(G - (double)hi);
-    eG[lane] = exp2_of(G);
-    wts[lane] = lane < cnt ? exp2_of(last - G) : 0.f;
+  const auto stage = [&](auto ld, T *copy, const T *from, int stride, int width, int cnt,
+                         int per_lane, int i) __attribute__((always_inline)) {
+    int row, c;
+    piece(ld, per_lane, i, row, c);
+    T *to = copy + (w * per_lane + i) * 64 * kP;
+    if constexpr (FAST)
+      lds_request16(
+          raw_rsrc(from, cnt > 0 ? (uint32_t)(((cnt - 1) * stride + width) * kEs) : 0u),
+          c < width ? (row * stride + c) * kEs : kNowhere, to);
+    else
+      *reinterpret_cast<u32x4 *>(to + lane * kP) =
+          load_piece(from + row * stride + c, row < cnt ? width - c : 0);
+  };
+  using std::integral_constant;
+  typedef integral_constant<int, DK> RowDK;
+  typedef integral_constant<int, kCols> RowV;
+  // load i of a tile's 2 kNK + kNV (without q: the last kNK are left out)
+  const auto stage_one = [&](const Source &s, int cnt, int buf, int i)
+      __attribute__((always_inline)) {
+    if (i < kNK)
+      stage(RowDK(), Ks[buf], s.k, ks, a.dk, cnt, kNK, i);
+    else if (i < kNK + kNV)
+      stage(RowV(), Vs[buf], s.v, vs, cols, cnt, kNV, i - kNK);
+    else
+      stage(RowDK(), Qs[buf], s.q, qs, a.dk, cnt, kNK, i - kNK - kNV);
+  };
+  float gn = 0.f;
+  constexpr int kScan = NW - 1; // the wave that sums the decays (8 waves: it has no scores)
+  const auto load_g = [&](const Source &s, int cnt) __attribute__((always_inline)) {
+    if (w == kScan)
+      gn = lane < cnt ? s.g[lane * gs] : 0.f;
+  };
+
+  // The scan wave: G = log2 of the decay from the tile's start to each of its
+  // tokens, and what the chunk takes of it.
+  Pair G;
+  float g_exp, g_wt, g_all;
+  double decay_sum = 0.; // of the segment
+  const auto end_decays = [&](int cnt) __attribute__((always_inline)) { // of a chunk of cnt tokens
+    const Pair last = lane_pair(G, cnt - 1);
+    g_wt = lane < cnt ? exp2_of(last + -G) : 0.f;
+    g_all = exp2_of(last);
+  };
+  const auto scan_decays = [&](int cnt) __attribute__((always_inline)) {
+    if (w != kScan)
+      return;
+    G = prefix_sum(lane < cnt ? log2_decay(gn) : Pair{0.f, 0.f});
+    g_exp = exp2_of(G);
+    end_decays(cnt);
+  };
+  const auto put_decays = [&](int par) __attribute__((always_inline)) {
+    Ghi[par][lane] = G.hi;
+    Glo[par][lane] = G.lo;
+    eG[par][lane] = g_exp;
+    wts[par][lane] = g_wt;
     if (lane == 0)
-      total = exp2_of(last);
+      total[par] = g_all;
   };
-  const auto put_state = [&]() {
+  const auto count_decays = [&](int cnt) __attribute__((always_inline)) {
+    const Pair last = lane_pair(G, cnt - 1);
+    decay_sum += (double)last.hi + (double)last.lo;
+  };
+  // The first token of the staged tile that holds other than finite numbers
+  // in k or v (each wave looks at what it has staged itself).
+  const auto look = [&](int buf, int par) __attribute__((always_inline)) {
+    const auto at = [&](const T *copy, int per_lane, int i) __attribute__((always_inline)) {
+      return zero_sum(
+          *reinterpret_cast<const u32x4 *>(copy + ((w * per_lane + i) * 64 + lane) * kP), T());
+    };
+    float z = 0.f;
 #pragma unroll
-    for (int d = 0; d < kTD; ++d)
-      store4(Ss + my_col * kLdS + 16 * d + 4 * lg, S[d][0], S[d][1], S[d][2], S[d][3]);
-  };
-  // the tile into LDS; what it holds beside finite numbers is noted
-  const auto put_tile = [&]() {
+    for (int i = 0; i < kNK; ++i)
+      z += at(Ks[buf], kNK, i);
+#pragma unroll
+    for (int i = 0; i < kNV; ++i)
+      z += at(Vs[buf], kNV, i);
     int bad = kDC;
-#pragma unroll
-    for (int i = 0; i < kGK; ++i) {
-      const int row = (i * 256 + tid) / (DK / 8), c = (i * 256 + tid) % (DK / 8) * 8;
-      to_lds(Ks + row * kLdK + c, kr[i]);
-      if (non_finite(kr[i]))
-        bad = min(bad, row);
-    }
-#pragma unroll
-    for (int i = 0; i < kGV; ++i) {
-      const int row = (i * 256 + tid) / 8, c = (i * 256 + tid) % 8 * 8;
-      to_lds(Vs + row * kLdV + c, vr[i]);
-      if (non_finite(vr[i]))
-        bad = min(bad, row);
-    }
-    if (__any(bad < kDC))
+    if (__builtin_expect(__any(z != z), 0)) {
+      int row, c;
+      for (int i = 0; i < kNK; ++i) {
+        piece(RowDK(), kNK, i, row, c);
+        const float x = at(Ks[buf], kNK, i);
+        bad = x != x ? min(bad, row) : bad;
+      }
+      for (int i = 0; i < kNV; ++i) {
+        piece(RowV(), kNV, i, row, c);
+        const float x = at(Vs[buf], kNV, i);
+        bad = x != x ? min(bad, row) : bad;
+      }
       for (int b = 1; b < 64; b <<= 1)
         bad = min(bad, __shfl_xor(bad, b));
+    }
     if (lane == 0)
-      first_bad[w] = bad;
+      first_bad[par][w] = bad;
+  };
+  // The first token of the tile alone, its products in fp32: the state, and o
+  // from the state after it (this lane's rows, summed over the four lane
+  // groups).
+  const auto one_token = [&](auto out_tag, int buf, int par) __attribute__((always_inline)) {
+    // (rare: opaque, lest its addresses and conditions be kept in registers
+    // through every chunk)
+    const int group = opaque_lane() >> 4;
+    const T *qb = q + (tok0 + pos) * a.qs + (int64_t)(h / a.rq) * a.dk;
+    const float x = to_f32(Vs[buf][lds_at<T, kCols>(0, my_col)]), all = total[par];
+    float sum = 0.f;
+#pragma unroll
+    for (int d = 0; d < kTD; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = state_tile(d) + 8 * group + r;
+        S[d][r] = fmaf(to_f32(Ks[buf][lds_at<T, DK>(0, row)]), x, all * S[d][r]);
+        if (decltype(out_tag)::value && row < a.dk)
+          sum = fmaf(to_f32(qb[row]), S[d][r], sum);
+      }
+    if constexpr (decltype(out_tag)::value) {
+      sum = add_xor32(add_xor16(sum));
+      if (lg == 0 && my_col < cols)
+        o[(tok0 + pos) * a.os + (int64_t)h * a.dv + col0 + my_col] = from_f32<T>(sum * a.scale);
+    }
   };
 
-  double decay_sum = 0.; // (wave 0, lane 0) of the segment
-  int cnt = min(kDC, end - pos);
-  if (cnt > 0) {
-    load_tile(pos, cnt);
-    if (w == 0)
-      scan_decays(cnt);
+  // this lane's places in the LDS matrices: rows of fragments, and transposed
+  const int frag0 = lds_at<T, DK>(lr, 8 * lg);
+  int k_tr[kTrAt<T>], v_tr[kTrAt<T>];
+#pragma unroll
+  for (int r = 0; r < kTrAt<T>; ++r) {
+    const int row = 4 * lg + (sizeof(T) == 4 ? r : lr >> 2), m = sizeof(T) == 4 ? lr : 4 * (lr & 3);
+    k_tr[r] = lds_at<T, DK>(row, state_row(m));
+    v_tr[r] = lds_at<T, kCols>(row, 16 * w + m);
   }
-  while (cnt > 0) {
-    // (every wave is done with the tile before)
-    put_tile();
-    if (outputs)
-      put_state();
-    if (w == 0)
-      put_decays(cnt);
-    lds_barrier();
-    const int bad = min(min(first_bad[0], first_bad[1]), min(first_bad[2], first_bad[3]));
-    if (bad < cnt) {
-      cnt = max(1, bad);
-      lds_barrier();
-      for (int i = tid; i < (kDC - cnt) * kLdK; i += 256)
-        Ks[cnt * kLdK + i] = from_f32<T>(0.f);
-      for (int i = tid; i < (kDC - cnt) * kLdV; i += 256)
-        Vs[cnt * kLdV + i] = from_f32<T>(0.f);
-      if (w == 0)
-        put_decays(cnt);
-      lds_barrier();
-    }
-    if (w == 0)
-      decay_sum += __shfl(G, cnt - 1);
-    Frag<T> qf[kGK];
-#pragma unroll
-    for (int i = 0; i < kGK; ++i)
-      qf[i] = as_frag(qn[i]);
-    const int next = pos + cnt, next_cnt = min(kDC, end - next);
-    if (next_cnt > 0)
-      load_tile(next, next_cnt);
 
-    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-    if (outputs && 16 * w < cnt) {
-      // o^T of this wave's tokens: tile e, lane (lr, lg) element r is column
-      // 32 (e / 2) + 8 lg + 4 (e % 2) + r of token 16 w + lr
-      f32x4 O[4] = {zero, zero, zero, zero};
+  // Walks the segment's tokens; OUT: with outputs.
+  const auto walk = [&](auto out_tag) __attribute__((always_inline)) {
+    constexpr bool OUT = decltype(out_tag)::value;
+    constexpr int kLoads = kNK + kNV + (OUT ? kNK : 0);
+    int cnt = min(kDC, end - pos), buf = 0, par = 0;
+    if (cnt <= 0)
+      return;
+    const auto first_loads = [&]() __attribute__((always_inline)) {
+      const Source s = source(pos);
+      if constexpr (AHEAD)
 #pragma unroll
-      for (int s = 0; s < kGK; ++s)
+        for (int i = 0; i < kLoads; ++i)
+          stage_one(s, cnt, buf, i);
+      load_g(s, cnt);
+      scan_decays(cnt);
+    };
+    first_loads();
+    while (true) {
+      if constexpr (!AHEAD) { // (every wave is done with the tile before)
+        const Source s = source(pos);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mma(O[e], load_frag(Ss + val_col(e)(lr) * kLdS + 32 * s + 8 * lg), qf[s]);
-      const int i = 16 * w + lr;
-      const float ei = eG[i], hi = Ghi[i], lo = Glo[i];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        O[e] *= ei;
-      for (int c = 0; c <= w >> 1; ++c) {
-        f32x4 P[2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          P[t] = zero;
-          const int j0 = 32 * c + 16 * t;
-          if (j0 > 16 * w)
-            continue;
-#pragma unroll
-          for (int s = 0; s < kGK; ++s)
-            mma(P[t], load_frag(Ks + (j0 + lr) * kLdK + 32 * s + 8 * lg), qf[s]);
-          const f32x4 jh = *reinterpret_cast<const f32x4 *>(Ghi + j0 + 4 * lg);
-          const f32x4 jl = *reinterpret_cast<const f32x4 *>(Glo + j0 + 4 * lg);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float d = __builtin_amdgcn_exp2f((hi - jh[r]) + (lo - jl[r]));
-            P[t][r] = j0 + 4 * lg + r <= i ? P[t][r] * d : 0.f;
-          }
-        }
-        const Frag<T> pf = pack_scores(P[0], P[1], T());
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mma(O[e], tr_frag(Vs, kLdV, 32 * c, lr, lg, val_col(e)), pf);
+        for (int i = 0; i < kLoads; ++i)
+          stage_one(s, cnt, buf, i);
       }
-      if (i < cnt) {
-        T *op = o + (tok0 + pos + i) * a.os + (int64_t)h * a.dv + col0;
+      if (w == kScan)
+        put_decays(par);
+      wait_vmem_all(); // this wave's pieces are in LDS
+      look(buf, par);
+      lds_barrier();
+      int bad = first_bad[par][0];
 #pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          const int c = 32 * (e >> 1) + 8 * lg, left = a.dv - col0 - c;
-          float x[8];
+      for (int i = 1; i < NW; ++i)
+        bad = min(bad, first_bad[par][i]);
+      bad = __builtin_amdgcn_readfirstlane(bad);
+      if (__builtin_expect(bad < cnt, 0)) {
+        cnt = max(1, bad);
+        lds_barrier();
+        if (w == kScan) {
+          end_decays(cnt);
+          put_decays(par);
+          count_decays(cnt);
+        }
+        if (bad > 0) { // the tokens in front of it
+          for (int i = tid; i < (kDC - cnt) * DK; i += 64 * NW)
+            Ks[buf][cnt * DK + i] = from_f32<T>(0.f);
+          for (int i = tid; i < (kDC - cnt) * kCols; i += 64 * NW)
+            Vs[buf][cnt * kCols + i] = from_f32<T>(0.f);
+        }
+        lds_barrier();
+        if (bad == 0) { // itself, by the recurrence
+          one_token(out_tag, buf, par);
+          if (++pos == end)
+            break;
+          cnt = min(kDC, end - pos);
+          lds_barrier();
+          first_loads();
+          par ^= 1;
+          continue;
+        }
+      } else if (w == kScan) {
+        count_decays(cnt);
+      }
+      // The next chunk's loads, one here and one there: all at once, they wait
+      // for each other.
+      const int next = pos + cnt, next_cnt = min(kDC, end - next);
+      const Source s = source(next);
+      constexpr int kSteps = OUT ? 16 : 4;
+      const auto request = [&](int step) __attribute__((always_inline)) {
+        if constexpr (AHEAD)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            x[r] = O[e][r] * a.scale;
-            x[4 + r] = O[e + 1][r] * a.scale;
-          }
-          if (left >= 8) {
-            if constexpr (std::is_same<T, float>::value) {
-              *reinterpret_cast<f32x4_any *>(op + c) = f32x4{x[0], x[1], x[2], x[3]};
-              *reinterpret_cast<f32x4_any *>(op + c + 4) = f32x4{x[4], x[5], x[6], x[7]};
-            } else {
-              *reinterpret_cast<u32x4_any *>(op + c) = __builtin_bit_cast(u32x4, pack8(x).v);
+          for (int i = 0; i < kLoads; ++i)
+            if (i * kSteps / kLoads == step)
+              stage_one(s, next_cnt, buf ^ 1, i);
+      };
+      load_g(s, next_cnt);
+      const T *Qb = Qs[buf], *Kb = Ks[buf], *Vb = Vs[buf];
+      const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+      Frag<T> vf[2]; // this wave's columns of V, tokens 0 .. 31 and 32 .. 63
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        vf[c] = tr_frag(Vb + 32 * c * kCols, kCols, v_tr, 0);
+
+      if constexpr (OUT) {
+        // Scores: unit u is tokens 16 t .. of q against tokens 32 c .. of k,
+        // (t, c) = (u, 0), and (2, 1), (3, 1) for u = 4, 5; the others are
+        // above the diagonal.  Unit u is wave u % NW's.
+        f32x4 P[2][2];
+        const auto unit_of = [&](int y, int &t, int &c) __attribute__((always_inline)) {
+          const int u = w + y * NW;
+          t = u < 4 ? u : u - 2;
+          c = u < 4 ? 0 : 1;
+          return u < 6;
+        };
+        constexpr int kUnits = NW == 8 ? 1 : 2;
+#pragma unroll
+        for (int y = 0; y < kUnits; ++y) {
+          int t, c;
+          P[y][0] = P[y][1] = zero;
+          if (unit_of(y, t, c)) {
+#pragma unroll
+            for (int x = 0; x < kGQ; ++x) {
+              const Frag<T> qf = lds_frag(Qb + 16 * t * DK, frag0 ^ 32 * x);
+#pragma unroll
+              for (int g = 0; g < 2; ++g)
+                mma(P[y][g], lds_frag(Kb + (32 * c + 16 * g) * DK, frag0 ^ 32 * x), qf);
             }
-          } else {
+          }
+        }
+        // o^T of this wave's columns from the entering state: tile t, element
+        // r is column 4 lg + r of token 16 t + lr
+        f32x4 O[4] = {zero, zero, zero, zero};
+        {
+          Frag<T> f[2][4];
+          const auto read_q = [&](int x) __attribute__((always_inline)) {
 #pragma unroll
-            for (int r = 0; r < 7; ++r)
-              if (r < left)
-                op[c + r] = from_f32<T>(x[r]);
+            for (int t = 0; t < 4; ++t)
+              f[x & 1][t] = lds_frag(Qb + 16 * t * DK, frag0 ^ 32 * x);
+          };
+          read_q(0);
+#pragma unroll
+          for (int x = 0; x < kGQ; ++x) {
+            reads_stay();
+            if (x + 1 < kGQ)
+              read_q(x + 1);
+#pragma unroll
+            for (int y = x * 8 / kGQ; y < (x + 1) * 8 / kGQ; ++y)
+              request(y);
+            const Frag<T> sf = pack_scores(S[2 * x], S[2 * x + 1], T());
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              mma(O[t], sf, f[x & 1][t]);
+          }
+          reads_stay();
+        }
+        const float *gh = Ghi[par], *gl = Glo[par];
+        T *Pb = OWN_P ? Ps : Qs[buf];
+        if constexpr (!OWN_P)
+          lds_barrier(); // every wave has read q
+#pragma unroll
+        for (int y = 0; y < kUnits; ++y) {
+          int t, c;
+          if (unit_of(y, t, c)) {
+            const int i = 16 * t + lr;
+            const float hi = gh[i], lo = gl[i];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const int j0 = 32 * c + 16 * g + 4 * lg;
+              const f32x4 jh = *reinterpret_cast<const f32x4 *>(gh + j0);
+              const f32x4 jl = *reinterpret_cast<const f32x4 *>(gl + j0);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const float d = __builtin_amdgcn_exp2f((hi - jh[r]) + (lo - jl[r]));
+                P[y][g][r] = j0 + r <= i ? P[y][g][r] * d : 0.f;
+              }
+            }
+            put_frag(Pb + (2 * t + c) * 512, lane, pack_scores(P[y][0], P[y][1], T()));
+          }
+        }
+        lds_barrier(); // the scores are there
+        T *ob = o + (tok0 + pos) * a.os + (int64_t)h * a.dv + col0;
+        const auto ro =
+            buffer_rsrc(ob, (uint32_t)(((cnt - 1) * os + cols) * kEs));
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int i = 16 * t + lr;
+          O[t] *= eG[par][i];
+#pragma unroll
+          for (int c = 0; c <= t >> 1; ++c)
+            mma(O[t], vf[c], get_frag(Pb + (2 * t + c) * 512, lane));
+          O[t] *= a.scale;
+          const int c = 16 * w + 4 * lg;
+          if constexpr (FAST) {
+            const int at = c < cols ? (i * os + c) * kEs : kNowhere;
+            if constexpr (kEs == 2) {
+              typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
+              typedef uint32_t u32x2_t4 __attribute__((ext_vector_type(2)));
+              bf16x4_t y;
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                y[r] = static_cast<bf16>(O[t][r]);
+              __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t4, y), ro, at, 0, 0);
+            } else {
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[t]), ro, at, 0, 0);
+            }
+          } else if (i < cnt) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (c + r < cols)
+                ob[i * os + c + r] = from_f32<T>(O[t][r]);
           }
         }
       }
-    }
 
-    const float all = total;
-    if (cnt == 1) { // a token alone: its products are exact
-      const float x = to_f32(Vs[my_col]);
-#pragma unroll
-      for (int d = 0; d < kTD; ++d)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          S[d][r] = fmaf(to_f32(Ks[16 * d + 4 * lg + r]), x, all * S[d][r]);
-    } else {
+      // The state's update, four row tiles at a time, each four's operands
+      // read while the ones before are multiplied.
+      const float all = total[par];
 #pragma unroll
       for (int d = 0; d < kTD; ++d)
         S[d] *= all;
+      constexpr int kBatch = kTD / 4;
+      Frag<T> kf[2][4];
+      const auto read_k = [&](int b) __attribute__((always_inline)) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const f32x4 w0 = *reinterpret_cast<const f32x4 *>(wts + 32 * s + 4 * lg);
-        const f32x4 w1 = *reinterpret_cast<const f32x4 *>(wts + 32 * s + 16 + 4 * lg);
-        const auto vw = weigh(tr_frag(Vs, kLdV, 32 * s, lr, lg, val_col(w)), w0, w1);
+        for (int d = 0; d < 4; ++d)
+          kf[b & 1][d] = tr_frag(Kb + 32 * (b / kBatch) * DK, DK, k_tr,
+                                 state_tile(b % kBatch * 4 + d));
+      };
+      read_k(0);
 #pragma unroll
-        for (int d = 0; d < kTD; ++d) {
-          const Frag<T> kf = tr_frag(Ks, kLdK, 32 * s, lr, lg, row_col(d));
+      for (int x = 0; x < 2; ++x) {
+        const f32x4 w0 = *reinterpret_cast<const f32x4 *>(wts[par] + 32 * x + 4 * lg);
+        const f32x4 w1 = *reinterpret_cast<const f32x4 *>(wts[par] + 32 * x + 16 + 4 * lg);
+        const auto vw = weigh(vf[x], w0, w1);
+#pragma unroll
+        for (int b = x * kBatch; b < (x + 1) * kBatch; ++b) {
+          reads_stay();
+          if (b + 1 < 2 * kBatch)
+            read_k(b + 1);
+          constexpr int kFirst = OUT ? 8 : 0, kHere = kSteps - kFirst;
+#pragma unroll
+          for (int y = kFirst + b * kHere / (2 * kBatch); y < kFirst + (b + 1) * kHere / (2 * kBatch); ++y)
+            request(y);
 #pragma unroll
           for (const auto &p : vw.part)
-            mma(S[d], kf, p);
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+              mma(S[b % kBatch * 4 + d], kf[b & 1][d], p);
         }
       }
-    }
-    pos = next;
-    cnt = next_cnt;
-    if (cnt > 0 && w == 0)
+      if (next_cnt <= 0)
+        break;
+      pos = next;
+      cnt = next_cnt;
+      par ^= 1;
       scan_decays(cnt);
-    lds_barrier();
-  }
+      if constexpr (AHEAD)
+        buf ^= 1;
+      else
+        lds_barrier();
+    }
+  };
+  if (pass == 1 || seg == 0)
+    walk(std::true_type());
+  else
+    walk(std::false_type());
 
   if (seg < nseg - 1) { // (pass 0)
     float *to = pairs + seg * pair_step;
 #pragma unroll
     for (int d = 0; d < kTD; ++d)
-      *reinterpret_cast<f32x4 *>(to + d * 1024) = S[d];
-    if (tid == 0 && slice == 0)
+      *reinterpret_cast<f32x4 *>(to + d * 256 * NW) = S[d];
+    if (tid == 64 * kScan && slice == 0)
       a.pair_decay[(pair0 + seg) * a.H + h] = decay_sum;
-  } else if (a.fin && kept && col0 + my_col < a.dv) {
+  } else if (a.fin && kept && my_col < cols) {
 #pragma unroll
     for (int d = 0; d < kTD; ++d)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int row = 16 * d + 4 * lg + r;
+        const int row = state_tile(d) + 8 * lg + r;
         if (row < a.dk)
           a.fin[global + (int64_t)row * a.dv] = S[d][r];
       }
@@ -518,13 +796,16 @@ __global__ __launch_bounds__(256) void decay_fold_kernel(SeqTable tab, DecayArgs
   f32x4 S = *p;
   for (int64_t i = pair0 + 1; i < last; ++i) {
     p += step;
-    S = *p + exp2_of(a.pair_decay[i * a.H + h]) * S;
+    const double x = a.pair_decay[i * a.H + h];
+    const float hi = (float)x;
+    S = *p + exp2_of(Pair{hi, (float)(x - (double)hi)}) * S;
     *p = S;
   }
 }
 
 // ---- single tokens ----------------------------------------------------------------
 
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
 constexpr int kStepRows = 16; // state rows a lane has in flight
 
 // A workgroup per (row, head): 2^lanes_log2 lanes a state row, four columns
@@ -641,13 +922,20 @@ DecayArgs decay_args(const DecayCall &c) {
 namespace {
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 int padded_dk(int dk) { return dk <= 64 ? 64 : dk <= 128 ? 128 : 256; }
+// Waves of a workgroup: 16 value columns each.  Heads of more than 128 keys
+// leave no registers (fp32: no LDS) for eight.
+int waves_of(int dk, int dv) { return dv <= 64 || dk > 128 ? 4 : 8; }
+int slices_of(int dk, int dv) {
+  const int cols = 16 * waves_of(dk, dv);
+  return (dv + cols - 1) / cols;
+}
 int64_t num_segments(int64_t len, int64_t seg) { return len <= seg ? 1 : (len + seg - 1) / seg; }
 } // namespace
 
 DecayPlan decay_plan(int32_t num_seqs, const int64_t *cu, int32_t H, int32_t dk, int32_t dv,
-                     int, int32_t split_hint) {
+                     int32_t split_hint) {
   DecayPlan p{};
-  const int64_t slices = (dv + kDCols - 1) / kDCols;
+  const int64_t slices = slices_of(dk, dv), cols = 16 * waves_of(dk, dv);
   int64_t longest = 0;
   for (int32_t n = 0; n < num_seqs; ++n)
     longest = std::max(longest, cu[n + 1] - cu[n]);
@@ -656,16 +944,15 @@ DecayPlan decay_plan(int32_t num_seqs, const int64_t *cu, int32_t H, int32_t dk,
   if (split_hint > 1) {
     p.seg = whole((longest + split_hint - 1) / split_hint);
   } else if (split_hint == 0) {
-    const int64_t seg =
-        std::max<int64_t>(256, whole((cu[num_seqs] * H * slices + 511) / 512));
-    if (longest >= 3 * seg)
+    const int64_t seg = std::max<int64_t>(256, whole((cu[num_seqs] * H * slices + 255) / 256));
+    if (2 * longest >= 5 * seg)
       p.seg = seg;
   }
   for (int32_t n = 0; n < num_seqs; ++n)
     p.pairs += num_segments(cu[n + 1] - cu[n], p.seg) - 1;
   size_t at = seq_table_bytes(num_seqs);
   p.off_state = at;
-  at = up(at + (size_t)p.pairs * H * slices * kDCols * padded_dk(dk) * sizeof(float));
+  at = up(at + (size_t)p.pairs * H * slices * cols * padded_dk(dk) * sizeof(float));
   p.off_decay = at;
   p.total = up(at + (size_t)p.pairs * H * sizeof(double));
   return p;
@@ -674,7 +961,8 @@ DecayPlan decay_plan(int32_t num_seqs, const int64_t *cu, int32_t H, int32_t dk,
 hipError_t launch_decay(int elt, const DecayCall &c, int32_t num_seqs, const int64_t *cu,
                         const DecayPlan &plan, void *ws, hipStream_t s) {
   DecayArgs a = decay_args(c);
-  a.slices = (a.dv + kDCols - 1) / kDCols;
+  const int waves = waves_of(a.dk, a.dv);
+  a.slices = slices_of(a.dk, a.dv);
   a.seg = (int32_t)plan.seg;
   a.pair_state = (float *)((uint8_t *)ws + plan.off_state);
   a.pair_decay = (double *)((uint8_t *)ws + plan.off_decay);
@@ -689,10 +977,10 @@ hipError_t launch_decay(int elt, const DecayCall &c, int32_t num_seqs, const int
   int64_t grid[2];
   for (int pass = 0; pass < 2; ++pass) {
     grid[pass] = (total[pass] * a.H + 7) / 8 * 8 * a.slices;
-    if (grid[pass] * 256 > UINT32_MAX)
+    if (grid[pass] * 64 * waves > UINT32_MAX)
       return hipErrorInvalidConfiguration;
   }
-  const int per = a.slices * padded_dk(a.dk) / 16; // blocks of a state
+  const int per = a.slices * waves * padded_dk(a.dk) / 64; // blocks of a state
   const int64_t fold = total[2] * a.H * per;
   if (fold * 256 > UINT32_MAX)
     return hipErrorInvalidConfiguration;
@@ -700,12 +988,22 @@ hipError_t launch_decay(int elt, const DecayCall &c, int32_t num_seqs, const int
   const hipError_t e = make_seq_table(tab, num_seqs, cu, tiles, ws, s);
   if (e != hipSuccess)
     return e;
-  const auto run = [&](auto tag, auto dk) {
+  const size_t es = elt == 1 ? 2 : 4;
+  const auto even = [es](const void *p, int64_t stride) {
+    return ((uintptr_t)p & 15u) == 0 && stride * es % 16 == 0;
+  };
+  const bool fast = a.dk * es % 16 == 0 && a.dv * es % 16 == 0 && even(c.io.q, a.qs) && even(c.io.k, a.ks) &&
+                    even(c.io.v, a.vs) && even(c.io.o, a.os);
+  const auto run = [&](auto tag, auto dk, auto nw) {
     using T = decltype(tag);
+    constexpr int DK = decltype(dk)::value, NW = decltype(nw)::value;
     const auto chunks = [&](int pass) {
       a.units = total[pass] * a.H;
-      decay_chunk_kernel<T, decltype(dk)::value><<<(unsigned)grid[pass], 256, 0, s>>>(
-          tab, a, pass, (const T *)c.io.q, (const T *)c.io.k, (const T *)c.io.v, (T *)c.io.o);
+      const auto kernel =
+          fast ? decay_chunk_kernel<T, DK, NW, true> : decay_chunk_kernel<T, DK, NW, false>;
+      kernel<<<(unsigned)grid[pass], 64 * NW, 0, s>>>(tab, a, pass, (const T *)c.io.q,
+                                                      (const T *)c.io.k, (const T *)c.io.v,
+                                                      (T *)c.io.o);
     };
     chunks(0);
     if (fold > 0)
@@ -714,13 +1012,20 @@ hipError_t launch_decay(int elt, const DecayCall &c, int32_t num_seqs, const int
       chunks(1);
     return hipGetLastError();
   };
+  using std::integral_constant;
+  const auto wide = [&](auto tag, auto dk) {
+    if (waves == 4)
+      return run(tag, dk, integral_constant<int, 4>());
+    if constexpr (decltype(dk)::value <= 128)
+      return run(tag, dk, integral_constant<int, 8>());
+    return hipErrorInvalidConfiguration; // (waves_of gives these four)
+  };
   const auto sized = [&](auto tag) {
-    using std::integral_constant;
     if (a.dk <= 64)
-      return run(tag, integral_constant<int, 64>());
+      return wide(tag, integral_constant<int, 64>());
     if (a.dk <= 128)
-      return run(tag, integral_constant<int, 128>());
-    return run(tag, integral_constant<int, 256>());
+      return wide(tag, integral_constant<int, 128>());
+    return wide(tag, integral_constant<int, 256>());
   };
   return elt == 1 ? sized(bf16()) : sized(float());
 }
