@@ -26,10 +26,12 @@ struct DecayCall {
 struct DecayPlan {
   int64_t seg;
   int64_t pairs; // transition pairs of all cut sequences
+  int waves;     // of a workgroup, 16 value columns each
+  bool streams;  // where rows are aligned: a workgroup for each chain, none cut
   size_t off_state, off_decay, total; // workspace layout (the table first)
 };
-DecayPlan decay_plan(int32_t num_seqs, const int64_t *cu, int32_t H, int32_t dk, int32_t dv,
-                     int32_t split_hint);
+DecayPlan decay_plan(int elt, int32_t num_seqs, const int64_t *cu, int32_t H, int32_t dk,
+                     int32_t dv, int32_t split_hint);
 
 hipError_t launch_decay(int elt, const DecayCall &c, int32_t num_seqs, const int64_t *cu,
                         const DecayPlan &plan, void *ws, hipStream_t s);

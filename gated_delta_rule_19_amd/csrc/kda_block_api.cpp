@@ -78,7 +78,7 @@ size_t kda_decay_attention_workspace_size(int32_t num_seqs, const int64_t *cu_se
   if (!good_cu(num_seqs, cu_seqlens_host) || check_decay(H, dk, dv, dt) != KDA_OK ||
       split_hint < 0)
     return 0;
-  return decay_plan(num_seqs, cu_seqlens_host, H, dk, dv, split_hint).total;
+  return decay_plan(elt_of(dt), num_seqs, cu_seqlens_host, H, dk, dv, split_hint).total;
 }
 
 kda_status kda_decay_attention(int32_t num_seqs, const int64_t *cu_seqlens_host, int32_t H,
@@ -104,7 +104,7 @@ kda_status kda_decay_attention(int32_t num_seqs, const int64_t *cu_seqlens_host,
       (initial_state != final_state && overlap(init, fin)))
     return KDA_ERR_INVALID_ARG;
   const DecayPlan plan =
-      decay_plan(num_seqs, cu_seqlens_host, H, io->dk, io->dv, split_hint);
+      decay_plan(elt_of(dt), num_seqs, cu_seqlens_host, H, io->dk, io->dv, split_hint);
   st = check_workspace(plan.total, workspace, workspace_bytes);
   if (st != KDA_OK)
     return st;

@@ -295,6 +295,13 @@ __device__ __forceinline__ void reads_stay() { __builtin_amdgcn_sched_barrier(0x
 // whose bounds take the place of branches at a chunk's end, and q, K and V
 // straight into LDS.  AHEAD: a chunk ahead into the other one of two copies;
 // without, the loads of the one copy are waited for.
+//
+// 131072 tokens, 12 heads of 128, bf16: 780 us in 21 segments a head (2.5 TB/s
+// of the 1.6 GB of q, k, v, o and the second reading of k and v).  No unit is
+// full (matrix cores 27 %, VALU 36 %, LDS 39 %): what bounds it is the chain of
+// a chunk's products, its barriers and LDS round trips, 8700 cycles for 128
+// columns.  fp32 multiplies on the fp32 matrix instructions, at a sixteenth of
+// bf16's rate: bound by these.
 template <typename T, int DK, int NW> constexpr int kCopyBytes =
     kDC * (2 * DK + 16 * NW) * (int)sizeof(T);
 template <typename T, int DK, int NW, bool FAST>
@@ -736,8 +743,8 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
             read_k(b + 1);
           constexpr int kFirst = OUT ? 8 : 0, kHere = kSteps - kFirst;
 #pragma unroll
-          for (int y = kFirst + b * kHere / (2 * kBatch); y < kFirst + (b + 1) * kHere / (2 * kBatch); ++y)
-            request(y);
+          for (int y = b * kHere / (2 * kBatch); y < (b + 1) * kHere / (2 * kBatch); ++y)
+            request(kFirst + y);
 #pragma unroll
           for (const auto &p : vw.part)
 #pragma unroll
@@ -770,6 +777,373 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
     if (tid == 64 * kScan && slice == 0)
       a.pair_decay[(pair0 + seg) * a.H + h] = decay_sum;
   } else if (a.fin && kept && my_col < cols) {
+#pragma unroll
+    for (int d = 0; d < kTD; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = state_tile(d) + 8 * lg + r;
+        if (row < a.dk)
+          a.fin[global + (int64_t)row * a.dv] = S[d][r];
+      }
+  }
+}
+
+// Streams: uncut bf16 sequences of aligned rows and up to 128 keys a head, with
+// the work of a chunk spread over two kinds of waves, so that the chain of
+// chunks runs at the pace of the state's own products.  Four waves carry 16
+// columns of the state each (o from the entering state and from the scores, the
+// update).  Eight others are a chunk ahead of them and look at k and v and form
+// the scores, and two chunks ahead request q, K and V (straight into LDS) and
+// sum the decays.  One barrier a chunk.  Three copies of q, K, V and the decays
+// (chunk i % 3), two of the scores.
+//
+// 8192 tokens, 96 heads of 128: 192 workgroups, 292 us on the GPU, 4700 cycles a
+// chunk, of them 3600 of matrix products, transposed reads and roundings in the
+// state waves, the rest the wait for scores and decays.  With the same waves
+// doing both in turn a chunk took 7600.  Four score waves: 5200; a score wave
+// of two units and the wait for the decays behind it set the pace.
+template <int DK>
+__global__ __launch_bounds__(768, 3) void decay_stream_kernel(SeqTable tab, DecayArgs a,
+                                                              const bf16 *__restrict__ q,
+                                                              const bf16 *__restrict__ k,
+                                                              const bf16 *__restrict__ v,
+                                                              bf16 *__restrict__ o) {
+  typedef bf16 T;
+  const SeqView sv(tab);
+  constexpr int kEs = 2, kP = 8, NW = 4, NS = 8, kCols = 64;
+  constexpr int kGQ = DK / 32, kTD = DK / 16;
+  constexpr int kNK = DK / 64, kNV = 1; // pieces of K (q) and V a lane stages
+  __shared__ alignas(16) T Qs[3][kDC * DK], Ks[3][kDC * DK], Vs[3][kDC * kCols];
+  __shared__ alignas(16) T Ps[2][kDC * kDC];
+  __shared__ alignas(16) float Ghi[3][kDC], Glo[3][kDC], wts[3][kDC], eG[3][kDC];
+  __shared__ float total[3];
+  __shared__ alignas(16) int strange[2][NS];
+
+  const int64_t unit = (int64_t)(blockIdx.x / (8 * a.slices)) * 8 + blockIdx.x % 8;
+  if (unit >= a.units)
+    return;
+  const int slice = blockIdx.x / 8 % a.slices;
+  const int h = (int)(unit % a.H), blk = (int)(unit / a.H);
+  const int n = sv.find(blk, 0);
+  const int seq = sv.seq(n), end = sv.len(n);
+  int pos = 0;
+  const int64_t slot = a.slots ? a.slots[seq] : seq;
+  const bool kept = slot >= 0 && slot < a.num_slots;
+
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave < NW ? wave : wave - NW;
+  const int col0 = slice * kCols;
+  const int cols = min(kCols, a.dv - col0);
+  const int64_t tok0 = sv.tok0(n);
+  const int ks = (int)a.ks, vs = (int)a.vs, qs = (int)a.qs, os = (int)a.os, gs = (int)a.gs;
+  const T *q0 = q + tok0 * a.qs + (int64_t)(h / a.rq) * a.dk;
+  const T *k0 = k + tok0 * a.ks + (int64_t)(h / a.rk) * a.dk;
+  const T *v0 = v + tok0 * a.vs + (int64_t)(h / a.rv) * a.dv + col0;
+  const float *g0 = a.g + tok0 * a.gs + h;
+  T *o0 = o + tok0 * a.os + (int64_t)h * a.dv + col0;
+  const int frag0 = lds_at<T, DK>(lr, 8 * lg);
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  // whether a wave met other than finite numbers in k or v of chunk `par`
+  const auto any_strange = [&](int par) __attribute__((always_inline)) {
+    int any = 0;
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      any |= strange[par][i];
+    return __builtin_amdgcn_readfirstlane(any) != 0;
+  };
+
+  if (wave >= NW) {
+    // ---- scores ----
+    const auto stage = [&](auto ld, T *copy, const T *from, int stride, int width, int cnt,
+                           int per_lane, int i) __attribute__((always_inline)) {
+      constexpr int LD = decltype(ld)::value, per = LD / kP;
+      const int at = (w * per_lane + i) * 64 + lane, row = at / per;
+      const int c = ((at % per) ^ row_flip<T, LD>(row)) * kP;
+      lds_request16(raw_rsrc(from, (uint32_t)(((cnt - 1) * stride + width) * kEs)),
+                    c < width ? (row * stride + c) * kEs : kNowhere,
+                    copy + (w * per_lane + i) * 64 * kP);
+    };
+    using std::integral_constant;
+    const auto request = [&](int at, int copy) __attribute__((always_inline)) {
+      const int cnt = min(kDC, end - at);
+      if (cnt <= 0)
+        return;
+#pragma unroll
+      for (int i = 0; i < kNK; ++i)
+        stage(integral_constant<int, DK>(), Ks[copy], k0 + (int64_t)at * ks, ks, a.dk, cnt, kNK, i);
+#pragma unroll
+      for (int i = 0; i < kNK; ++i)
+        stage(integral_constant<int, DK>(), Qs[copy], q0 + (int64_t)at * qs, qs, a.dk, cnt, kNK, i);
+#pragma unroll
+      for (int i = 0; i < kNV; ++i)
+        stage(integral_constant<int, kCols>(), Vs[copy], v0 + (int64_t)at * vs, vs, cols, cnt, kNV,
+              i);
+    };
+    const auto load_g = [&](int at) __attribute__((always_inline)) {
+      return w == NS - 1 && lane < end - at ? g0[(int64_t)(at + lane) * gs] : 0.f;
+    };
+    const auto decays = [&](float gn, int at, int copy) __attribute__((always_inline)) {
+      if (w != NS - 1)
+        return;
+      const int cnt = max(1, min(kDC, end - at));
+      const Pair G = prefix_sum(lane < cnt ? log2_decay(gn) : Pair{0.f, 0.f});
+      const Pair last = lane_pair(G, cnt - 1);
+      Ghi[copy][lane] = G.hi;
+      Glo[copy][lane] = G.lo;
+      eG[copy][lane] = exp2_of(G);
+      wts[copy][lane] = lane < cnt ? exp2_of(last + -G) : 0.f;
+      if (lane == 0)
+        total[copy] = exp2_of(last);
+    };
+    // the chunk's k and v looked at, and its scores as operands: unit u is
+    // tokens 16 t .. of q against tokens 32 c .. of k, (t, c) = (u, 0), and
+    // (2, 1), (3, 1) for u = 4, 5; the others are above the diagonal
+    const auto scores = [&](int par, int copy) __attribute__((always_inline)) {
+      // (the last wave, which has the decays to sum, leaves its share to the
+      // one before)
+      float z = 0.f;
+      const auto check = [&](int share) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < kNK; ++i)
+          z += zero_sum(
+              *reinterpret_cast<const u32x4 *>(&Ks[copy][((share * kNK + i) * 64 + lane) * kP]),
+              T());
+#pragma unroll
+        for (int i = 0; i < kNV; ++i)
+          z += zero_sum(
+              *reinterpret_cast<const u32x4 *>(&Vs[copy][((share * kNV + i) * 64 + lane) * kP]),
+              T());
+      };
+      if (w != NS - 1)
+        check(w);
+      if (w == NS - 2)
+        check(NS - 1);
+      const bool met = __any(z != z);
+      if (lane == 0)
+        strange[par][w] = met;
+      const float *gh = Ghi[copy], *gl = Glo[copy];
+      const auto one = [&](int t, int c) __attribute__((always_inline)) {
+        f32x4 P[2] = {zero, zero};
+#pragma unroll
+        for (int x = 0; x < kGQ; ++x) {
+          const Frag<T> qf = lds_frag(Qs[copy] + 16 * t * DK, frag0 ^ 32 * x);
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+            mma(P[g], lds_frag(Ks[copy] + (32 * c + 16 * g) * DK, frag0 ^ 32 * x), qf);
+        }
+        const int i = 16 * t + lr;
+        const float hi = gh[i], lo = gl[i];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const int j0 = 32 * c + 16 * g + 4 * lg;
+          const f32x4 jh = *reinterpret_cast<const f32x4 *>(gh + j0);
+          const f32x4 jl = *reinterpret_cast<const f32x4 *>(gl + j0);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float d = __builtin_amdgcn_exp2f((hi - jh[r]) + (lo - jl[r]));
+            P[g][r] = j0 + r <= i ? P[g][r] * d : 0.f;
+          }
+        }
+        put_frag(&Ps[par][(2 * t + c) * 512], lane, pack_scores(P[0], P[1], T()));
+      };
+      if (w < 6)
+        one(w < 4 ? w : w - 2, w >> 2);
+    };
+    while (pos < end) {
+      request(pos, 0);
+      request(pos + kDC, 1);
+      const float ga = load_g(pos), gb = load_g(pos + kDC);
+      float gn = load_g(pos + 2 * kDC);
+      decays(ga, pos, 0);
+      decays(gb, pos + kDC, 1);
+      wait_vmem_all(); // this wave's pieces are in LDS
+      lds_barrier();
+      scores(0, 0);
+      lds_barrier();
+      bool met = false;
+      // copies of the chunks at hand, after it, and after that
+      for (int par = 0, c1 = 1, c2 = 2; pos < end; par ^= 1) {
+        met = any_strange(par);
+        if (__builtin_expect(met, 0))
+          break;
+        const float gc = gn; // (the next one's request early: it is waited for below)
+        gn = load_g(pos + 3 * kDC);
+        request(pos + 2 * kDC, c2);
+        if (pos + kDC < end)
+          scores(par ^ 1, c1);
+        decays(gc, pos + 2 * kDC, c2);
+        pos += kDC;
+        c1 = c2;
+        c2 = c2 == 2 ? 0 : c2 + 1;
+        wait_vmem_all();
+        lds_barrier();
+      }
+      if (met) { // (the chunk goes by the recurrence, and all begins again)
+        pos += kDC;
+        lds_barrier();
+      }
+    }
+    return;
+  }
+
+  // ---- states ----
+  const int my_col = 16 * w + lr; // of the state this lane holds
+  // the state that enters: element r of tile d is row state_tile(d) + 8 lg + r
+  // of column my_col
+  f32x4 S[kTD];
+  const int64_t global = (slot * a.H + h) * a.dk * a.dv + col0 + my_col;
+#pragma unroll
+  for (int d = 0; d < kTD; ++d)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = state_tile(d) + 8 * lg + r;
+      S[d][r] = a.init && kept && my_col < cols && row < a.dk
+                    ? a.init[global + (int64_t)row * a.dv]
+                    : 0.f;
+    }
+  int k_tr[1], v_tr[1];
+  k_tr[0] = lds_at<T, DK>(4 * lg + (lr >> 2), state_row(4 * (lr & 3)));
+  v_tr[0] = lds_at<T, kCols>(4 * lg + (lr >> 2), 16 * w + 4 * (lr & 3));
+  // Tokens one by one, by the recurrence and straight from memory: the state,
+  // and o from the state after a token (this lane's rows, summed over the four
+  // lane groups).
+  const auto by_token = [&](int count) __attribute__((always_inline)) {
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+      const int64_t at = pos + i;
+      // (rare: opaque, lest its conditions be kept in registers all along)
+      const int group = opaque_lane() >> 4;
+      const float decay = exp2_of(log2_decay(g0[at * gs]));
+      const float x = my_col < cols ? to_f32(v0[at * vs + my_col]) : 0.f;
+      float sum = 0.f;
+#pragma unroll
+      for (int d = 0; d < kTD; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = state_tile(d) + 8 * group + r;
+          const bool in = row < a.dk;
+          S[d][r] = fmaf(in ? to_f32(k0[at * ks + row]) : 0.f, x, decay * S[d][r]);
+          if (in)
+            sum = fmaf(to_f32(q0[at * qs + row]), S[d][r], sum);
+        }
+      sum = add_xor32(add_xor16(sum));
+      if (lg == 0 && my_col < cols)
+        o0[at * os + my_col] = static_cast<T>(sum * a.scale);
+    }
+  };
+  while (pos < end) {
+    lds_barrier();
+    lds_barrier();
+    bool met = false;
+    for (int par = 0, c0 = 0; pos < end; par ^= 1) {
+      met = any_strange(par);
+      if (__builtin_expect(met, 0))
+        break;
+      const T *Qb = Qs[c0], *Kb = Ks[c0], *Vb = Vs[c0];
+      Frag<T> vf[2]; // this wave's columns of V, tokens 0 .. 31 and 32 .. 63
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        vf[c] = tr_frag(Vb + 32 * c * kCols, kCols, v_tr, 0);
+      const float all = total[c0];
+      // o^T of this wave's columns: tile t, element r is column 4 lg + r
+      // of token 16 t + lr
+      f32x4 O[4] = {zero, zero, zero, zero};
+      Frag<T> f[2][4];
+      const auto read_q = [&](int x) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          f[x & 1][t] = lds_frag(Qb + 16 * t * DK, frag0 ^ 32 * x);
+      };
+      Frag<T> pf[4][2];
+      float ei[4];
+      const auto read_p = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          ei[t] = eG[c0][16 * t + lr];
+#pragma unroll
+          for (int c = 0; c <= t >> 1; ++c)
+            pf[t][c] = get_frag(&Ps[par][(2 * t + c) * 512], lane);
+        }
+      };
+      read_q(0);
+#pragma unroll
+      for (int x = 0; x < kGQ; ++x) {
+        reads_stay();
+        if (x + 1 < kGQ)
+          read_q(x + 1);
+        else
+          read_p();
+        const Frag<T> sf = pack_acc2(S[2 * x], S[2 * x + 1]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          mma(O[t], sf, f[x & 1][t]);
+      }
+      reads_stay();
+      const auto ro = buffer_rsrc(o0 + (int64_t)pos * os,
+                                  (uint32_t)(((min(kDC, end - pos) - 1) * os + cols) * kEs));
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        O[t] *= ei[t];
+#pragma unroll
+        for (int c = 0; c <= t >> 1; ++c)
+          mma(O[t], vf[c], pf[t][c]);
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int i = 16 * t + lr;
+        O[t] *= a.scale;
+        const int c = 16 * w + 4 * lg;
+        typedef uint32_t u32x2_o __attribute__((ext_vector_type(2)));
+        bf16x4 y;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          y[r] = static_cast<bf16>(O[t][r]);
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_o, y), ro,
+                                              c < cols ? (i * os + c) * kEs : kNowhere, 0, 0);
+      }
+      // The state's update, four row tiles at a time, each four's operands
+      // read while the ones before are multiplied.
+#pragma unroll
+      for (int d = 0; d < kTD; ++d)
+        S[d] *= all;
+      constexpr int kBatch = kTD / 4;
+      Frag<T> kf[2][4];
+      const auto read_k = [&](int b) __attribute__((always_inline)) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          kf[b & 1][d] = tr_frag(Kb + 32 * (b / kBatch) * DK, DK, k_tr,
+                                 state_tile(b % kBatch * 4 + d));
+      };
+      read_k(0);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const f32x4 w0 = *reinterpret_cast<const f32x4 *>(wts[c0] + 32 * x + 4 * lg);
+        const f32x4 w1 = *reinterpret_cast<const f32x4 *>(wts[c0] + 32 * x + 16 + 4 * lg);
+        const Split3 vw = weigh(vf[x], w0, w1);
+#pragma unroll
+        for (int b = x * kBatch; b < (x + 1) * kBatch; ++b) {
+          reads_stay();
+          if (b + 1 < 2 * kBatch)
+            read_k(b + 1);
+#pragma unroll
+          for (const auto &p : vw.part)
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+              mma(S[b % kBatch * 4 + d], kf[b & 1][d], p);
+        }
+      }
+      pos += kDC;
+      c0 = c0 == 2 ? 0 : c0 + 1;
+      lds_barrier();
+    }
+    if (met) {
+      by_token(min(kDC, end - pos));
+      pos += kDC;
+      lds_barrier();
+    }
+  }
+
+  if (a.fin && kept && my_col < cols) {
 #pragma unroll
     for (int d = 0; d < kTD; ++d)
 #pragma unroll
@@ -922,37 +1296,62 @@ DecayArgs decay_args(const DecayCall &c) {
 namespace {
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 int padded_dk(int dk) { return dk <= 64 ? 64 : dk <= 128 ? 128 : 256; }
-// Waves of a workgroup: 16 value columns each.  Heads of more than 128 keys
-// leave no registers (fp32: no LDS) for eight.
-int waves_of(int dk, int dv) { return dv <= 64 || dk > 128 ? 4 : 8; }
-int slices_of(int dk, int dv) {
-  const int cols = 16 * waves_of(dk, dv);
-  return (dv + cols - 1) / cols;
-}
 int64_t num_segments(int64_t len, int64_t seg) { return len <= seg ? 1 : (len + seg - 1) / seg; }
 } // namespace
 
-DecayPlan decay_plan(int32_t num_seqs, const int64_t *cu, int32_t H, int32_t dk, int32_t dv,
-                     int32_t split_hint) {
+// How a call runs.  Measured (MI355X, 96 heads of 128, bf16 unless told):
+//
+// - Streams (four state waves, 64 columns a workgroup, one workgroup a CU) take
+//   1.9 us a chunk of 64 tokens, eight waves of the other kernel 3.6 us for
+//   128 columns, four 3.4 us for 64.  A stream for each chain is the fastest
+//   while all of them run at once: 8192 tokens, 192 streams: 292 us, the
+//   chunk kernel uncut 467, cut 375.  With more chains than CUs the others'
+//   wider blocks are: 16 x 2048 tokens: 868 us, streams 1008.  Four waves are
+//   for value heads that eight would leave half empty (32 sequences of 256
+//   tokens, 16 heads of 64: 25 us, eight waves 36, streams 30).
+// - A cut sequence is read twice for k and v and has three launches.  With
+//   streams it is worth it from five segments on (32 heads, 1024 tokens:
+//   cut in four 49 us, a stream 38; 2048: in eight 56, 64; 8192: 149, 227), where
+//   the chunk kernel would take a whole sequence from two and a half.
+// - fp32: 14.8 us a chunk with eight waves and 128 columns, 11.2 with four and
+//   64: four where the longest sequence sets the time (9001 tokens in 37 ragged
+//   sequences, 10 heads of 100: 160 us against 182), eight where the number of
+//   workgroups does (37 sequences of 243: 138 us against 148).
+constexpr int64_t kCUs = 256;
+
+DecayPlan decay_plan(int elt, int32_t num_seqs, const int64_t *cu, int32_t H, int32_t dk,
+                     int32_t dv, int32_t split_hint) {
   DecayPlan p{};
-  const int64_t slices = slices_of(dk, dv), cols = 16 * waves_of(dk, dv);
   int64_t longest = 0;
   for (int32_t n = 0; n < num_seqs; ++n)
     longest = std::max(longest, cu[n + 1] - cu[n]);
   const auto whole = [](int64_t x) { return std::max<int64_t>(kDC, (x + kDC - 1) / kDC * kDC); };
+  const auto slices = [dv](int waves) { return (dv + 16 * waves - 1) / (16 * waves); };
+  // tokens that each CU has to take when all are busy
+  const auto share = [&](int waves) {
+    return (cu[num_seqs] * H * slices(waves) + kCUs - 1) / kCUs;
+  };
+  // (heads of more than 128 keys leave no registers, in fp32 no LDS, for eight)
+  p.waves = dk > 128 || dv <= 64 ? 4 : 8;
+  p.streams = elt == 1 && dk <= 128 && dk % 8 == 0 && dv % 8 == 0 &&
+              (int64_t)num_seqs * H * slices(4) <= kCUs;
   p.seg = whole(longest);
   if (split_hint > 1) {
     p.seg = whole((longest + split_hint - 1) / split_hint);
   } else if (split_hint == 0) {
-    const int64_t seg = std::max<int64_t>(256, whole((cu[num_seqs] * H * slices + 255) / 256));
-    if (2 * longest >= 5 * seg)
+    const int64_t seg = std::max<int64_t>(256, whole(share(p.waves)));
+    if (2 * longest >= (p.streams ? 10 : 5) * seg)
       p.seg = seg;
   }
   for (int32_t n = 0; n < num_seqs; ++n)
     p.pairs += num_segments(cu[n + 1] - cu[n], p.seg) - 1;
+  p.streams = p.streams && p.pairs == 0;
+  if (elt != 1 && p.pairs == 0 && 3 * std::max(longest, share(4)) < 4 * std::max(longest, share(8)))
+    p.waves = 4;
   size_t at = seq_table_bytes(num_seqs);
   p.off_state = at;
-  at = up(at + (size_t)p.pairs * H * slices * cols * padded_dk(dk) * sizeof(float));
+  const size_t state = (size_t)slices(p.waves) * 16 * p.waves * padded_dk(dk) * sizeof(float);
+  at = up(at + (size_t)p.pairs * H * state);
   p.off_decay = at;
   p.total = up(at + (size_t)p.pairs * H * sizeof(double));
   return p;
@@ -961,8 +1360,15 @@ DecayPlan decay_plan(int32_t num_seqs, const int64_t *cu, int32_t H, int32_t dk,
 hipError_t launch_decay(int elt, const DecayCall &c, int32_t num_seqs, const int64_t *cu,
                         const DecayPlan &plan, void *ws, hipStream_t s) {
   DecayArgs a = decay_args(c);
-  const int waves = waves_of(a.dk, a.dv);
-  a.slices = slices_of(a.dk, a.dv);
+  const size_t es = elt == 1 ? 2 : 4;
+  const auto even = [es](const void *p, int64_t stride) {
+    return ((uintptr_t)p & 15u) == 0 && stride * es % 16 == 0;
+  };
+  const bool fast = a.dk * es % 16 == 0 && a.dv * es % 16 == 0 && even(c.io.q, a.qs) &&
+                    even(c.io.k, a.ks) && even(c.io.v, a.vs) && even(c.io.o, a.os);
+  const bool streams = plan.streams && fast;
+  const int waves = streams ? 4 : plan.waves;
+  a.slices = (a.dv + 16 * waves - 1) / (16 * waves);
   a.seg = (int32_t)plan.seg;
   a.pair_state = (float *)((uint8_t *)ws + plan.off_state);
   a.pair_decay = (double *)((uint8_t *)ws + plan.off_decay);
@@ -974,10 +1380,11 @@ hipError_t launch_decay(int elt, const DecayCall &c, int32_t num_seqs, const int
   int64_t total[kCounts];
   if (!seq_totals(num_seqs, cu, tiles, total))
     return hipErrorInvalidConfiguration;
+  const int threads = streams ? 768 : 64 * waves;
   int64_t grid[2];
   for (int pass = 0; pass < 2; ++pass) {
     grid[pass] = (total[pass] * a.H + 7) / 8 * 8 * a.slices;
-    if (grid[pass] * 64 * waves > UINT32_MAX)
+    if (grid[pass] * threads > UINT32_MAX)
       return hipErrorInvalidConfiguration;
   }
   const int per = a.slices * waves * padded_dk(a.dk) / 64; // blocks of a state
@@ -988,12 +1395,13 @@ hipError_t launch_decay(int elt, const DecayCall &c, int32_t num_seqs, const int
   const hipError_t e = make_seq_table(tab, num_seqs, cu, tiles, ws, s);
   if (e != hipSuccess)
     return e;
-  const size_t es = elt == 1 ? 2 : 4;
-  const auto even = [es](const void *p, int64_t stride) {
-    return ((uintptr_t)p & 15u) == 0 && stride * es % 16 == 0;
-  };
-  const bool fast = a.dk * es % 16 == 0 && a.dv * es % 16 == 0 && even(c.io.q, a.qs) && even(c.io.k, a.ks) &&
-                    even(c.io.v, a.vs) && even(c.io.o, a.os);
+  a.units = total[0] * a.H;
+  if (streams) {
+    const auto kernel = a.dk <= 64 ? decay_stream_kernel<64> : decay_stream_kernel<128>;
+    kernel<<<(unsigned)grid[0], threads, 0, s>>>(tab, a, (const bf16 *)c.io.q, (const bf16 *)c.io.k,
+                                                 (const bf16 *)c.io.v, (bf16 *)c.io.o);
+    return hipGetLastError();
+  }
   const auto run = [&](auto tag, auto dk, auto nw) {
     using T = decltype(tag);
     constexpr int DK = decltype(dk)::value, NW = decltype(nw)::value;
@@ -1001,7 +1409,7 @@ hipError_t launch_decay(int elt, const DecayCall &c, int32_t num_seqs, const int
       a.units = total[pass] * a.H;
       const auto kernel =
           fast ? decay_chunk_kernel<T, DK, NW, true> : decay_chunk_kernel<T, DK, NW, false>;
-      kernel<<<(unsigned)grid[pass], 64 * NW, 0, s>>>(tab, a, pass, (const T *)c.io.q,
+      kernel<<<(unsigned)grid[pass], threads, 0, s>>>(tab, a, pass, (const T *)c.io.q,
                                                       (const T *)c.io.k, (const T *)c.io.v,
                                                       (T *)c.io.o);
     };
@@ -1018,7 +1426,7 @@ hipError_t launch_decay(int elt, const DecayCall &c, int32_t num_seqs, const int
       return run(tag, dk, integral_constant<int, 4>());
     if constexpr (decltype(dk)::value <= 128)
       return run(tag, dk, integral_constant<int, 8>());
-    return hipErrorInvalidConfiguration; // (waves_of gives these four)
+    return hipErrorInvalidConfiguration; // (the plan gives these four)
   };
   const auto sized = [&](auto tag) {
     if (a.dk <= 64)
