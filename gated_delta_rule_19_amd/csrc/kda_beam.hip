@@ -11,13 +11,14 @@
 //     the parts' candidates in 64 bits, and takes the K best of them.
 // The part kernel finds its K largest without sorting them all: the K-th
 // largest of the lanes' own maxima has K elements at or above it, so only what
-// reaches it is collected and ranked.  A logit of -inf is never collected:
-// where fewer than K candidates are above -inf, the lowest (w, v) that are not
-// among them fill up the selection.
+// is above it is collected and ranked (elements of fewer than K lanes), and
+// where these are fewer than K the first ones equal to it follow.  A logit of
+// -inf is never collected: where fewer than K candidates are above -inf, the
+// lowest (w, v) that are not among them fill up the selection.
 //
 // Sums: exp from fp32 with its argument's rounding put back (about 2^-23
-// relative a term), added in 64 bits; so two beams' candidates change places
-// only if their values are that near.
+// relative a term), four of them added in fp32 and the fours in 64 bits; so two
+// beams' candidates change places only if their values are that near.
 //
 // Reordering.  One pass in place: a lane holds the same 16 bytes of all rows
 // of its group that change, loads them all, then stores them, so no order of
@@ -40,6 +41,8 @@ template <typename T> constexpr int kPart = kPartBytes / (int)sizeof(T);
 struct BeamArgs {
   int32_t B, W, V, K, eos, order;
   int32_t parts, groups_log2; // lane groups whose maxima set the threshold
+  int32_t lanes_log2;         // lanes that join a beam's parts
+  double inv_of_beam;         // 1 / (parts K)
   int64_t row_stride;
 };
 
@@ -53,44 +56,43 @@ struct PartSum {
   int32_t pad;
 };
 
-// Keys in the order of the selection: the value's order (-0 as 0) above the
-// complement of the place in the part.  Unique, and never 0 for a value above
-// -inf.
-template <typename T> struct KeyOf;
-template <> struct KeyOf<bf16> {
-  typedef uint32_t type; // 16 bits of value, 13 of place
-  static __device__ __forceinline__ uint32_t make(float x, int at) {
-    uint32_t u = __builtin_bit_cast(uint32_t, x + 0.f) >> 16;
-    u ^= u & 0x8000u ? 0xffffu : 0x8000u;
-    return u << 13 | (uint32_t)(kPart<bf16> - 1 - at);
+// The order of a type's values as unsigned numbers (-0 as 0).
+template <typename T> struct OrderOf;
+template <> struct OrderOf<bf16> {
+  static constexpr int kBits = 16;
+  static __device__ __forceinline__ uint32_t make(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x + 0.f) >> 16;
+    return u ^ (u & 0x8000u ? 0xffffu : 0x8000u);
   }
-  static __device__ __forceinline__ int place(uint32_t k) {
-    return kPart<bf16> - 1 - (int)(k & (kPart<bf16> - 1));
-  }
-  static __device__ __forceinline__ float value(uint32_t k) {
-    uint32_t u = k >> 13;
-    u ^= u & 0x8000u ? 0x8000u : 0xffffu;
-    return __builtin_bit_cast(float, u << 16);
+  static __device__ __forceinline__ float value(uint32_t u) {
+    return __builtin_bit_cast(float, (u ^ (u & 0x8000u ? 0x8000u : 0xffffu)) << 16);
   }
 };
-template <> struct KeyOf<float> {
-  typedef uint64_t type; // 32 bits of value, 12 of place
-  static __device__ __forceinline__ uint64_t make(float x, int at) {
-    uint32_t u = __builtin_bit_cast(uint32_t, x + 0.f);
-    u ^= u & 0x80000000u ? 0xffffffffu : 0x80000000u;
-    return (uint64_t)u << 12 | (uint64_t)(kPart<float> - 1 - at);
+template <> struct OrderOf<float> {
+  static constexpr int kBits = 32;
+  static __device__ __forceinline__ uint32_t make(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x + 0.f);
+    return u ^ (u & 0x80000000u ? 0xffffffffu : 0x80000000u);
   }
-  static __device__ __forceinline__ int place(uint64_t k) {
-    return kPart<float> - 1 - (int)(k & (kPart<float> - 1));
-  }
-  static __device__ __forceinline__ float value(uint64_t k) {
-    uint32_t u = (uint32_t)(k >> 12);
-    u ^= u & 0x80000000u ? 0x80000000u : 0xffffffffu;
-    return __builtin_bit_cast(float, u);
+  static __device__ __forceinline__ float value(uint32_t u) {
+    return __builtin_bit_cast(float, u ^ (u & 0x80000000u ? 0x80000000u : 0xffffffffu));
   }
 };
-static_assert(kPart<bf16> == 1 << 13 && kPart<float> == 1 << 12, "key layout");
-
+// Keys in the order of the selection: the value's order above the complement
+// of the place in the part.
+template <typename T> struct KeyOf {
+  typedef std::conditional_t<sizeof(T) == 2, uint32_t, uint64_t> type;
+  static constexpr int kPlaces = kPart<T>;
+  static __device__ __forceinline__ type make(float x, int at) {
+    return (type)OrderOf<T>::make(x) * kPlaces + (type)(kPlaces - 1 - at);
+  }
+  static __device__ __forceinline__ int place(type k) {
+    return kPlaces - 1 - (int)(k & (kPlaces - 1));
+  }
+  static __device__ __forceinline__ float value(type k) {
+    return OrderOf<T>::value((uint32_t)(k / kPlaces));
+  }
+};
 // eight elements with their type's alignment only
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
@@ -107,31 +109,26 @@ __device__ __forceinline__ void load8(const float *p, float *x) {
   }
 }
 
-__device__ __forceinline__ float lane_f32(float x, int lane) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+// the largest of a wave's values
+template <int CTRL, int ROWS> __device__ __forceinline__ float dpp_max(float x) {
+  const int u = __builtin_bit_cast(int, x);
+  return fmaxf(x, __builtin_bit_cast(
+                      float, __builtin_amdgcn_update_dpp(u, u, CTRL, ROWS, 0xf, false)));
+}
+__device__ __forceinline__ float wave_max(float x) {
+  x = dpp_max<0x111, 0xf>(x); // 1, 2, 4, 8 lanes within rows of 16
+  x = dpp_max<0x112, 0xf>(x);
+  x = dpp_max<0x114, 0xf>(x);
+  x = dpp_max<0x118, 0xf>(x);
+  x = dpp_max<0x142, 0xa>(x); // ends of rows to those behind
+  x = dpp_max<0x143, 0xc>(x);
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
 }
 __device__ __forceinline__ double lane_f64(double x, int lane) {
   const uint64_t u = __builtin_bit_cast(uint64_t, x);
   const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
   const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-
-// The K-th largest of the maxima of 2^groups_log2 >= K lane groups: at least K
-// elements of the wave reach it, or it is -inf.
-template <typename F, typename R>
-__device__ __forceinline__ F kth_of_groups(F m, int K, int groups_log2, R &&read_lane) {
-  const int lane = threadIdx.x & 63, width = 64 >> groups_log2;
-  for (int b = 1; b < width; b <<= 1) {
-    const F o = __shfl_xor(m, b);
-    m = o > m ? o : m;
-  }
-  int above = 0;
-  for (int g = 0; g < (1 << groups_log2); ++g) {
-    const F o = read_lane(m, g * width);
-    above += o > m || (o == m && g * width < (lane & -width));
-  }
-  return read_lane(m, __builtin_ctzll(__ballot(above == K - 1)));
 }
 
 // exp(d) for d <= 0: exp2 of the product with log2(e), whose rounding and the
@@ -144,19 +141,28 @@ __device__ __forceinline__ float exp_neg(float d) {
   return t < -126.f ? e : fmaf(e, r * ln2, e); // (there d may be -inf)
 }
 
+// 64 x 8 beams of 128001 bf16 logits: 8192 workgroups, 43 us (3.0 TB/s), bound
+// by the vector units: some 600 instructions a wave for 32 logits a lane, 12
+// for each exp with its sum, of about 32 us; the loads of the eight workgroups
+// of a CU hide behind them.  The threshold from 256 lanes' maxima by bits costs
+// one wave 16 (32) steps of four ballots; from groups of each wave's lanes, and
+// an LDS atomic for each element found, it took 66 us.
 template <typename T>
 __global__ __launch_bounds__(256) void beam_part_kernel(BeamArgs a, const T *__restrict__ logits,
                                                         Cand *__restrict__ cand,
                                                         PartSum *__restrict__ sums) {
   typedef KeyOf<T> KO;
   typedef typename KO::type Key;
+  typedef OrderOf<T> Order;
   constexpr int kN = kPart<T> / 256 / 8; // groups of eight a lane
-  __shared__ Key keys[kPart<T>];
-  __shared__ float wave_max[4], wave_kth[4];
-  __shared__ double wave_sum[4];
-  __shared__ int count;
+  __shared__ Key keys[KDA_BEAM_MAX * 8 * kN];
+  __shared__ float lane_max[256], wave_top[4];
+  __shared__ double lane_sum[256];
+  __shared__ float bar_at, tie_at;
+  __shared__ int count, wave_ties[2][4];
   const int row = blockIdx.x / a.parts, part = blockIdx.x - row * a.parts;
-  const int tid = threadIdx.x, wv = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int first = part * kPart<T>;
   const int left = a.V - first; // elements from the part's start on
   const T *p = logits + row * a.row_stride + first;
@@ -173,42 +179,60 @@ __global__ __launch_bounds__(256) void beam_part_kernel(BeamArgs a, const T *__r
         x[i][j] = c + j < left ? to_f32(p[c + j]) : -__builtin_inff();
     }
   }
-  float m = -__builtin_inff();
+  float m = -__builtin_inff(), most[kN]; // of each eight
 #pragma unroll
-  for (int i = 0; i < kN; ++i)
+  for (int i = 0; i < kN; ++i) {
+    most[i] = x[i][0];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      m = fmaxf(m, x[i][j]); // (a NaN is found by the sum)
-  const float kth = kth_of_groups(m, a.K, a.groups_log2, lane_f32);
-  float top = m;
-#pragma unroll
-  for (int b = 1; b < 64; b <<= 1)
-    top = fmaxf(top, __shfl_xor(top, b));
-  if ((tid & 63) == 0) {
-    wave_max[wv] = top;
-    wave_kth[wv] = kth;
+    for (int j = 1; j < 8; ++j)
+      most[i] = fmaxf(most[i], x[i][j]); // (a NaN is found by the sum)
+    m = fmaxf(m, most[i]);
   }
+  lane_max[tid] = m;
+  m = wave_max(m);
+  if (lane == 0)
+    wave_top[wv] = m;
   if (tid == 0)
     count = 0;
   __syncthreads();
-  top = fmaxf(fmaxf(wave_max[0], wave_max[1]), fmaxf(wave_max[2], wave_max[3]));
-  const float bar = fmaxf(fmaxf(wave_kth[0], wave_kth[1]), fmaxf(wave_kth[2], wave_kth[3]));
+  const float top = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
 
-  // what reaches the threshold, in any order: the keys are ordered below
+  if (wv == 0) {
+    // The K-th largest of the lanes' maxima, bit by bit, or any number that
+    // parts the K largest from the others.
+    uint32_t of[4], low = 0;
+    bool parts = false;
 #pragma unroll
-  for (int i = 0; i < kN; ++i)
+    for (int i = 0; i < 4; ++i)
+      of[i] = Order::make(lane_max[i * 64 + lane]);
+    for (int bit = Order::kBits - 1; bit >= 0 && !parts; --bit) {
+      const uint32_t at = low | 1u << bit;
+      int reach = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (x[i][j] >= bar && x[i][j] > -__builtin_inff())
-        keys[atomicAdd(&count, 1)] = KO::make(x[i][j], (i * 256 + tid) * 8 + j);
+      for (int i = 0; i < 4; ++i)
+        reach += __popcll(__ballot(of[i] >= at));
+      if (reach >= a.K) {
+        low = at;
+        parts = reach == a.K;
+      }
+    }
+    if (lane == 0) {
+      // (the next number above infinity is a NaN: nothing reaches it)
+      bar_at = Order::value(parts ? low : low + 1);
+      const bool none = parts || low <= Order::make(-__builtin_inff());
+      tie_at = none ? __builtin_nanf("") : Order::value(low);
+    }
+  }
 
   double sum = 0.;
   if (top > -__builtin_inff()) {
 #pragma unroll
     for (int i = 0; i < kN; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        sum += (double)exp_neg(x[i][j] - top);
+      for (int j = 0; j < 8; j += 4) {
+        const auto e = [&](int l) { return exp_neg(x[i][j + l] - top); };
+        sum += (double)((e(0) + e(1)) + (e(2) + e(3)));
+      }
   } else {
     // nothing, unless a NaN hides there
 #pragma unroll
@@ -218,56 +242,86 @@ __global__ __launch_bounds__(256) void beam_part_kernel(BeamArgs a, const T *__r
         if (x[i][j] != x[i][j])
           sum = __builtin_nan("");
   }
-#pragma unroll
-  for (int b = 1; b < 64; b <<= 1)
-    sum += __shfl_xor(sum, b);
-  if ((tid & 63) == 0)
-    wave_sum[wv] = sum;
+  lane_sum[tid] = sum;
   __syncthreads();
-  if (tid == 0)
-    sums[blockIdx.x] = {wave_sum[0] + wave_sum[1] + (wave_sum[2] + wave_sum[3]), top, 0};
 
-  const int n = count;
-  Cand *out = cand + (int64_t)blockIdx.x * a.K;
-  const auto put = [&](int at, Key k) { out[at] = {KO::value(k), first + KO::place(k)}; };
-  if (n <= 256) { // by rank
-    if (tid < n) {
-      const Key k = keys[tid];
-      int above = 0;
-      for (int i = 0; i < n; ++i)
-        above += keys[i] > k;
-      if (above < a.K)
-        put(above, k);
+  // what reaches the threshold, in any order: the keys are ordered below
+  const float bar = bar_at, tie = tie_at;
+#pragma unroll
+  for (int i = 0; i < kN; ++i)
+    if (most[i] >= bar) {
+      int n = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        n += x[i][j] >= bar;
+      int at = atomicAdd(&count, n);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (x[i][j] >= bar)
+          keys[at++] = KO::make(x[i][j], (i * 256 + tid) * 8 + j);
     }
-  } else { // (many equal logits, or few distinct lanes) sorted whole
-    int size = 512;
-    while (size < n)
-      size <<= 1;
-    for (int i = n + tid; i < size; i += 256)
-      keys[i] = 0;
-    for (int run = 2; run <= size; run <<= 1)
-      for (int d = run >> 1; d > 0; d >>= 1) {
-        __syncthreads();
-        for (int i = tid; i < size / 2; i += 256) {
-          const int lo = (i & ~(d - 1)) << 1 | (i & (d - 1)), hi = lo | d;
-          const Key u = keys[lo], v = keys[hi];
-          if ((u < v) == ((lo & run) == 0)) {
-            keys[lo] = v;
-            keys[hi] = u;
-          }
-        }
-      }
-    __syncthreads();
-    if (tid < a.K)
-      put(tid, keys[tid]); // (n > 256 >= K)
+  if (wv == 3) { // (each lane's sum is there since the barrier)
+    sum = (lane_sum[lane] + lane_sum[64 + lane]) + (lane_sum[128 + lane] + lane_sum[192 + lane]);
+#pragma unroll
+    for (int b = 1; b < 64; b <<= 1)
+      sum += __shfl_xor(sum, b);
+    if (lane == 0)
+      sums[blockIdx.x] = {sum, top, 0};
   }
-  if (n < a.K && tid >= n && tid < a.K)
+  __syncthreads();
+
+  const int n = __builtin_amdgcn_readfirstlane(count);
+  Cand *out = cand + (int64_t)blockIdx.x * a.K;
+  for (int i = tid; i < n; i += 256) { // by rank
+    const Key k = keys[i];
+    int above = 0;
+    for (int j = 0; j < n; ++j)
+      above += keys[j] > k;
+    if (above < a.K)
+      out[above] = {KO::value(k), first + KO::place(k)};
+  }
+  int have = n;
+  if (have < a.K && tie == tie) { // the first elements that are equal to it
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      int mine = 0, upto;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        mine += x[i][j] == tie;
+      upto = mine; // of the lanes up to this one
+#pragma unroll
+      for (int b = 1; b < 64; b <<= 1) {
+        const int o = __shfl_up(upto, b);
+        upto += lane >= b ? o : 0;
+      }
+      if (lane == 63)
+        wave_ties[i & 1][wv] = upto;
+      __syncthreads();
+      int at = have + upto - mine;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        at += s < wv ? wave_ties[i & 1][s] : 0;
+        have += wave_ties[i & 1][s];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (x[i][j] == tie) {
+          if (at < a.K)
+            out[at] = {tie, first + (i * 256 + tid) * 8 + j};
+          ++at;
+        }
+      if (have >= a.K)
+        break;
+    }
+  }
+  if (tid >= have && tid < a.K)
     out[tid] = {0.f, -1};
 }
 
 // ---- selection: merge -----------------------------------------------------------
 
 constexpr int kMergeCap = 1024;
+constexpr int kHeld = 4; // candidates a lane holds at a time
 
 // A valued candidate.  Before another one: the larger value, then the lower
 // beam, then (where 64 bits do not tell a beam's values apart) the larger
@@ -278,15 +332,32 @@ struct Valued {
   int32_t w, v;
 };
 __device__ __forceinline__ bool before(const Valued &p, const Valued &q) {
-  if (p.val != q.val)
-    return p.val > q.val;
-  if (p.w != q.w)
-    return p.w < q.w;
-  if (p.x != q.x)
-    return p.x > q.x;
-  return p.v < q.v;
+  const bool tail = (p.x > q.x) | ((p.x == q.x) & (p.v < q.v)); // (all at once: no branches)
+  return (p.val > q.val) |
+         ((p.val == q.val) & ((p.w < q.w) | ((p.w == q.w) & tail)));
 }
 
+// The K-th largest of the maxima of 2^groups_log2 >= K lane groups: at least K
+// elements of the wave reach it, or it is -inf.
+__device__ __forceinline__ double kth_of_groups(double m, int K, int groups_log2) {
+  const int lane = threadIdx.x & 63, width = 64 >> groups_log2;
+  for (int b = 1; b < width; b <<= 1) {
+    const double o = __shfl_xor(m, b);
+    m = o > m ? o : m;
+  }
+  int above = 0;
+  for (int g = 0; g < (1 << groups_log2); ++g) {
+    const double o = lane_f64(m, g * width);
+    above += o > m || (o == m && g * width < (lane & -width));
+  }
+  return lane_f64(m, __builtin_ctzll(__ballot(above == K - 1)));
+}
+
+// A chain of latencies, a workgroup a batch: 10 us for 64 batches of 8 beams in
+// 16 parts, 5 us for one of 4 beams in 8; so the candidates are asked for
+// before the sums, a beam's parts are joined by as many lanes, and the ranks
+// are counted by all four waves without branches (one lane each, with
+// branches: 22 us).
 __global__ __launch_bounds__(256) void beam_merge_kernel(
     BeamArgs a, const Cand *__restrict__ cand, const PartSum *__restrict__ sums,
     const float *__restrict__ scores, const uint8_t *__restrict__ finished,
@@ -294,62 +365,110 @@ __global__ __launch_bounds__(256) void beam_merge_kernel(
     int32_t *__restrict__ out_tokens, uint8_t *__restrict__ out_finished) {
   __shared__ double lse[KDA_BEAM_MAX], base[KDA_BEAM_MAX]; // base NaN: beam without value
   __shared__ bool done[KDA_BEAM_MAX];
+  __shared__ double open_base[KDA_BEAM_MAX]; // base, NaN for a finished beam too
   __shared__ double wave_kth[4];
+  __shared__ int rank[kMergeCap];
   __shared__ Valued buf[kMergeCap];
   __shared__ Valued sel[KDA_BEAM_MAX];
   __shared__ Valued wave_best[4];
   __shared__ int count;
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int K = a.K, W = a.W, P = a.parts;
   const double inf = __builtin_inf();
   const PartSum *ps = sums + (int64_t)b * W * P;
   const Cand *cs = cand + (int64_t)b * W * P * K;
 
-  for (int w = wv; w < W; w += 4) {
-    float top = -__builtin_inff();
-    for (int p = lane; p < P; p += 64)
-      top = fmaxf(top, ps[w * P + p].max);
+  // Candidate i: the (i % K)-th of part i / K % P of beam i / (P K).  The first
+  // ones are asked for before all else, so that their way from memory and the
+  // sums' is one.
+  const int of_beam = P * K, all = W * of_beam;
+  const auto load = [&](Cand(&c)[kHeld], int i0) {
 #pragma unroll
-    for (int s = 1; s < 64; s <<= 1)
+    for (int j = 0; j < kHeld; ++j) {
+      const int i = i0 + j * 256 + tid;
+      c[j] = i < all ? cs[i] : Cand{0.f, -1};
+    }
+  };
+  Cand held[kHeld];
+  load(held, 0);
+
+  // lse: 2^lanes_log2 lanes a beam
+  const int wide = 1 << a.lanes_log2;
+  for (int w0 = 0; w0 < W; w0 += 256 >> a.lanes_log2) {
+    const int w = w0 + (tid >> a.lanes_log2), p0 = tid & (wide - 1);
+    const bool in = w < W;
+    const float sc = in ? scores[b * W + w] : 0.f;
+    const bool fin = in && finished && finished[b * W + w];
+    const PartSum none{0., -__builtin_inff(), 0};
+    const PartSum q0 = in && p0 < P ? ps[w * P + p0] : none;
+    float top = q0.max;
+    for (int p = p0 + wide; p < P && in; p += wide)
+      top = fmaxf(top, ps[w * P + p].max);
+    for (int s = 1; s < wide; s <<= 1)
       top = fmaxf(top, __shfl_xor(top, s));
     double sum = 0.;
-    for (int p = lane; p < P; p += 64) {
-      const PartSum q = ps[w * P + p];
-      // (a part of -inf only has the sum 0, or NaN)
+    PartSum q = q0;
+    for (int p = p0;;) { // (a part of -inf only has the sum 0, or NaN)
       sum += q.max > -__builtin_inff() ? q.sum * exp((double)q.max - (double)top) : q.sum;
+      p += wide;
+      if (p >= P || !in)
+        break;
+      q = ps[w * P + p];
     }
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1)
+    for (int s = 1; s < wide; s <<= 1)
       sum += __shfl_xor(sum, s);
-    if (lane == 0) {
+    if (in && p0 == 0) {
       const double l = (double)top + log(sum);
-      const float sc = scores[b * W + w];
-      const bool fin = finished && finished[b * W + w];
       const bool has = sc - sc == 0.f && (fin || l - l == 0.); // finite
       done[w] = fin;
       lse[w] = l;
       base[w] = has ? (double)sc : __builtin_nan("");
+      open_base[w] = has && !fin ? (double)sc : __builtin_nan("");
     }
   }
   if (tid == 0)
     count = 0;
   __syncthreads();
 
-  // list i: the candidates of part i % P of beam i / P, best first
-  const int lists = W * P;
-  const auto open = [&](int w) { return base[w] == base[w] && !done[w]; };
-  const auto value = [&](int w, const Cand &c) { return base[w] + ((double)c.x - lse[w]); };
   const auto of_done = [&](int w) { // the one candidate of a finished beam
     return Valued{base[w], 0.f, w, a.eos};
   };
+  // What the held candidates are worth, NaN if nothing.
+  double worth[kHeld];
+  int beam[kHeld];
+  const auto rate = [&](int i0) {
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      // (i / of_beam: the double is off by less than half of what parts
+      // i + 1/2 from a multiple)
+      beam[j] = held[j].v >= 0 ? (int)(((double)(i0 + j * 256 + tid) + 0.5) * a.inv_of_beam) : 0;
+      const double v = open_base[beam[j]] + ((double)held[j].x - lse[beam[j]]);
+      worth[j] = held[j].v >= 0 ? v : __builtin_nan("");
+    }
+  };
+  // goes over the candidates that have a value
+  rate(0);
+  const auto for_all = [&](auto &&f) {
+    for (int i0 = 0;;) {
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j)
+        if (worth[j] == worth[j])
+          f(Valued{worth[j], held[j].x, beam[j], held[j].v});
+      if (all <= kHeld * 256) // (they stay for the next time)
+        break;
+      i0 += kHeld * 256;
+      const bool more = i0 < all;
+      i0 = more ? i0 : 0;
+      load(held, i0);
+      rate(i0);
+      if (!more)
+        break;
+    }
+  };
   double best = -inf;
-  for (int i = tid; i < lists; i += 256) {
-    const int w = i / P;
-    const Cand c = cs[(int64_t)i * K];
-    if (open(w) && c.v >= 0)
-      best = fmax(best, value(w, c));
-  }
-  const double kth = kth_of_groups(best, K, a.groups_log2, lane_f64);
+  for_all([&](const Valued &v) { best = fmax(best, v.val); });
+  const double kth = kth_of_groups(best, K, a.groups_log2);
   if (lane == 0)
     wave_kth[wv] = kth;
   __syncthreads();
@@ -359,34 +478,31 @@ __global__ __launch_bounds__(256) void beam_merge_kernel(
     if (at < kMergeCap)
       buf[at] = v;
   };
-  for (int i = tid; i < lists; i += 256) {
-    const int w = i / P;
-    if (!open(w))
-      continue;
-    for (int k = 0; k < K; ++k) {
-      const Cand c = cs[(int64_t)i * K + k];
-      if (c.v < 0)
-        break;
-      const double v = value(w, c);
-      if (v < bar)
-        break;
-      push({v, c.x, w, c.v});
-    }
-  }
+  for_all([&](const Valued &v) {
+    if (v.val >= bar)
+      push(v);
+  });
   if (tid < W && done[tid] && base[tid] == base[tid])
     push(of_done(tid));
   __syncthreads();
 
   const int n = count;
   if (n <= kMergeCap) {
-    for (int i = tid; i < n; i += 256) {
+    // by rank: wave wv counts every fourth one
+    for (int i = tid; i < n; i += 256)
+      rank[i] = 0;
+    __syncthreads();
+    for (int i = lane; i < n; i += 64) {
       const Valued v = buf[i];
       int above = 0;
-      for (int j = 0; j < n; ++j)
+      for (int j = wv; j < n; j += 4)
         above += before(buf[j], v);
-      if (above < K)
-        sel[above] = v;
+      atomicAdd(&rank[i], above);
     }
+    __syncthreads();
+    for (int i = tid; i < n; i += 256)
+      if (rank[i] < K)
+        sel[rank[i]] = buf[i];
   } else {
     // more than the buffer holds (thousands of equal values): one by one, each
     // time the best of all candidates that come after the last one
@@ -397,14 +513,7 @@ __global__ __launch_bounds__(256) void beam_merge_kernel(
         if (before(last, v) && before(v, mine))
           mine = v;
       };
-      for (int i = tid; i < lists; i += 256)
-        if (open(i / P))
-          for (int j = 0; j < K; ++j) {
-            const Cand c = cs[(int64_t)i * K + j];
-            if (c.v < 0)
-              break;
-            take({value(i / P, c), c.x, i / P, c.v});
-          }
+      for_all(take);
       if (tid < W && done[tid] && base[tid] == base[tid])
         take(of_done(tid));
       for (int s = 1; s < 64; s <<= 1) {
@@ -587,6 +696,9 @@ hipError_t launch_beam_select(int elt, const BeamCall &c, void *ws, hipStream_t 
   // wave
   while ((1 << a.groups_log2) < 2 * c.K && a.groups_log2 < 6)
     ++a.groups_log2;
+  while ((1 << a.lanes_log2) < a.parts && a.lanes_log2 < 6)
+    ++a.lanes_log2;
+  a.inv_of_beam = 1. / ((double)a.parts * c.K);
   const int64_t n = (int64_t)c.B * c.W * a.parts;
   if (n * 256 > UINT32_MAX)
     return hipErrorInvalidConfiguration;

@@ -301,7 +301,7 @@ __device__ __forceinline__ void reads_stay() { __builtin_amdgcn_sched_barrier(0x
 // full (matrix cores 27 %, VALU 36 %, LDS 39 %): what bounds it is the chain of
 // a chunk's products, its barriers and LDS round trips, 8700 cycles for 128
 // columns.  fp32 multiplies on the fp32 matrix instructions, at a sixteenth of
-// bf16's rate: bound by these.
+// bf16's rate: 9.4 of the 14.8 us of a chunk of eight waves are theirs.
 template <typename T, int DK, int NW> constexpr int kCopyBytes =
     kDC * (2 * DK + 16 * NW) * (int)sizeof(T);
 template <typename T, int DK, int NW, bool FAST>
