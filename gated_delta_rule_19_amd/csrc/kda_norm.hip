@@ -4,12 +4,20 @@
 //   r = residual + scale * u,  y = r * weight / sqrt(mean(r^2) + eps)
 //
 // A few operations on every element moved: bound by HBM.  A row stays in the
-// registers of the lanes that read it, eight neighbouring elements at a time,
+// registers of the lanes that read it, 16 bytes of the widest type at a time,
 // so that each input is read once although both means need the whole row;
 // the gate and the residual are requested before the first mean is formed.
-// Rows of up to 2048 elements take one wave or a part of one, longer ones a
+// Rows of up to 256 groups take one wave or a part of one, longer ones a
 // workgroup, whose waves join their sums in LDS.  Sums are fp32: each lane's
-// own, then the lanes' in a tree, so at most 8 NV + 10 roundings deep.
+// own of up to 64 elements, then the lanes' in a tree: 74 roundings deep at most.
+//
+// 8192 x 12288 bf16 with all parts: 194 us for 1.01 GB, 5.2 TB/s, what a large
+// copy reaches on the same card.  Two groups a lane keep more rows in flight
+// than four (205 us), and non-temporal accesses, here larger than all caches,
+// gain as much (cached: 216 us).  20000 x 1002 fp32: 82 us for 401 MB (4.9
+// TB/s): rows that end inside a 128-byte line cost a tenth (1024 columns: 5.5).
+// One row: 6.6 us on the GPU, the latency of three rounds to memory and two
+// joins of sums.
 #include "kda_block.h"
 #include "kda_device.h"
 
@@ -26,76 +34,67 @@ struct NormArgs {
   float post_eps, eps, scale_all, inv_D;
 };
 
-// eight elements with their type's alignment only
+// E neighbouring elements, with their type's alignment only: 16 bytes of the
+// widest type, so that a wave's access is one run of memory.
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
-template <typename T> struct Oct;
-template <> struct Oct<bf16> { u32x4 r; };
-template <> struct Oct<float> { f32x4 lo, hi; };
+template <typename T, int E> struct GroupOf;
+template <> struct GroupOf<bf16, 8> { typedef u32x4 type; typedef u32x4_any any; };
+template <> struct GroupOf<bf16, 4> { typedef u32x2 type; typedef u32x2_any any; };
+template <> struct GroupOf<float, 4> { typedef f32x4 type; typedef f32x4_any any; };
+template <typename T, int E> using Group = typename GroupOf<T, E>::type;
 
-__device__ __forceinline__ void load_oct(const bf16 *p, Oct<bf16> &o) {
-  o.r = *reinterpret_cast<const u32x4_any *>(p);
-}
-__device__ __forceinline__ void load_oct(const float *p, Oct<float> &o) {
-  o.lo = *reinterpret_cast<const f32x4_any *>(p);
-  o.hi = *reinterpret_cast<const f32x4_any *>(p + 4);
-}
-__device__ __forceinline__ void widen(const Oct<bf16> &o, float *x) { widen8(o.r, x); }
-__device__ __forceinline__ void widen(const Oct<float> &o, float *x) {
+__device__ __forceinline__ void widen(const u32x4 &g, float *x) { widen8(g, x); }
+__device__ __forceinline__ void widen(const u32x2 &g, float *x) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[i] = o.lo[i];
-    x[4 + i] = o.hi[i];
-  }
+  for (int i = 0; i < 4; ++i)
+    x[i] = __builtin_bit_cast(float, i % 2 ? g[i / 2] & 0xffff0000u : g[i / 2] << 16);
 }
-__device__ __forceinline__ void store_oct(bf16 *p, const float *x) {
-  bf16x8 v;
+__device__ __forceinline__ void widen(const f32x4 &g, float *x) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    v[i] = static_cast<bf16>(x[i]);
-  *reinterpret_cast<u32x4_any *>(p) = __builtin_bit_cast(u32x4, v);
+  for (int i = 0; i < 4; ++i)
+    x[i] = g[i];
 }
-__device__ __forceinline__ void store_oct(float *p, const float *x) {
-  *reinterpret_cast<f32x4_any *>(p) = f32x4{x[0], x[1], x[2], x[3]};
-  *reinterpret_cast<f32x4_any *>(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
+template <typename T, int E> __device__ __forceinline__ Group<T, E> rounded(const float *x) {
+  typedef T Vec __attribute__((ext_vector_type(E)));
+  Vec v;
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    v[i] = from_f32<T>(x[i]);
+  return __builtin_bit_cast(Group<T, E>, v);
 }
 
-// n of eight elements of a row (n >= 8: all; the others read 0)
-template <typename T> __device__ __forceinline__ void load_part(const T *p, int n, Oct<T> &o) {
-  o = Oct<T>{};
-  if (n >= 8) {
-    load_oct(p, o);
-  } else {
-    float x[8] = {};
-    for (int i = 0; i < 8; ++i)
-      if (i < n)
-        x[i] = to_f32(p[i]);
-    if constexpr (std::is_same<T, float>::value) {
-      o.lo = f32x4{x[0], x[1], x[2], x[3]};
-      o.hi = f32x4{x[4], x[5], x[6], x[7]};
-    } else {
-      bf16x8 v;
-      for (int i = 0; i < 8; ++i)
-        v[i] = static_cast<bf16>(x[i]);
-      o.r = __builtin_bit_cast(u32x4, v);
-    }
-  }
+// n of E elements of a row (n >= E: all; the others read 0)
+template <int E, typename T>
+__device__ __forceinline__ Group<T, E> load_part(const T *p, int n) {
+  if (n >= E)
+    return __builtin_nontemporal_load(reinterpret_cast<const typename GroupOf<T, E>::any *>(p));
+  float x[E];
+  for (int i = 0; i < E; ++i)
+    x[i] = i < n ? to_f32(p[i]) : 0.f;
+  return rounded<T, E>(x);
 }
-template <typename T> __device__ __forceinline__ void store_part(T *p, int n, const float *x) {
-  if (n >= 8) {
-    store_oct(p, x);
+template <int E, typename T>
+__device__ __forceinline__ void store_part(T *p, int n, const float *x) {
+  if (n >= E) {
+    __builtin_nontemporal_store(rounded<T, E>(x),
+                                reinterpret_cast<typename GroupOf<T, E>::any *>(p));
   } else {
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < E; ++i)
       if (i < n)
         p[i] = from_f32<T>(x[i]);
   }
 }
-// eight of a parameter's fp32 values (16-byte aligned at whole groups)
-__device__ __forceinline__ void load_param(const float *p, int n, float *x) {
-  if (n >= 8) {
-    load8f(p, x);
+// E of a parameter's fp32 values (16-byte aligned at whole groups)
+template <int E> __device__ __forceinline__ void load_param(const float *p, int n, float *x) {
+  if (n >= E) {
+#pragma unroll
+    for (int i = 0; i < E; i += 4)
+      widen(*reinterpret_cast<const f32x4 *>(p + i), x + i);
   } else {
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < E; ++i)
       x[i] = i < n ? p[i] : 0.f;
   }
 }
@@ -118,9 +117,17 @@ template <bool BLOCK> __device__ __forceinline__ float row_sum(float v, int lane
   return v;
 }
 
+// Elements of a group.
+template <typename T, typename R> constexpr int kGroup = sizeof(T) + sizeof(R) == 4 ? 8 : 4;
+
+// NV groups a lane.  Rows of more than 32768 elements leave no registers to
+// hold x, the gate and the residual at once: these two are read behind the
+// first mean.
 template <typename T, typename R, int NV, bool BLOCK>
 __global__ __launch_bounds__(BLOCK ? 1024 : 256) void norm_kernel(
     NormArgs a, const T *x, const T *gate, const R *residual, R *residual_out, T *y) {
+  constexpr int E = kGroup<T, R>;
+  constexpr bool AHEAD = NV * E <= 32;
   int64_t row;
   int lane, lanes;
   if constexpr (BLOCK) {
@@ -133,31 +140,30 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 256) void norm_kernel(
     row = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> a.lanes_log2;
   }
   const bool real = row < a.rows;
-  int left[NV]; // elements of each group of eight that the row has
-  Oct<T> xr[NV], gr[NV];
-  Oct<R> rr[NV];
+  int left[NV]; // elements from each group's start on that the row has
+  Group<T, E> xr[NV], gr[NV];
+  Group<R, E> rr[NV];
+  const auto load_others = [&](int i) __attribute__((always_inline)) {
+    const int c = (i * lanes + lane) * E;
+    gr[i] = gate && left[i] > 0 ? load_part<E>(gate + row * a.gs + c, left[i]) : Group<T, E>{};
+    rr[i] = residual && left[i] > 0 ? load_part<E>(residual + row * a.rs + c, left[i])
+                                    : Group<R, E>{};
+  };
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * lanes + lane) * 8;
+    const int c = (i * lanes + lane) * E;
     left[i] = real ? a.D - c : 0;
-    xr[i] = Oct<T>{};
-    gr[i] = Oct<T>{};
-    rr[i] = Oct<R>{};
-    if (left[i] > 0) {
-      load_part(x + row * a.xs + c, left[i], xr[i]);
-      if (gate)
-        load_part(gate + row * a.gs + c, left[i], gr[i]);
-      if (residual)
-        load_part(residual + row * a.rs + c, left[i], rr[i]);
-    }
+    xr[i] = left[i] > 0 ? load_part<E>(x + row * a.xs + c, left[i]) : Group<T, E>{};
+    if constexpr (AHEAD)
+      load_others(i);
   }
-  float u[NV][8];
+  float u[NV][E];
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     widen(xr[i], u[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < E; ++j)
       sum = fmaf(u[i][j], u[i][j], sum);
   }
   float inv = 1.f;
@@ -166,49 +172,51 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 256) void norm_kernel(
   sum = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * lanes + lane) * 8;
+    const int c = (i * lanes + lane) * E;
     if (left[i] <= 0)
       continue;
-    float w[8], res[8];
+    if constexpr (!AHEAD)
+      load_others(i);
+    float w[E], res[E];
     if (a.post_weight) {
-      load_param(a.post_weight + c, left[i], w);
+      load_param<E>(a.post_weight + c, left[i], w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < E; ++j)
         u[i][j] *= inv * w[j];
     }
     if (gate) {
       widen(gr[i], w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < E; ++j)
         u[i][j] *= __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-w[j] * 1.4426950408889634f));
     }
     if (a.scale)
-      load_param(a.scale + c, left[i], w);
+      load_param<E>(a.scale + c, left[i], w);
     widen(rr[i], res);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < E; ++j) {
       const float su = (a.scale ? w[j] : a.scale_all) * u[i][j];
       u[i][j] = residual ? res[j] + su : su;
       if (j < left[i])
         sum = fmaf(u[i][j], u[i][j], sum);
     }
     if (residual_out)
-      store_part(residual_out + row * a.os + c, left[i], u[i]);
+      store_part<E>(residual_out + row * a.os + c, left[i], u[i]);
   }
   if (!y)
     return;
   inv = 1.f / sqrtf(row_sum<BLOCK>(sum, a.lanes_log2, 1) * a.inv_D + a.eps);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * lanes + lane) * 8;
+    const int c = (i * lanes + lane) * E;
     if (left[i] <= 0)
       continue;
-    float w[8];
-    load_param(a.weight + c, left[i], w);
+    float w[E];
+    load_param<E>(a.weight + c, left[i], w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < E; ++j)
       w[j] *= inv * u[i][j];
-    store_part(y + row * a.ys + c, left[i], w);
+    store_part<E>(y + row * a.ys + c, left[i], w);
   }
 }
 
@@ -231,10 +239,11 @@ hipError_t launch_block_norm(int elt, int32_t rows, int32_t D, const kda_norm_io
   a.eps = io.eps;
   a.scale_all = io.scale_all;
   a.inv_D = 1.f / (float)D;
-  const int need = (D + 7) / 8; // groups of eight
   const auto typed = [&](auto xt, auto rt) {
     using T = decltype(xt);
     using R = decltype(rt);
+    constexpr int E = kGroup<T, R>;
+    const int need = (D + E - 1) / E; // groups
     const auto run = [&](auto nv, auto block, int64_t grid, int threads) {
       // (the device's grids: 2^32 - 1 threads)
       if (grid * threads > UINT32_MAX)
@@ -258,10 +267,17 @@ hipError_t launch_block_norm(int elt, int32_t rows, int32_t D, const kda_norm_io
         return run(integral_constant<int, 2>(), false_type(), grid, 256);
       return run(integral_constant<int, 4>(), false_type(), grid, 256);
     }
-    const auto threads = [&](int nv) { return ((need + nv - 1) / nv + 63) / 64 * 64; };
-    if (threads(4) <= 1024)
-      return run(integral_constant<int, 4>(), true_type(), rows, threads(4));
-    return run(integral_constant<int, 8>(), true_type(), rows, threads(8));
+    const auto block = [&](auto nv) {
+      const int threads = ((need + decltype(nv)::value - 1) / decltype(nv)::value + 63) / 64 * 64;
+      return threads <= 1024 ? run(nv, true_type(), rows, threads) : hipErrorInvalidConfiguration;
+    };
+    if (need <= 2048)
+      return block(integral_constant<int, 2>());
+    if (need <= 4096)
+      return block(integral_constant<int, 4>());
+    if (E == 8 || need <= 8192)
+      return block(integral_constant<int, 8>());
+    return block(integral_constant<int, 64 / E>());
   };
   if (elt == 1)
     return io.residual_dt == KDA_BF16 ? typed(bf16(), bf16()) : typed(bf16(), float());
