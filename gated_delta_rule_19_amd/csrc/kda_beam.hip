@@ -589,21 +589,30 @@ __global__ __launch_bounds__(256) void beam_merge_kernel(
 // ---- reordering ----------------------------------------------------------------
 
 typedef u32x4 u32x4_byte __attribute__((aligned(1)));
-typedef uint32_t u32_byte __attribute__((aligned(1)));
-constexpr int kReorderCols = 4; // units a lane
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_byte __attribute__((aligned(1)));
 
-// KM: rows that change, at most; U: bytes a lane holds of each.
-template <int KM, typename U>
+// States of the size of the card's last cache and below are left in it for the
+// step that reads them next; the stores of larger ones go past it (2 groups of 4
+// rows of 96 x 128 x 128 fp32, reorder and step: 30 us, 33; 32 groups: 471, 445).
+constexpr int64_t kLastCache = 256 << 20;
+
+// KM: rows that change, at most; U: bytes a lane holds of each, in turns of
+// STEP rows without a branch (a place behind the last row repeats it).
+//
+// 32 groups of 4 rows of 6.3 MB, of which 64 change: 135 us, 5.96 TB/s, what
+// memory gives.  One piece a lane: with four, one after the other, 144 us.
+template <int KM, int STEP, bool PAST, typename U>
 __global__ __launch_bounds__(256) void reorder_kernel(ReorderCall c) {
   __shared__ int64_t from[KDA_BEAM_MAX], to[KDA_BEAM_MAX];
   __shared__ int moved;
+  constexpr int64_t kSpan = 256 * (int64_t)sizeof(U);
   // state, group and block of columns
   int64_t blk = blockIdx.x;
   int s = 0;
   int64_t per = 0;
   for (; s < c.num_states; ++s) {
-    per = (c.bytes[s] + 256 * kReorderCols * (int64_t)sizeof(U) - 1) /
-          (256 * kReorderCols * (int64_t)sizeof(U));
+    per = (c.bytes[s] + kSpan - 1) / kSpan;
     if (blk < per * c.groups)
       break;
     blk -= per * c.groups;
@@ -611,7 +620,7 @@ __global__ __launch_bounds__(256) void reorder_kernel(ReorderCall c) {
   if (s == c.num_states)
     return;
   const int group = (int)(blk / per);
-  const int64_t col0 = (blk - group * per) * (256 * kReorderCols * (int64_t)sizeof(U));
+  const int64_t col = (blk - group * per) * kSpan + threadIdx.x * (int64_t)sizeof(U);
   const int64_t bytes = c.bytes[s];
   if (threadIdx.x < 64) {
     const int r = threadIdx.x;
@@ -640,32 +649,37 @@ __global__ __launch_bounds__(256) void reorder_kernel(ReorderCall c) {
   if (n == 0)
     return;
   uint8_t *base = (uint8_t *)c.state[s];
-  for (int k = 0; k < kReorderCols; ++k) {
-    const int64_t col = col0 + ((int64_t)k * 256 + threadIdx.x) * (int64_t)sizeof(U);
-    if (col + (int64_t)sizeof(U) <= bytes) {
-      typedef std::conditional_t<sizeof(U) == 16, u32x4_byte, u32_byte> Any;
-      U v[KM];
+  if (col + (int64_t)sizeof(U) <= bytes) {
+    typedef std::conditional_t<sizeof(U) == 16, u32x4_byte, u32x2_byte> Any;
+    U v[KM];
+#pragma unroll
+    for (int i0 = 0; i0 < KM; i0 += STEP)
+      if (i0 < n)
+#pragma unroll
+        for (int i = i0; i < i0 + STEP; ++i)
+          v[i] = *reinterpret_cast<const Any *>(base + from[min(i, n - 1)] + col);
+#pragma unroll
+    for (int i0 = 0; i0 < KM; i0 += STEP)
+      if (i0 < n)
+#pragma unroll
+        for (int i = i0; i < i0 + STEP; ++i) {
+          Any *p = reinterpret_cast<Any *>(base + to[min(i, n - 1)] + col);
+          if constexpr (PAST)
+            __builtin_nontemporal_store(v[i], p);
+          else
+            *p = v[i];
+        }
+  } else {
+    // the last bytes of a slice whose size is no multiple of the unit
+#pragma unroll 1
+    for (int64_t at = col; at < bytes; ++at) {
+      uint8_t v[KM];
 #pragma unroll
       for (int i = 0; i < KM; ++i)
-        if (i < n)
-          v[i] = *reinterpret_cast<const Any *>(base + from[i] + col);
+        v[i] = base[from[min(i, n - 1)] + at];
 #pragma unroll
       for (int i = 0; i < KM; ++i)
-        if (i < n)
-          *reinterpret_cast<Any *>(base + to[i] + col) = v[i];
-    } else {
-      // the last bytes of a slice whose size is no multiple of the unit
-      for (int64_t at = col; at < bytes; ++at) {
-        uint8_t v[KM];
-#pragma unroll
-        for (int i = 0; i < KM; ++i)
-          if (i < n)
-            v[i] = base[from[i] + at];
-#pragma unroll
-        for (int i = 0; i < KM; ++i)
-          if (i < n)
-            base[to[i] + at] = v[i];
-      }
+        base[to[min(i, n - 1)] + at] = v[i];
     }
   }
 }
@@ -718,27 +732,37 @@ hipError_t launch_beam_select(int elt, const BeamCall &c, void *ws, hipStream_t 
 }
 
 hipError_t launch_state_reorder(const ReorderCall &c, hipStream_t s) {
-  const auto run = [&](auto km, auto unit) {
+  int64_t held = 0;
+  for (int i = 0; i < c.num_states; ++i)
+    held += c.bytes[i] * c.groups * c.K;
+  const auto run = [&](auto km, auto step, auto unit) {
     typedef decltype(unit) U;
-    const int64_t cols = 256 * kReorderCols * (int64_t)sizeof(U);
+    constexpr int KM = decltype(km)::value, STEP = decltype(step)::value;
+    const int64_t span = 256 * (int64_t)sizeof(U);
     int64_t grid = 0;
     for (int i = 0; i < c.num_states; ++i) {
-      const int64_t per = (c.bytes[i] + cols - 1) / cols;
+      const int64_t per = (c.bytes[i] + span - 1) / span;
       if (per * c.groups > UINT32_MAX / 256 - grid)
         return hipErrorInvalidConfiguration;
       grid += per * c.groups;
     }
-    reorder_kernel<decltype(km)::value, U><<<(unsigned)grid, 256, 0, s>>>(c);
+    const auto kernel = held > kLastCache ? reorder_kernel<KM, STEP, true, U>
+                                          : reorder_kernel<KM, STEP, false, U>;
+    kernel<<<(unsigned)grid, 256, 0, s>>>(c);
     return hipGetLastError();
   };
   using std::integral_constant;
+  typedef integral_constant<int, 1> Single;
+  typedef integral_constant<int, 8> Eight;
   if (c.K <= 4)
-    return run(integral_constant<int, 4>(), u32x4());
-  if (c.K <= 8)
-    return run(integral_constant<int, 8>(), u32x4());
+    return run(integral_constant<int, 4>(), Single(), u32x4());
+  if (c.K <= 8) // (one by one, the compiler spends 234 registers: 32 groups of 8, 715 us, 443)
+    return run(integral_constant<int, 8>(), integral_constant<int, 2>(), u32x4());
   if (c.K <= 16)
-    return run(integral_constant<int, 16>(), u32x4());
-  return run(integral_constant<int, 64>(), uint32_t());
+    return run(integral_constant<int, 16>(), Single(), u32x4());
+  if (c.K <= 32)
+    return run(integral_constant<int, 32>(), Eight(), u32x4());
+  return run(integral_constant<int, 64>(), Eight(), u32x2());
 }
 
 } // namespace kda
