@@ -61,9 +61,12 @@ def strip_c_comments(text: str) -> str:
 
 
 # Sources of the calls beside the recurrence (convolution, selective scan,
-# state cache): no workload that carries counters here runs them.
-OTHER_SOURCES = ("kda_conv.hip", "kda_recurrent.h", "kda_recurrent_api.cpp", "kda_seqtab.h",
-                 "kda_ssm.hip", "kda_state_cache.hip")
+# state cache, decayed attention, beam search, block norm): no workload that
+# carries counters here runs them.
+OTHER_SOURCES = ("kda_beam.hip", "kda_block.h", "kda_block_api.cpp", "kda_checks.h",
+                 "kda_conv.hip", "kda_decay.hip", "kda_norm.hip", "kda_recurrent.h",
+                 "kda_recurrent_api.cpp", "kda_seqtab.h", "kda_ssm.hip",
+                 "kda_state_cache.hip")
 
 
 def kernel_source_hash() -> str:

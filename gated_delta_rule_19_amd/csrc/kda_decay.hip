@@ -98,8 +98,10 @@ __device__ __forceinline__ Pair prefix_sum(Pair x) {
 }
 __device__ __forceinline__ Pair lane_pair(const Pair &x, int lane) {
   lane = __builtin_amdgcn_readfirstlane(lane);
-  return {__builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x.hi), lane)),
-          __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x.lo), lane))};
+  const auto read = [lane](float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+  };
+  return {read(x.hi), read(x.lo)};
 }
 
 // ---- prompts ----------------------------------------------------------------------
@@ -188,7 +190,8 @@ __device__ __forceinline__ Frag<bf16> tr_frag(const bf16 *m, int ld, const int (
   const bf16x4 r1 = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4 *)(p + 16 * ld));
   return {__builtin_shufflevector(r0, r1, 0, 1, 2, 3, 4, 5, 6, 7)};
 }
-__device__ __forceinline__ Frag<float> tr_frag(const float *m, int ld, const int (&at)[4], int flip) {
+__device__ __forceinline__ Frag<float> tr_frag(const float *m, int ld, const int (&at)[4],
+                                               int flip) {
   Frag<float> f;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
