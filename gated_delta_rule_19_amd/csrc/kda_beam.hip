@@ -608,7 +608,7 @@ __global__ __launch_bounds__(256) void reorder_kernel(ReorderCall c) {
   __shared__ int moved;
   constexpr int64_t kSpan = 256 * (int64_t)sizeof(U);
   // state, group and block of columns
-  int64_t blk = blockIdx.x;
+  int64_t blk = c.first + blockIdx.x;
   int s = 0;
   int64_t per = 0;
   for (; s < c.num_states; ++s) {
@@ -731,7 +731,8 @@ hipError_t launch_beam_select(int elt, const BeamCall &c, void *ws, hipStream_t 
   return hipGetLastError();
 }
 
-hipError_t launch_state_reorder(const ReorderCall &c, hipStream_t s) {
+hipError_t launch_state_reorder(const ReorderCall &call, hipStream_t s) {
+  ReorderCall c = call;
   int64_t held = 0;
   for (int i = 0; i < c.num_states; ++i)
     held += c.bytes[i] * c.groups * c.K;
@@ -739,17 +740,20 @@ hipError_t launch_state_reorder(const ReorderCall &c, hipStream_t s) {
     typedef decltype(unit) U;
     constexpr int KM = decltype(km)::value, STEP = decltype(step)::value;
     const int64_t span = 256 * (int64_t)sizeof(U);
-    int64_t grid = 0;
-    for (int i = 0; i < c.num_states; ++i) {
-      const int64_t per = (c.bytes[i] + span - 1) / span;
-      if (per * c.groups > UINT32_MAX / 256 - grid)
-        return hipErrorInvalidConfiguration;
-      grid += per * c.groups;
-    }
+    int64_t blocks = 0;
+    for (int i = 0; i < c.num_states; ++i)
+      blocks += (c.bytes[i] + span - 1) / span * c.groups;
     const auto kernel = held > kLastCache ? reorder_kernel<KM, STEP, true, U>
                                           : reorder_kernel<KM, STEP, false, U>;
-    kernel<<<(unsigned)grid, 256, 0, s>>>(c);
-    return hipGetLastError();
+    // (the device's grids: 2^32 - 1 threads)
+    constexpr int64_t kMost = UINT32_MAX / 256;
+    for (c.first = 0; c.first < blocks; c.first += kMost) {
+      kernel<<<(unsigned)std::min(kMost, blocks - c.first), 256, 0, s>>>(c);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess)
+        return e;
+    }
+    return hipSuccess;
   };
   using std::integral_constant;
   typedef integral_constant<int, 1> Single;

@@ -56,6 +56,7 @@ hipError_t launch_beam_select(int elt, const BeamCall &c, void *ws, hipStream_t 
 // One launch's argument block: the buffers by value.
 struct ReorderCall {
   int32_t groups, K, num_states;
+  int64_t first; // block of this launch's first one
   const int32_t *parents, *slots;
   void *state[KDA_REORDER_MAX_STATES];
   int64_t bytes[KDA_REORDER_MAX_STATES];

@@ -295,7 +295,9 @@ kda_status kda_state_reorder(int32_t groups, int32_t K, const int32_t *parents,
     c.bytes[c.num_states] = bytes;
     c.num_slots[c.num_states++] = held;
   }
-  return c.num_states == 0 ? KDA_OK : result(launch_state_reorder(c, (hipStream_t)stream));
+  if (c.num_states == 0 || K == 1) // (one row has no other parent)
+    return KDA_OK;
+  return result(launch_state_reorder(c, (hipStream_t)stream));
 }
 
 } // extern "C"

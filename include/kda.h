@@ -763,7 +763,7 @@ kda_status kda_block_norm(int32_t rows, int32_t D, kda_dtype dt, const kda_norm_
  *                   may not overlap the inputs or each other.
  *   workspace     : DEVICE, of the queried size, 256-byte aligned.
  * Within a beam candidates are ordered by their logits as they are, across
- * beams by values in 64 bits; the logarithm's sum is good to some 2^-24.
+ * beams by values in 64 bits; the logarithm's sum is good to some 2^-23 of it.
  * out_scores are rounded to fp32.
  */
 #define KDA_BEAM_MAX 64
