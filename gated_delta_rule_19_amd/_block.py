@@ -24,30 +24,29 @@ def _decay_io(q, k, v, g, scale, o):
     for x, name in ((q, "q"), (k, "k"), (v, "v")):
         if x.dim() != 3:
             raise ValueError("%s must be [tokens, heads, size] (got %s)" % (name, tuple(x.shape)))
-    rows, dk, dv = q.shape[0], q.shape[2], v.shape[2]
+    rows, Hq, dk = q.shape
+    Hk, (_, Hv, dv) = k.shape[1], v.shape
     if g.dim() not in (1, 2):
         raise ValueError("g must be [tokens, H] or [H] (got %s)" % (tuple(g.shape),))
-    H = g.shape[-1]
+    H = _count(g.shape[-1], "the number of heads")
     code = _dtype(q, "q")
     dt = q.dtype
-    io = DecayIo()
-    for x, name in ((q, "q"), (k, "k"), (v, "v")):
-        few = x.shape[1]
+    for few, name in ((Hq, "q"), (Hk, "k"), (Hv, "v")):
         if few < 1 or H % few != 0:
             raise ValueError("the decay's %d heads must be a multiple of %s's %d" % (H, name, few))
-        setattr(io, "H" + name, _count(few, "the number of heads"))
-    io.q_stride = _rows(q, (rows, q.shape[1], dk), dt, "q")
-    io.k_stride = _rows(k, (rows, k.shape[1], dk), dt, "k")
-    io.v_stride = _rows(v, (rows, v.shape[1], dv), dt, "v")
+    qs = _rows(q, (rows, Hq, dk), dt, "q")
+    ks = _rows(k, (rows, Hk, dk), dt, "k")
+    vs = _rows(v, (rows, Hv, dv), dt, "v")
+    gs = 0
     if g.dim() == 2:
-        io.g_stride = _rows(g, (rows, H), torch.float32, "g")
+        gs = _rows(g, (rows, H), torch.float32, "g")
     else:
         _dense(g, (H,), torch.float32, "g")
-    io.o_stride = H * dv if o is None else _rows(o, (rows, H, dv), dt, "o")
-    io.q, io.k, io.v, io.g = _p(q), _p(k), _p(v), _p(g)
-    io.dk, io.dv = _count(dk, "q's size"), _count(dv, "v's size")
-    io.scale = float(scale)
-    return io, rows, _count(H, "the number of heads"), dk, dv, code
+    os = H * dv if o is None else _rows(o, (rows, H, dv), dt, "o")
+    # (in one go: a field set by name costs more than the checks)
+    io = DecayIo(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), None, qs, ks, vs, gs, os,
+                 Hq, Hk, Hv, _count(dk, "q's size"), _count(dv, "v's size"), float(scale))
+    return io, rows, H, dk, dv, code
 
 
 def decay_attention(q, k, v, g, scale: float = 1.0, cu_seqlens=None, initial_state=None,
@@ -132,14 +131,15 @@ def block_norm(x, weight=None, eps: float = 1e-6, residual=None, scale=1.0, gate
         raise ValueError("y needs weight")
     rdt = residual.dtype if residual is not None else \
         residual_out.dtype if residual_out is not None else dt
-    io = NormIo()
-    io.residual_dt = code if rdt == dt else _dtype(
+    rcode = code if rdt == dt else _dtype(
         residual if residual is not None else residual_out, "residual")
-    io.x_stride = _rows(x, (rows, D), dt, "x")
+    shape = (rows, D)
+    xs = _rows(x, shape, dt, "x")
+    gs = rs = ros = ys = 0
     if gate is not None:
-        io.gate_stride = _rows(gate, (rows, D), dt, "gate")
+        gs = _rows(gate, shape, dt, "gate")
     if residual is not None:
-        io.residual_stride = _rows(residual, (rows, D), rdt, "residual")
+        rs = _rows(residual, shape, rdt, "residual")
     per_channel = isinstance(scale, torch.Tensor)
     f32 = torch.float32
     _dense(post_weight, (D,), f32, "post_weight")
@@ -149,23 +149,19 @@ def block_norm(x, weight=None, eps: float = 1e-6, residual=None, scale=1.0, gate
     dev = _device(x, gate, residual, residual_out, y, post_weight, weight,
                   scale if per_channel else None)
     if residual_out is not None:
-        io.residual_out_stride = _rows(residual_out, (rows, D), rdt, "residual_out")
+        ros = _rows(residual_out, shape, rdt, "residual_out")
     elif residual is not None or weight is None:
-        residual_out = torch.empty((rows, D), dtype=rdt, device=dev)
-        io.residual_out_stride = D
+        residual_out = torch.empty(shape, dtype=rdt, device=dev)
+        ros = D
     if y is not None:
-        io.y_stride = _rows(y, (rows, D), dt, "y")
+        ys = _rows(y, shape, dt, "y")
     elif weight is not None:
-        y = torch.empty((rows, D), dtype=dt, device=dev)
-        io.y_stride = D
-    io.x, io.gate, io.residual = _p(x), _p(gate), _p(residual)
-    io.residual_out, io.y = _p(residual_out), _p(y)
-    io.post_weight, io.weight = _p(post_weight), _p(weight)
-    io.post_eps, io.eps = float(post_eps), float(eps)
-    if per_channel:
-        io.scale = _p(scale)
-    else:
-        io.scale_all = float(scale)
+        y = torch.empty(shape, dtype=dt, device=dev)
+        ys = D
+    # (in one go: a field set by name costs more than the checks)
+    io = NormIo(x.data_ptr(), _p(gate), _p(residual), _p(residual_out), _p(y), xs, gs, rs, ros, ys,
+                _p(post_weight), _p(weight), scale.data_ptr() if per_channel else None,
+                float(post_eps), float(eps), 0.0 if per_channel else float(scale), rcode)
     _call("kda_block_norm", dev, _count(rows, "the number of rows"), _count(D, "the row length"),
           code, ctypes.byref(io))
     return residual_out, y
@@ -206,10 +202,11 @@ def beam_select(logits, scores, beams=None, finished=None, eos: int = -1, order:
     dev = _device(logits, scores, finished, workspace)
     args = (_count(B, "the batch"), W, _count(V, "the vocabulary"), K, code)
     ws = _workspace(workspace, load().kda_beam_select_workspace_size(*args), dev)
-    out = torch.empty((B, K), dtype=torch.float32, device=dev)
-    parents = torch.empty((B, K), dtype=torch.int32, device=dev)
-    tokens = torch.empty((B, K), dtype=torch.int32, device=dev)
-    done = torch.empty((B, K), dtype=torch.bool, device=dev)
+    shape = (B, K)
+    out = torch.empty(shape, dtype=torch.float32, device=dev)
+    parents = torch.empty(shape, dtype=torch.int32, device=dev)
+    tokens = torch.empty(shape, dtype=torch.int32, device=dev)
+    done = torch.empty(shape, dtype=torch.bool, device=dev)
     _call("kda_beam_select", dev, *args, _p(logits), stride, _p(scores), _p(finished),
           _count(int(eos), "eos"), _ORDERS[order], _p(out), _p(parents), _p(tokens), _p(done),
           _p(ws), 0 if ws is None else ws.numel())
