@@ -49,8 +49,8 @@ struct DecayArgs {
   // prompts
   int32_t slices, seg; // slices of dv (a workgroup's columns), tokens per segment
   int64_t units;       // (segment, head) pairs of this launch
-  float *pair_state;   // [pairs, H, slices, DK / 16, lanes] of four
-  double *pair_decay;  // [pairs, H]: log2 of a segment's decay
+  float *seg_state;    // [segments of cut sequences, H, slices, DK / 16, lanes] of four
+  double *pair_decay;  // [segments of pass 0, H]: log2 of a segment's decay
 };
 
 constexpr float kMinDecay = -150.f; // fp32's exp is 0 there
@@ -290,20 +290,22 @@ constexpr int kNowhere = 0x7fffffe0; // a byte offset past every buffer's end
 // scheduler would otherwise raise all of a chunk's, and spill registers).
 __device__ __forceinline__ void reads_stay() { __builtin_amdgcn_sched_barrier(0x000f); }
 
-// Launch `pass` 0: all segments but each sequence's last (all of them where a
-// sequence is not cut): the first segments in full, the others only their
-// state from zero.  Pass 1: the other segments from the states that enter
-// them.  NW waves, 16 value columns each.  FAST: dk, dv and the rows'
+// Launch `pass` 0, of cut sequences: all segments but the last, only their
+// states: the first from the state that enters the sequence, which is put into
+// the workspace as it is, the others from zero.  Pass 1: all segments in full
+// from the states that enter them.  NW waves, 16 value columns each.  FAST: dk, dv and the rows'
 // addresses are multiples of 16 bytes: everything moves through raw buffers,
 // whose bounds take the place of branches at a chunk's end, and q, K and V
 // straight into LDS.  AHEAD: a chunk ahead into the other one of two copies;
 // without, the loads of the one copy are waited for.
 //
-// 131072 tokens, 12 heads of 128, bf16: 780 us in 21 segments a head (2.5 TB/s
-// of the 1.6 GB of q, k, v, o and the second reading of k and v).  No unit is
-// full (matrix cores 27 %, VALU 36 %, LDS 39 %): what bounds it is the chain of
-// a chunk's products, its barriers and LDS round trips, 8700 cycles for 128
-// columns.  fp32 multiplies on the fp32 matrix instructions, at a sixteenth of
+// 131072 tokens, 12 heads of 128, bf16: 21 segments a head, 280 us for their
+// states and 445 for the outputs (3.6 TB/s of q, k, v and o).  No unit is full
+// (matrix cores 27 %, VALU 36 %, LDS 39 %): what bounds it is the chain of a
+// chunk's products, its barriers and LDS round trips, 8700 cycles for 128
+// columns alone, some 10500 with every CU busy.  Chunks requested two ahead
+// (a third copy, 158 KB of LDS) gain 2 % there and lose 15 % on sequences of two
+// chunks.  fp32 multiplies on the fp32 matrix instructions, at a sixteenth of
 // bf16's rate: 9.4 of the 14.8 us of a chunk of eight waves are theirs.
 template <typename T, int DK, int NW> constexpr int kCopyBytes =
     kDC * (2 * DK + 16 * NW) * (int)sizeof(T);
@@ -337,9 +339,9 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
   const int h = (int)(unit % a.H), blk = (int)(unit / a.H);
   const int n = sv.find(blk, pass);
   const int seq = sv.seq(n), len = sv.len(n);
-  const int nseg = sv.blk(n + 1, 1) - sv.blk(n, 1) + 1; // (pairs in front: pass 1's blocks)
-  const int seg = blk - sv.blk(n, pass) + pass;
-  const int64_t pair0 = sv.blk(n, 1);
+  const int nseg = sv.blk(n + 1, 1) - sv.blk(n, 1), seg = blk - sv.blk(n, pass);
+  // (states in front: of each cut sequence one more than its blocks in pass 0)
+  const int64_t pair0 = sv.blk(n, 0), state0 = pair0 + sv.blk(n, 2);
   int pos = seg * a.seg;
   const int end = min(len, pos + a.seg);
   const int64_t slot = a.slots ? a.slots[seq] : seq;
@@ -355,13 +357,19 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
   // of column my_col
   f32x4 S[kTD];
   const int64_t global = (slot * a.H + h) * a.dk * a.dv + col0 + my_col;
-  float *pairs =
-      a.pair_state + ((pair0 * a.H + h) * a.slices + slice) * (kTD * 256 * NW) + tid * 4;
-  const int64_t pair_step = (int64_t)a.H * a.slices * (kTD * 256 * NW);
-  if (pass == 1) {
+  const int64_t seg_step = (int64_t)a.H * a.slices * (kTD * 256 * NW);
+  // the state that enters this segment
+  float *entry = a.seg_state + (state0 + seg) * seg_step +
+                 ((int64_t)h * a.slices + slice) * (kTD * 256 * NW) + tid * 4;
+  const auto put_state = [&](float *to) __attribute__((always_inline)) {
 #pragma unroll
     for (int d = 0; d < kTD; ++d)
-      S[d] = *reinterpret_cast<const f32x4 *>(pairs + (seg - 1) * pair_step + d * 256 * NW);
+      *reinterpret_cast<f32x4 *>(to + d * 256 * NW) = S[d];
+  };
+  if (pass == 1 && nseg > 1) {
+#pragma unroll
+    for (int d = 0; d < kTD; ++d)
+      S[d] = *reinterpret_cast<const f32x4 *>(entry + d * 256 * NW);
   } else {
     const bool from = seg == 0 && a.init && kept && my_col < cols;
 #pragma unroll
@@ -371,6 +379,8 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
         const int row = state_tile(d) + 8 * lg + r;
         S[d][r] = from && row < a.dk ? a.init[global + (int64_t)row * a.dv] : 0.f;
       }
+    if (pass == 0 && seg == 0) // (pass 1 may write the last state in its place)
+      put_state(entry);
   }
 
   // Staging.  Wave w's piece i is the (pieces a lane) * w + i-th kilobyte of
@@ -767,19 +777,17 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
         lds_barrier();
     }
   };
-  if (pass == 1 || seg == 0)
+  if (pass == 1)
     walk(std::true_type());
   else
     walk(std::false_type());
+  wait_vmem_all(); // (nothing lands in LDS behind the workgroup's end)
 
-  if (seg < nseg - 1) { // (pass 0)
-    float *to = pairs + seg * pair_step;
-#pragma unroll
-    for (int d = 0; d < kTD; ++d)
-      *reinterpret_cast<f32x4 *>(to + d * 256 * NW) = S[d];
+  if (pass == 0) {
+    put_state(entry + seg_step);
     if (tid == 64 * kScan && slice == 0)
       a.pair_decay[(pair0 + seg) * a.H + h] = decay_sum;
-  } else if (a.fin && kept && my_col < cols) {
+  } else if (seg == nseg - 1 && a.fin && kept && my_col < cols) {
 #pragma unroll
     for (int d = 0; d < kTD; ++d)
 #pragma unroll
@@ -827,7 +835,7 @@ __global__ __launch_bounds__(768, 3) void decay_stream_kernel(SeqTable tab, Deca
     return;
   const int slice = blockIdx.x / 8 % a.slices;
   const int h = (int)(unit % a.H), blk = (int)(unit / a.H);
-  const int n = sv.find(blk, 0);
+  const int n = sv.find(blk, 1);
   const int seq = sv.seq(n), end = sv.len(n);
   int pos = 0;
   const int64_t slot = a.slots ? a.slots[seq] : seq;
@@ -1162,14 +1170,14 @@ __global__ __launch_bounds__(768, 3) void decay_stream_kernel(SeqTable tab, Deca
 // one by one, an element of the state per lane.
 __global__ __launch_bounds__(256) void decay_fold_kernel(SeqTable tab, DecayArgs a, int per) {
   const SeqView sv(tab);
-  const int64_t b = blockIdx.x; // (sequence with middle segments, head, 1024 elements)
+  const int64_t b = blockIdx.x; // (cut sequence, head, 1024 elements)
   const int x = (int)(b % per);
   const int h = (int)(b / per % a.H);
   const int n = sv.find((int)(b / per / a.H), 2);
-  const int64_t pair0 = sv.blk(n, 1), last = sv.blk(n + 1, 1);
+  const int64_t pair0 = sv.blk(n, 0), last = sv.blk(n + 1, 0); // (the segments of pass 0)
   const int64_t step = (int64_t)a.H * per * 256;
-  f32x4 *p = reinterpret_cast<f32x4 *>(a.pair_state) + (pair0 * a.H + h) * per * 256 + x * 256 +
-             threadIdx.x;
+  f32x4 *p = reinterpret_cast<f32x4 *>(a.seg_state) + (pair0 + sv.blk(n, 2) + 1) * step +
+             (h * (int64_t)per + x) * 256 + threadIdx.x;
   f32x4 S = *p;
   for (int64_t i = pair0 + 1; i < last; ++i) {
     p += step;
@@ -1317,10 +1325,13 @@ int64_t num_segments(int64_t len, int64_t seg) { return len <= seg ? 1 : (len + 
 //   wider blocks are: 16 x 2048 tokens: 868 us, streams 1008.  Four waves are
 //   for value heads that eight would leave half empty (32 sequences of 256
 //   tokens, 16 heads of 64: 25 us, eight waves 36, streams 30).
-// - A cut sequence is read twice for k and v and has three launches.  With
-//   streams it is worth it from five segments on (32 heads, 1024 tokens:
-//   cut in four 49 us, a stream 38; 2048: in eight 56, 64; 8192: 149, 227), where
-//   the chunk kernel would take a whole sequence from two and a half.
+// - Of a cut sequence k and v are read twice, in three launches: 2.8 us a chunk
+//   for the states alone, 4.5 for all of it with every CU busy, some 20 us
+//   beside.  A stream takes the whole in 2.0 us a chunk, so that cuts begin to
+//   pay at four segments and 256 tokens (32 heads: 1024 tokens in four segments
+//   44 us, uncut 36; 2048 in eight 52, 63; 8192 133, 217; 48 heads and 32768
+//   tokens in five 730, 1020), where the chunk kernel would take a whole
+//   sequence from two and a half on.
 // - fp32: 14.8 us a chunk with eight waves and 128 columns, 11.2 with four and
 //   64: four where the longest sequence sets the time (9001 tokens in 37 ragged
 //   sequences, 10 heads of 100: 160 us against 182), eight where the number of
@@ -1347,19 +1358,32 @@ DecayPlan decay_plan(int elt, int32_t num_seqs, const int64_t *cu, int32_t H, in
   if (split_hint > 1) {
     p.seg = whole((longest + split_hint - 1) / split_hint);
   } else if (split_hint == 0) {
-    const int64_t seg = std::max<int64_t>(256, whole(share(p.waves)));
-    if (2 * longest >= (p.streams ? 10 : 5) * seg)
+    // (the shortest segments whose workgroups run at once)
+    const auto blocks = [&](int64_t seg) {
+      int64_t all = 0;
+      for (int32_t n = 0; n < num_seqs; ++n)
+        all += num_segments(cu[n + 1] - cu[n], seg);
+      return all * H * slices(p.waves);
+    };
+    int64_t seg = std::max<int64_t>(256, whole(share(p.waves)));
+    while (seg < longest && blocks(seg) > kCUs)
+      seg += whole(seg / 32);
+    if (p.streams ? longest >= 4 * seg + 256 : 2 * longest >= 5 * seg)
       p.seg = seg;
   }
-  for (int32_t n = 0; n < num_seqs; ++n)
-    p.pairs += num_segments(cu[n + 1] - cu[n], p.seg) - 1;
+  int64_t states = 0;
+  for (int32_t n = 0; n < num_seqs; ++n) {
+    const int64_t nseg = num_segments(cu[n + 1] - cu[n], p.seg);
+    p.pairs += nseg - 1;
+    states += nseg > 1 ? nseg : 0;
+  }
   p.streams = p.streams && p.pairs == 0;
   if (elt != 1 && p.pairs == 0 && 3 * std::max(longest, share(4)) < 4 * std::max(longest, share(8)))
     p.waves = 4;
   size_t at = seq_table_bytes(num_seqs);
   p.off_state = at;
   const size_t state = (size_t)slices(p.waves) * 16 * p.waves * padded_dk(dk) * sizeof(float);
-  at = up(at + (size_t)p.pairs * H * state);
+  at = up(at + (size_t)states * H * state);
   p.off_decay = at;
   p.total = up(at + (size_t)p.pairs * H * sizeof(double));
   return p;
@@ -1378,12 +1402,12 @@ hipError_t launch_decay(int elt, const DecayCall &c, int32_t num_seqs, const int
   const int waves = streams ? 4 : plan.waves;
   a.slices = (a.dv + 16 * waves - 1) / (16 * waves);
   a.seg = (int32_t)plan.seg;
-  a.pair_state = (float *)((uint8_t *)ws + plan.off_state);
+  a.seg_state = (float *)((uint8_t *)ws + plan.off_state);
   a.pair_decay = (double *)((uint8_t *)ws + plan.off_decay);
-  // blocks: segments in each pass, and (2) whether there are pairs to fold
+  // blocks: segments in each pass, and (2) whether the sequence is cut
   const auto tiles = [&](int64_t len, int w) -> int64_t {
     const int64_t nseg = num_segments(len, plan.seg);
-    return w == 0 ? std::max<int64_t>(1, nseg - 1) : (w == 1 ? nseg - 1 : nseg > 2);
+    return w == 0 ? nseg - 1 : (w == 1 ? nseg : nseg > 1);
   };
   int64_t total[kCounts];
   if (!seq_totals(num_seqs, cu, tiles, total))
@@ -1403,10 +1427,10 @@ hipError_t launch_decay(int elt, const DecayCall &c, int32_t num_seqs, const int
   const hipError_t e = make_seq_table(tab, num_seqs, cu, tiles, ws, s);
   if (e != hipSuccess)
     return e;
-  a.units = total[0] * a.H;
   if (streams) {
+    a.units = total[1] * a.H;
     const auto kernel = a.dk <= 64 ? decay_stream_kernel<64> : decay_stream_kernel<128>;
-    kernel<<<(unsigned)grid[0], threads, 0, s>>>(tab, a, (const bf16 *)c.io.q, (const bf16 *)c.io.k,
+    kernel<<<(unsigned)grid[1], threads, 0, s>>>(tab, a, (const bf16 *)c.io.q, (const bf16 *)c.io.k,
                                                  (const bf16 *)c.io.v, (bf16 *)c.io.o);
     return hipGetLastError();
   }
@@ -1421,11 +1445,11 @@ hipError_t launch_decay(int elt, const DecayCall &c, int32_t num_seqs, const int
                                                       (const T *)c.io.k, (const T *)c.io.v,
                                                       (T *)c.io.o);
     };
-    chunks(0);
-    if (fold > 0)
+    if (plan.pairs > 0) {
+      chunks(0);
       decay_fold_kernel<<<(unsigned)fold, 256, 0, s>>>(tab, a, per);
-    if (total[1] > 0)
-      chunks(1);
+    }
+    chunks(1);
     return hipGetLastError();
   };
   using std::integral_constant;
