@@ -131,22 +131,22 @@ __device__ __forceinline__ double lane_f64(double x, int lane) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// exp(d) for d <= 0: exp2 of the product with log2(e), whose rounding and the
-// constant's are put back to first order.
+// exp(d) for d <= 0 (0 from -104 down, -inf too; NaN for NaN): exp2 of the
+// rounded product t with log2(e), and to first order what t leaves of d,
+// d - t ln(2) in one operation (fp32's ln(2) is 3e-9 off).
 __device__ __forceinline__ float exp_neg(float d) {
-  constexpr float c1 = 0x1.715476p+0f, c2 = 0x1.4ae0bep-26f, ln2 = 0x1.62e43p-1f;
-  const float t = d * c1;
-  const float r = fmaf(d, c2, fmaf(d, c1, -t));
+  d = __builtin_elementwise_maximum(d, -104.f);
+  const float t = d * 0x1.715476p+0f;
   const float e = __builtin_amdgcn_exp2f(t);
-  return t < -126.f ? e : fmaf(e, r * ln2, e); // (there d may be -inf)
+  return fmaf(e, fmaf(t, -0x1.62e43p-1f, d), e);
 }
 
-// 64 x 8 beams of 128001 bf16 logits: 8192 workgroups, 43 us (3.0 TB/s), bound
-// by the vector units: some 600 instructions a wave for 32 logits a lane, 12
-// for each exp with its sum, of about 32 us; the loads of the eight workgroups
-// of a CU hide behind them.  The threshold from 256 lanes' maxima by bits costs
-// one wave 16 (32) steps of four ballots; from groups of each wave's lanes, and
-// an LDS atomic for each element found, it took 66 us.
+// 64 x 8 beams of 128001 bf16 logits: 8192 workgroups, 41 us (3.2 TB/s), bound
+// by the vector units: some 520 instructions a wave for 32 logits a lane, nine
+// for each exp with its sum, about 33 us; the loads of the eight workgroups of a
+// CU hide behind them.  The threshold from 256 lanes' maxima by bits costs one
+// wave 16 (32) steps of four ballots; from groups of each wave's lanes, and an
+// LDS atomic for each element found, all of it took 66 us.
 template <typename T>
 __global__ __launch_bounds__(256) void beam_part_kernel(BeamArgs a, const T *__restrict__ logits,
                                                         Cand *__restrict__ cand,
