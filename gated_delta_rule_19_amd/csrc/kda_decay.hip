@@ -1358,12 +1358,16 @@ DecayPlan decay_plan(int elt, int32_t num_seqs, const int64_t *cu, int32_t H, in
   if (split_hint > 1) {
     p.seg = whole((longest + split_hint - 1) / split_hint);
   } else if (split_hint == 0) {
-    // (the shortest segments whose workgroups run at once)
+    // (the shortest segments whose workgroups run at once, if sequences that
+    // are shorter share CUs as their tokens let them)
     const auto blocks = [&](int64_t seg) {
-      int64_t all = 0;
-      for (int32_t n = 0; n < num_seqs; ++n)
-        all += num_segments(cu[n + 1] - cu[n], seg);
-      return all * H * slices(p.waves);
+      int64_t cut = 0, rest = 0;
+      for (int32_t n = 0; n < num_seqs; ++n) {
+        const int64_t len = cu[n + 1] - cu[n];
+        cut += len > seg ? num_segments(len, seg) : 0;
+        rest += len > seg ? 0 : len;
+      }
+      return (cut + (rest + seg - 1) / seg) * H * slices(p.waves);
     };
     int64_t seg = std::max<int64_t>(256, whole(share(p.waves)));
     while (seg < longest && blocks(seg) > kCUs)

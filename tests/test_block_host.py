@@ -110,6 +110,16 @@ def test_decay_attention_workspace(lib):
     assert size(1, p4, 1, 128, 128, BF16, 0) > 0 and size(1, p4, 1, 128, 128, F32, 0) > 0
 
 
+def test_a_long_sequence_among_many_short_ones_is_cut(lib):
+    """... and a batch of many equal ones is not."""
+    size = lib.kda_decay_attention_workspace_size
+    keep, p = cu_ptr(*np.concatenate([[0], np.cumsum([20000] + [30] * 300)]))
+    keep2, p2 = cu_ptr(*range(0, 64 * 501, 500))
+    for dt in (F32, BF16):
+        assert size(301, p, 2, 128, 128, dt, 0) >= size(301, p, 2, 128, 128, dt, 8)
+        assert size(64, p2, 16, 128, 128, dt, 0) == 0
+
+
 @pytest.mark.parametrize("status,io,kw", [(s, d, {}) for s, d in BAD_IO] + [
     (UNSUPPORTED, {}, dict(dt=9)), (INVALID, {}, dict(rows=-1)), (INVALID, {}, dict(state=None)),
     (INVALID, {}, dict(state=PTR + 5 * M + 8)), (INVALID, {}, dict(num_slots=2)),
