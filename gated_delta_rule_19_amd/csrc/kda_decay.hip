@@ -301,11 +301,10 @@ __device__ __forceinline__ void reads_stay() { __builtin_amdgcn_sched_barrier(0x
 //
 // 131072 tokens, 12 heads of 128, bf16: 21 segments a head, 280 us for their
 // states and 445 for the outputs (3.6 TB/s of q, k, v and o).  No unit is full
-// (matrix cores 27 %, VALU 36 %, LDS 39 %): what bounds it is the chain of a
-// chunk's products, its barriers and LDS round trips, 8700 cycles for 128
-// columns alone, some 10500 with every CU busy.  Chunks requested two ahead
-// (a third copy, 158 KB of LDS) gain 2 % there and lose 15 % on sequences of two
-// chunks.  fp32 multiplies on the fp32 matrix instructions, at a sixteenth of
+// (matrix cores 22 %): what bounds it is the chain of a chunk's products, its
+// barriers and LDS round trips, 8700 cycles for 128 columns alone, some 10500
+// with every CU busy.  Chunks requested two ahead (a third copy, 158 KB of LDS)
+// gain 2 % there and lose 15 % on sequences of two chunks.  fp32 multiplies on the fp32 matrix instructions, at a sixteenth of
 // bf16's rate: 9.4 of the 14.8 us of a chunk of eight waves are theirs.
 template <typename T, int DK, int NW> constexpr int kCopyBytes =
     kDC * (2 * DK + 16 * NW) * (int)sizeof(T);
