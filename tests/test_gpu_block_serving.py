@@ -387,3 +387,90 @@ def test_beam_search(order):
                 if tok == eos:
                     break
             assert abs(float(scores[b, w]) - total) <= steps * 2 * rel * float(row.abs().max())
+
+
+# ---- calls at the edge of what is documented ----------------------------------------------
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("split", [1, 4])
+def test_states_in_place_and_in_pools(split, dtype):
+    """final_state in initial_state's place, in slots of a pool, some of them
+    out of range: the same as with buffers of their own, and no other slice
+    changes.  Cut or not."""
+    print("in place", split, dtype, flush=True)
+    cu, H, dk, dv = [0, 500, 500, 577, 900], 3, 64, 40
+    g = gen(90)
+    q, k, v = f(g, 900, H, dk).to(dtype), (f(g, 900, H, dk) * dk ** -0.5).to(dtype), f(g, 900, H, dv).to(dtype)
+    gl = -torch.rand(900, H, device=DEV, generator=g) * 0.05
+    pool = f(g, 6, H, dk, dv)
+    slots = torch.tensor([4, 1, 9, 0], dtype=torch.int32, device=DEV)
+    init = pool[[4, 1, 0, 0]].clone()
+    init[2] = 0  # (a slot out of range: from nothing)
+    o, fin = kda.decay_attention(q, k, v, gl, cu_seqlens=cu, initial_state=init, split_hint=split)
+    before = pool.clone()
+    o2, _ = kda.decay_attention(q, k, v, gl, cu_seqlens=cu, initial_state=pool, final_state=pool, slots=slots,
+                                split_hint=split)
+    torch.cuda.synchronize()
+    assert torch.equal(o, o2)
+    for s, n in ((4, 0), (1, 1), (0, 3)):
+        assert torch.equal(pool[s], fin[n])
+    assert torch.equal(pool[[2, 3, 5]], before[[2, 3, 5]])
+
+
+def test_logits_below_the_normal_numbers_keep_their_order():
+    """Within a beam the logits' own order decides, where 64-bit values are
+    equal too."""
+    print("denormal logits", flush=True)
+    for dtype, unit in ((F32, 2.0 ** -149), (BF16, 2.0 ** -133)):
+        x = torch.full((1, 1, 9000), -1.0, dtype=dtype)
+        at = torch.tensor([8999, 17, 4096, 5000, 0])
+        x[0, 0, at] = (torch.tensor([5.0, 4.0, 3.0, 0.0, -1.0], dtype=torch.float64) * unit).to(dtype)
+        x[0, 0, 40] = -0.0  # (as 0: the lower token goes first)
+        _, _, tokens, _ = kda.beam_select(x.to(DEV), torch.zeros(1, 1, device=DEV), beams=6)
+        assert tokens[0].tolist() == [8999, 17, 4096, 40, 5000, 0]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_masks_of_the_lowest_value(dtype):
+    """A few tokens allowed, the others at the type's lowest value, over many
+    parts: these tie, and the first of them follow the allowed ones."""
+    print("lowest masks", dtype, flush=True)
+    V = 40000
+    x = torch.full((2, 3, V), torch.finfo(dtype).min, dtype=dtype)
+    g = torch.Generator().manual_seed(91)
+    for b in range(2):
+        for w in range(3):
+            x[b, w, torch.randperm(V, generator=g)[:2 + w]] = torch.randn(2 + w, generator=g).to(dtype)
+    scores = torch.tensor([[0.0, -1.0, -2.0], [-3.0, -0.5, 0.0]])
+    for K in (3, 8, 64):
+        got = kda.beam_select(x.to(DEV), scores.to(DEV), beams=K)
+        want = ref.beam_select(x, scores, K)
+        assert torch.equal(got[1].cpu(), want[1]) and torch.equal(got[2].cpu(), want[2])
+
+
+def test_the_same_parent_for_every_row_and_every_kind_of_state():
+    """One parent for all rows, states of every type and of a byte a slice,
+    beams of every count the reordering has its own way for."""
+    print("one parent", flush=True)
+    for K in (1, 2, 4, 5, 8, 9, 16, 17, 32, 33, 64):
+        g = gen(92 + K)
+        states = [f(g, 2 * K, 3, 7), f(g, 2 * K, 130).to(BF16), torch.randint(-9, 9, (2 * K, 1), device=DEV, generator=g).to(torch.int8),
+                  f(g, 2 * K, 33).to(torch.float8_e4m3fn).view(torch.int8), torch.zeros(2 * K, 0, device=DEV)]
+        parents = torch.randint(0, K, (2, 1), device=DEV, generator=g, dtype=torch.int32).expand(2, K).contiguous()
+        want = [ref.reorder(s.cpu(), parents.cpu()) for s in states]
+        kda.state_reorder(states, parents)
+        torch.cuda.synchronize()
+        for s, w in zip(states, want):
+            assert torch.equal(s.cpu(), w)
+
+
+def test_empty_and_single_rows_of_a_batch():
+    """Sequences without tokens only, a step of one row, a norm of one column."""
+    print("smallest", flush=True)
+    state = f(gen(95), 3, 2, 8, 8)
+    e = torch.empty(0, 2, 8, device=DEV)
+    o, fin = kda.decay_attention(e, e, e, torch.empty(0, 2, device=DEV), cu_seqlens=[0, 0, 0, 0], initial_state=state)
+    assert o.shape == (0, 2, 8) and torch.equal(fin, state)
+    x = torch.tensor([[3.0], [-2.0], [0.0]], device=DEV)
+    r, y = kda.block_norm(x, torch.ones(1, device=DEV), eps=0.0, residual=torch.zeros_like(x))
+    assert r.view(-1).tolist() == [3.0, -2.0, 0.0] and y[:2].view(-1).tolist() == [1.0, -1.0] and torch.isnan(y[2, 0])
