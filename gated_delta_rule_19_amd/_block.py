@@ -19,6 +19,14 @@ _ORDERS = {"score": 0, "rows": 1}
 _MAX_STATES = 32
 
 
+def _new(like, shape, dtype):
+    """A dense output on like's device (torch makes one of like's shape in 1.15
+    us, one from a shape in 1.65)."""
+    if like.shape == shape and like.is_contiguous():
+        return torch.empty_like(like, dtype=dtype)
+    return torch.empty(shape, dtype=dtype, device=like.device)
+
+
 def _decay_io(q, k, v, g, scale, o):
     """The attention's argument block, checked; o still to be filled in if None."""
     for x, name in ((q, "q"), (k, "k"), (v, "v")):
@@ -72,7 +80,7 @@ def decay_attention(q, k, v, g, scale: float = 1.0, cu_seqlens=None, initial_sta
     pool = _pools(initial_state, final_state, n, slots, (H, dk, dv), torch.float32)
     dev = _device(q, k, v, g, initial_state, final_state, slots, o, workspace)
     if o is None:
-        o = torch.empty((T, H, dv), dtype=q.dtype, device=dev)
+        o = _new(v, (T, H, dv), q.dtype)
     io.o = _p(o)
     if final_state is None and output_final_state and slots is None:
         final_state = torch.empty((n, H, dk, dv), dtype=torch.float32, device=dev)
@@ -98,7 +106,7 @@ def decay_attention_step(state, q, k, v, g, scale: float = 1.0, slots=None, o=No
     _dense(state, (pool, H, dk, dv), torch.float32, "state")
     dev = _device(q, k, v, g, state, slots, o)
     if o is None:
-        o = torch.empty((rows, H, dv), dtype=q.dtype, device=dev)
+        o = _new(v, (rows, H, dv), q.dtype)
     io.o = _p(o)
     _call("kda_decay_attention_step", dev, rows, H, code, ctypes.byref(io), _p(state), _p(slots),
           pool)
@@ -151,12 +159,12 @@ def block_norm(x, weight=None, eps: float = 1e-6, residual=None, scale=1.0, gate
     if residual_out is not None:
         ros = _rows(residual_out, shape, rdt, "residual_out")
     elif residual is not None or weight is None:
-        residual_out = torch.empty(shape, dtype=rdt, device=dev)
+        residual_out = _new(x, shape, rdt)
         ros = D
     if y is not None:
         ys = _rows(y, shape, dt, "y")
     elif weight is not None:
-        y = torch.empty(shape, dtype=dt, device=dev)
+        y = _new(x, shape, dt)
         ys = D
     # (in one go: a field set by name costs more than the checks)
     io = NormIo(x.data_ptr(), _p(gate), _p(residual), _p(residual_out), _p(y), xs, gs, rs, ros, ys,
@@ -203,10 +211,10 @@ def beam_select(logits, scores, beams=None, finished=None, eos: int = -1, order:
     args = (_count(B, "the batch"), W, _count(V, "the vocabulary"), K, code)
     ws = _workspace(workspace, load().kda_beam_select_workspace_size(*args), dev)
     shape = (B, K)
-    out = torch.empty(shape, dtype=torch.float32, device=dev)
-    parents = torch.empty(shape, dtype=torch.int32, device=dev)
-    tokens = torch.empty(shape, dtype=torch.int32, device=dev)
-    done = torch.empty(shape, dtype=torch.bool, device=dev)
+    out = _new(scores, shape, torch.float32)
+    parents = _new(scores, shape, torch.int32)
+    tokens = _new(scores, shape, torch.int32)
+    done = _new(scores, shape, torch.bool)
     _call("kda_beam_select", dev, *args, _p(logits), stride, _p(scores), _p(finished),
           _count(int(eos), "eos"), _ORDERS[order], _p(out), _p(parents), _p(tokens), _p(done),
           _p(ws), 0 if ws is None else ws.numel())
