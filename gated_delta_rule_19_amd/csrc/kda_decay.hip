@@ -297,7 +297,8 @@ __device__ __forceinline__ void reads_stay() { __builtin_amdgcn_sched_barrier(0x
 // addresses are multiples of 16 bytes: everything moves through raw buffers,
 // whose bounds take the place of branches at a chunk's end, and q, K and V
 // straight into LDS.  AHEAD: a chunk ahead into the other one of two copies;
-// without, the loads of the one copy are waited for.
+// TURNS, where LDS holds no two: each of the three as its place gets free;
+// without either, the loads of the one copy are waited for.
 //
 // 131072 tokens, 12 heads of 128, bf16: 21 segments a head, 280 us for their
 // states and 445 for the outputs (3.6 TB/s of q, k, v and o).  No unit is full
@@ -305,7 +306,9 @@ __device__ __forceinline__ void reads_stay() { __builtin_amdgcn_sched_barrier(0x
 // barriers and LDS round trips, 8700 cycles for 128 columns alone, some 10500
 // with every CU busy.  Chunks requested two ahead (a third copy, 158 KB of LDS)
 // gain 2 % there and lose 15 % on sequences of two chunks.  fp32 multiplies on the fp32 matrix instructions, at a sixteenth of
-// bf16's rate: 9.4 of the 14.8 us of a chunk of eight waves are theirs.
+// bf16's rate: 9.4 of the 13.1 us of a chunk of eight waves are theirs (with all
+// loads waited for, without TURNS, a chunk took 14.8; bf16 heads of 256: 5.5 us,
+// 4.7).
 template <typename T, int DK, int NW> constexpr int kCopyBytes =
     kDC * (2 * DK + 16 * NW) * (int)sizeof(T);
 template <typename T, int DK, int NW, bool FAST>
@@ -320,10 +323,14 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
   constexpr int kNK = DK * kEs / (16 * NW);     // pieces of K (q) a lane stages
   constexpr int kNV = kEs;                      // pieces of V a lane stages
   constexpr bool AHEAD = FAST && 2 * kCopyBytes<T, DK, NW> <= 98304;
-  constexpr int kBufs = AHEAD ? 2 : 1;
+  // TURNS: K alone has two copies; V is free once every wave holds its columns,
+  // q once the scores and S^T q are formed.
+  constexpr bool TURNS =
+      FAST && !AHEAD && kCopyBytes<T, DK, NW> + kDC * (DK + kDC) * kEs <= 155648;
+  constexpr int kBufs = AHEAD ? 2 : 1, kKBufs = AHEAD || TURNS ? 2 : 1;
   // (bf16 has room for the scores beside q; fp32 puts them in its place)
   constexpr bool OWN_P = kEs == 2;
-  __shared__ alignas(16) T Qs[kBufs][kDC * DK], Ks[kBufs][kDC * DK], Vs[kBufs][kDC * kCols];
+  __shared__ alignas(16) T Qs[kBufs][kDC * DK], Ks[kKBufs][kDC * DK], Vs[kBufs][kDC * kCols];
   __shared__ alignas(16) T Ps[OWN_P ? kDC * kDC : 8];
   __shared__ alignas(16) float Ghi[2][kDC], Glo[2][kDC], wts[2][kDC], eG[2][kDC];
   __shared__ float total[2];
@@ -426,9 +433,9 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
     if (i < kNK)
       stage(RowDK(), Ks[buf], s.k, ks, a.dk, cnt, kNK, i);
     else if (i < kNK + kNV)
-      stage(RowV(), Vs[buf], s.v, vs, cols, cnt, kNV, i - kNK);
+      stage(RowV(), Vs[AHEAD ? buf : 0], s.v, vs, cols, cnt, kNV, i - kNK);
     else
-      stage(RowDK(), Qs[buf], s.q, qs, a.dk, cnt, kNK, i - kNK - kNV);
+      stage(RowDK(), Qs[AHEAD ? buf : 0], s.q, qs, a.dk, cnt, kNK, i - kNK - kNV);
   };
   float gn = 0.f;
   constexpr int kScan = NW - 1; // the wave that sums the decays (8 waves: it has no scores)
@@ -479,7 +486,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
       z += at(Ks[buf], kNK, i);
 #pragma unroll
     for (int i = 0; i < kNV; ++i)
-      z += at(Vs[buf], kNV, i);
+      z += at(Vs[AHEAD ? buf : 0], kNV, i);
     int bad = kDC;
     if (__builtin_expect(__any(z != z), 0)) {
       int row, c;
@@ -490,7 +497,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
       }
       for (int i = 0; i < kNV; ++i) {
         piece(RowV(), kNV, i, row, c);
-        const float x = at(Vs[buf], kNV, i);
+        const float x = at(Vs[AHEAD ? buf : 0], kNV, i);
         bad = x != x ? min(bad, row) : bad;
       }
       for (int b = 1; b < 64; b <<= 1)
@@ -507,7 +514,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
     // through every chunk)
     const int group = opaque_lane() >> 4;
     const T *qb = q + (tok0 + pos) * a.qs + (int64_t)(h / a.rq) * a.dk;
-    const float x = to_f32(Vs[buf][lds_at<T, kCols>(0, my_col)]), all = total[par];
+    const float x = to_f32(Vs[AHEAD ? buf : 0][lds_at<T, kCols>(0, my_col)]), all = total[par];
     float sum = 0.f;
 #pragma unroll
     for (int d = 0; d < kTD; ++d)
@@ -544,7 +551,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
       return;
     const auto first_loads = [&]() __attribute__((always_inline)) {
       const Source s = source(pos);
-      if constexpr (AHEAD)
+      if constexpr (AHEAD || TURNS)
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
           stage_one(s, cnt, buf, i);
@@ -553,7 +560,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
     };
     first_loads();
     while (true) {
-      if constexpr (!AHEAD) { // (every wave is done with the tile before)
+      if constexpr (!AHEAD && !TURNS) { // (every wave is done with the tile before)
         const Source s = source(pos);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
@@ -581,7 +588,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
           for (int i = tid; i < (kDC - cnt) * DK; i += 64 * NW)
             Ks[buf][cnt * DK + i] = from_f32<T>(0.f);
           for (int i = tid; i < (kDC - cnt) * kCols; i += 64 * NW)
-            Vs[buf][cnt * kCols + i] = from_f32<T>(0.f);
+            Vs[AHEAD ? buf : 0][cnt * kCols + i] = from_f32<T>(0.f);
         }
         lds_barrier();
         if (bad == 0) { // itself, by the recurrence
@@ -608,14 +615,31 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
           for (int i = 0; i < kLoads; ++i)
             if (i * kSteps / kLoads == step)
               stage_one(s, next_cnt, buf ^ 1, i);
+        if constexpr (TURNS)
+#pragma unroll
+          for (int i = 0; i < kNK; ++i) { // K; with outputs q in the second half
+            if (i * (OUT ? 8 : kSteps) / kNK == step)
+              stage_one(s, next_cnt, buf ^ 1, i);
+            if (OUT && 8 + i * 8 / kNK == step)
+              stage_one(s, next_cnt, buf, kNK + kNV + i);
+          }
+      };
+      const auto request_v = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < kNV; ++i)
+          stage_one(s, next_cnt, buf, kNK + i);
       };
       load_g(s, next_cnt);
-      const T *Qb = Qs[buf], *Kb = Ks[buf], *Vb = Vs[buf];
+      const T *Qb = Qs[AHEAD ? buf : 0], *Kb = Ks[buf], *Vb = Vs[AHEAD ? buf : 0];
       const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
       Frag<T> vf[2]; // this wave's columns of V, tokens 0 .. 31 and 32 .. 63
 #pragma unroll
       for (int c = 0; c < 2; ++c)
         vf[c] = tr_frag(Vb + 32 * c * kCols, kCols, v_tr, 0);
+      if constexpr (TURNS && !OUT) {
+        lds_barrier(); // every wave holds its columns of V
+        request_v();
+      }
 
       if constexpr (OUT) {
         // Scores: unit u is tokens 16 t .. of q against tokens 32 c .. of k,
@@ -670,7 +694,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
           reads_stay();
         }
         const float *gh = Ghi[par], *gl = Glo[par];
-        T *Pb = OWN_P ? Ps : Qs[buf];
+        T *Pb = OWN_P ? Ps : Qs[AHEAD ? buf : 0];
         if constexpr (!OWN_P)
           lds_barrier(); // every wave has read q
 #pragma unroll
@@ -694,6 +718,8 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
           }
         }
         lds_barrier(); // the scores are there
+        if constexpr (TURNS)
+          request_v();
         T *ob = o + (tok0 + pos) * a.os + (int64_t)h * a.dv + col0;
         const auto ro =
             buffer_rsrc(ob, (uint32_t)(((cnt - 1) * os + cols) * kEs));
@@ -726,6 +752,8 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
                 ob[i * os + c + r] = from_f32<T>(O[t][r]);
           }
         }
+        if constexpr (TURNS && !OWN_P)
+          lds_barrier(); // the scores are read: q may come in their place
       }
 
       // The state's update, four row tiles at a time, each four's operands
@@ -770,7 +798,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
       cnt = next_cnt;
       par ^= 1;
       scan_decays(cnt);
-      if constexpr (AHEAD)
+      if constexpr (AHEAD || TURNS)
         buf ^= 1;
       else
         lds_barrier();
@@ -1331,10 +1359,10 @@ int64_t num_segments(int64_t len, int64_t seg) { return len <= seg ? 1 : (len + 
 //   44 us, uncut 36; 2048 in eight 52, 63; 8192 133, 217; 48 heads and 32768
 //   tokens in five 730, 1020), where the chunk kernel would take a whole
 //   sequence from two and a half on.
-// - fp32: 14.8 us a chunk with eight waves and 128 columns, 11.2 with four and
+// - fp32: 13.1 us a chunk with eight waves and 128 columns, 9.8 with four and
 //   64: four where the longest sequence sets the time (9001 tokens in 37 ragged
-//   sequences, 10 heads of 100: 160 us against 182), eight where the number of
-//   workgroups does (37 sequences of 243: 138 us against 148).
+//   sequences, 10 heads of 100: 153 us against 167), eight where the number of
+//   workgroups does (37 sequences of 243: 123 us against 140).
 constexpr int64_t kCUs = 256;
 
 DecayPlan decay_plan(int elt, int32_t num_seqs, const int64_t *cu, int32_t H, int32_t dk,
