@@ -305,10 +305,12 @@ __device__ __forceinline__ void reads_stay() { __builtin_amdgcn_sched_barrier(0x
 // (matrix cores 22 %): what bounds it is the chain of a chunk's products, its
 // barriers and LDS round trips, 8700 cycles for 128 columns alone, some 10500
 // with every CU busy.  Chunks requested two ahead (a third copy, 158 KB of LDS)
-// gain 2 % there and lose 15 % on sequences of two chunks.  fp32 multiplies on the fp32 matrix instructions, at a sixteenth of
-// bf16's rate: 9.4 of the 13.1 us of a chunk of eight waves are theirs (with all
-// loads waited for, without TURNS, a chunk took 14.8; bf16 heads of 256: 5.5 us,
-// 4.7).
+// gain 2 % there and lose 15 % on sequences of two chunks.
+//
+// fp32 multiplies on the fp32 matrix instructions, at a sixteenth of bf16's
+// rate: 9.4 of the 13.1 us of a chunk of eight waves are theirs.  With all loads
+// waited for, without TURNS, a chunk took 14.8; one of bf16 heads of 256 5.5 us,
+// now 4.7.
 template <typename T, int DK, int NW> constexpr int kCopyBytes =
     kDC * (2 * DK + 16 * NW) * (int)sizeof(T);
 template <typename T, int DK, int NW, bool FAST>
