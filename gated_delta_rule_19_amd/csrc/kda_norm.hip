@@ -16,7 +16,7 @@
 // than four (205 us), and non-temporal accesses, here larger than all caches,
 // gain as much (cached: 216 us).  20000 x 1002 fp32: 82 us for 401 MB (4.9
 // TB/s): rows that end inside a 128-byte line cost a tenth (1024 columns: 5.5).
-// One row: 6.6 us on the GPU, the latency of three rounds to memory and two
+// One row: 5.0 us on the GPU, the latency of three rounds to memory and two
 // joins of sums.
 #include "kda_block.h"
 #include "kda_device.h"
