@@ -54,8 +54,8 @@ struct DecayArgs {
 };
 
 constexpr float kMinDecay = -150.f; // fp32's exp is 0 there
-// exp(g), 0 from kMinDecay down (and for -inf)
-__device__ __forceinline__ float decay_of(float g) { return expf(fmaxf(g, kMinDecay)); }
+// exp(g), 0 from kMinDecay down (and for -inf); NaN for NaN
+__device__ __forceinline__ float decay_of(float g) { return expf(g < kMinDecay ? kMinDecay : g); }
 
 // Numbers of some 48 bits as the sum of two fp32 ones, hi the sum rounded.
 struct Pair {

@@ -474,3 +474,36 @@ def test_empty_and_single_rows_of_a_batch():
     x = torch.tensor([[3.0], [-2.0], [0.0]], device=DEV)
     r, y = kda.block_norm(x, torch.ones(1, device=DEV), eps=0.0, residual=torch.zeros_like(x))
     assert r.view(-1).tolist() == [3.0, -2.0, 0.0] and y[:2].view(-1).tolist() == [1.0, -1.0] and torch.isnan(y[2, 0])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lengths,split", [([150, 70], 1), ([150, 70], 2), ([60] * 90, 1)])
+def test_a_decay_of_nan_spoils_what_follows_it_only(lengths, split, dtype):
+    """Prompts and single tokens: the outputs before it, other heads and other
+    sequences stay what they are."""
+    print("nan decay", len(lengths), split, dtype, flush=True)
+    cu = [0] + np.cumsum(lengths).tolist()
+    T, H, d, at = cu[-1], 4, 64, 37
+    g = gen(97)
+    q, k, v = f(g, T, H, d).to(dtype), (f(g, T, H, d) * d ** -0.5).to(dtype), f(g, T, H, d).to(dtype)
+    gl = -torch.rand(T, H, device=DEV, generator=g) * 0.1
+    clean, cfin = kda.decay_attention(q, k, v, gl, cu_seqlens=cu, split_hint=split)
+    bad = gl.clone()
+    bad[at, 0] = float("nan")
+    o, fin = kda.decay_attention(q, k, v, bad, cu_seqlens=cu, split_hint=split)
+    end = cu[1]
+    torch.cuda.synchronize()
+    assert torch.equal(o[:at], clean[:at]) and torch.equal(o[:, 1:], clean[:, 1:]) and torch.equal(o[end:], clean[end:])
+    assert torch.isnan(o[at:end, 0].float()).all()
+    assert torch.isnan(fin[0, 0]).all()
+    assert torch.equal(fin[0, 1:], cfin[0, 1:]) and torch.equal(fin[1:], cfin[1:])
+
+    state = f(g, 3, H, d, d)
+    want = state.clone()
+    rows = slice(at - 1, at + 2)
+    wo = kda.decay_attention_step(want, q[rows], k[rows], v[rows], gl[rows])
+    so = kda.decay_attention_step(state, q[rows], k[rows], v[rows], bad[rows])
+    torch.cuda.synchronize()
+    assert torch.isnan(so[1, 0].float()).all() and torch.isnan(state[1, 0]).all()
+    so[1, 0], state[1, 0] = wo[1, 0], want[1, 0]
+    assert torch.equal(so, wo) and torch.equal(state, want)
