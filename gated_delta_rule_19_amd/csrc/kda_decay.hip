@@ -523,8 +523,10 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int row = state_tile(d) + 8 * group + r;
+        if (row >= a.dk) // (stays 0 beside an infinite x)
+          continue;
         S[d][r] = fmaf(to_f32(Ks[buf][lds_at<T, DK>(0, row)]), x, all * S[d][r]);
-        if (decltype(out_tag)::value && row < a.dk)
+        if (decltype(out_tag)::value)
           sum = fmaf(to_f32(qb[row]), S[d][r], sum);
       }
     if constexpr (decltype(out_tag)::value) {
@@ -1061,10 +1063,10 @@ __global__ __launch_bounds__(768, 3) void decay_stream_kernel(SeqTable tab, Deca
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int row = state_tile(d) + 8 * group + r;
-          const bool in = row < a.dk;
-          S[d][r] = fmaf(in ? to_f32(k0[at * ks + row]) : 0.f, x, decay * S[d][r]);
-          if (in)
-            sum = fmaf(to_f32(q0[at * qs + row]), S[d][r], sum);
+          if (row >= a.dk) // (stays 0 beside an infinite x)
+            continue;
+          S[d][r] = fmaf(to_f32(k0[at * ks + row]), x, decay * S[d][r]);
+          sum = fmaf(to_f32(q0[at * qs + row]), S[d][r], sum);
         }
       sum = add_xor32(add_xor16(sum));
       if (lg == 0 && my_col < cols)
