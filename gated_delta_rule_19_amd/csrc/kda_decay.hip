@@ -26,9 +26,13 @@
 // G is summed and kept as two fp32 numbers, so that differences within a chunk
 // keep their accuracy beside a decay of e^-150.
 //
-// An infinity or NaN in k or v would reach earlier tokens of its chunk as
-// 0 * inf: a chunk is ended in front of such a token, which is then worked on
-// alone, its update as an outer product.
+// Ends of fp32's range.  Where an infinity or a NaN, growth past fp32, or an
+// infinite state under a decay that underflows over a chunk would meet a 0 in
+// these products (an infinity in k or v would even reach earlier tokens of its
+// chunk), a wave's columns of the chunk go by the recurrence, token by token.
+// All of these show in o: a wave that finds one of its outputs not finite looks
+// for the cause (see by_recurrence), so that other chunks pay an operation a
+// value.  Launches that form only states look at k, v and the decay instead.
 #include "kda_block.h"
 #include "kda_device.h"
 
@@ -79,6 +83,26 @@ __device__ __forceinline__ Pair log2_decay(float g) {
   g = g < kMinDecay ? kMinDecay : g; // (a NaN stays one)
   const float hi = g * c1;
   return {hi, fmaf(g, c2, fmaf(g, c1, -hi))};
+}
+// Whether the decays of a chunk (a token a lane; 0 behind the last) grow a
+// state by more than some 2^64 on the way: by tokens then, lest factors of 2^127
+// and more meet small k and v.
+__device__ __forceinline__ bool grows(float g) {
+  if (__builtin_expect(!__any(g > 0.f), 1))
+    return false;
+  float up = fmaxf(g, 0.f);
+  for (int b = 1; b < 64; b <<= 1)
+    up += __shfl_xor(up, b);
+  return !(up < 44.f);
+}
+// log2 of a chunk's decay, from the sum over its tokens: -inf where a token's is
+// 0 (fp32's exp is, below -104), which an infinite state does not outlast.
+__device__ __forceinline__ double log2_total(const Pair &sum, float g) {
+  constexpr float kNone = -104.f;
+  if (__builtin_expect(!__any(!(g >= kNone && g < __builtin_inff())), 1))
+    return (double)sum.hi + (double)sum.lo;
+  return (__any(g < kNone) ? -__builtin_inf() : 0.) + (__any(g == __builtin_inff()) ? __builtin_inf() : 0.) +
+         (__any(g != g) ? __builtin_nan("") : 0.);
 }
 // Sum over lanes 0 .. of a wave up to each (DPP: 1, 2, 4 and 8 lanes within
 // rows of 16, then the ends of rows to those behind).
@@ -263,6 +287,106 @@ __device__ __forceinline__ Whole weigh(const Frag<float> &v, const f32x4 &w0, co
   return {{{v.lo * w0, v.hi * w1}}};
 }
 
+__device__ __forceinline__ float zero_sum(const Frag<bf16> &f) {
+  return zero_sum(__builtin_bit_cast(u32x4, f.v), bf16());
+}
+__device__ __forceinline__ float zero_sum(const Frag<float> &f) {
+  return zero_sum(__builtin_bit_cast(u32x4, f.lo), 0.f) + zero_sum(__builtin_bit_cast(u32x4, f.hi), 0.f);
+}
+
+// ---- tokens one by one ------------------------------------------------------------
+
+// One head's tokens from a place on.
+template <typename T> struct Tokens {
+  const T *q, *k, *v;
+  const float *g;
+  T *o;
+};
+
+// `count` of them by the recurrence, in fp32 and straight from memory: this
+// lane's column `col` of the state (`in`: there is one), and with OUT o from the
+// state after a token (this lane's rows, summed over the four lane groups).
+template <bool OUT, typename T, int TD>
+__device__ __forceinline__ void by_token(f32x4 (&S)[TD], const DecayArgs &a, const Tokens<T> &s,
+                                         int count, int col, bool in) {
+#pragma unroll 1
+  for (int i = 0; i < count; ++i) {
+    // (rare: opaque, lest its addresses and conditions be kept in registers)
+    const int group = opaque_lane() >> 4;
+    const float decay = decay_of(s.g[i * a.gs]), x = in ? to_f32(s.v[i * a.vs + col]) : 0.f;
+    float sum = 0.f;
+#pragma unroll
+    for (int d = 0; d < TD; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = state_tile(d) + 8 * group + r;
+        if (row >= a.dk) // (stays 0 beside an infinite x or decay)
+          continue;
+        S[d][r] = fmaf(to_f32(s.k[i * a.ks + row]), x, decay * S[d][r]);
+        if constexpr (OUT)
+          sum = fmaf(to_f32(s.q[i * a.qs + row]), S[d][r], sum);
+      }
+    if constexpr (OUT) {
+      sum = add_xor32(add_xor16(sum));
+      if (group == 0 && in)
+        s.o[i * a.os + col] = from_f32<T>(sum * a.scale);
+    }
+  }
+}
+
+template <int TD> __device__ __forceinline__ bool any_infinite(const f32x4 (&S)[TD]) {
+  bool inf = false;
+#pragma unroll
+  for (int d = 0; d < TD; ++d)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      inf |= fabsf(S[d][r]) == __builtin_inff();
+  return __any(inf);
+}
+
+constexpr float kLeast = 0x1p-126f; // what exp2 of less than -126 falls short of (it is 0)
+
+// Whether a wave that met outputs (O) or a decay (all) that are not finite takes
+// the chunk by the recurrence.  Not where a NaN among the decays is the cause, or
+// the state that enters alone: these the products carry on as the recurrence
+// does, and a sequence that has met a NaN stays as fast as others.  vf, P, eG: the
+// chunk's V (this wave's columns), scores (which an infinity or NaN in q or k
+// leaves not finite) and decays to each token (NaN behind one).
+template <typename T, int TD>
+__device__ __forceinline__ bool by_recurrence(const f32x4 (&S)[TD], const f32x4 (&O)[4],
+                                              const Frag<T> (&vf)[2], const T *P, const float *eG,
+                                              float all) {
+  const int lane = opaque_lane();
+  const bool grown = all == __builtin_inff();
+  float o = 0.f, s = 0.f, z = zero_sum(vf[0]) + zero_sum(vf[1]);
+  bool gone = all < kLeast;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const float e = eG[16 * t + (lane & 15)]; // (of the token of O[t] and of P's rows)
+    gone |= e < kLeast;
+    if (e == e) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        o = fmaf(O[t][r], 0.f, o);
+#pragma unroll
+      for (int c = 0; c <= t >> 1; ++c)
+        z += zero_sum(get_frag(P + (2 * t + c) * 512, lane));
+    }
+  }
+#pragma unroll
+  for (int d = 0; d < TD; ++d)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      s = fmaf(S[d][r], 0.f, s);
+  if (__any(grown))
+    return true;
+  if (!__any(o != o)) // (behind a NaN)
+    return false;
+  return !__any(s != s) || __any(z != z) || (__any(gone) && any_infinite(S));
+}
+
+// ---- the chunks -------------------------------------------------------------------
+
 // A raw buffer's descriptor over `bytes` bytes at p (wave-uniform), in four
 // scalars.
 __device__ __forceinline__ u32x4 raw_rsrc(const void *p, uint32_t bytes) {
@@ -336,7 +460,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
   __shared__ alignas(16) T Ps[OWN_P ? kDC * kDC : 8];
   __shared__ alignas(16) float Ghi[2][kDC], Glo[2][kDC], wts[2][kDC], eG[2][kDC];
   __shared__ float total[2];
-  __shared__ int first_bad[2][NW];
+  __shared__ int strange[2][NW];
 
   // block b: unit (b / 8 / slices) * 8 + b % 8, slice b / 8 % slices: slices
   // of one unit, which share q and k, are on one die
@@ -451,17 +575,16 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
   Pair G;
   float g_exp, g_wt, g_all;
   double decay_sum = 0.; // of the segment
-  const auto end_decays = [&](int cnt) __attribute__((always_inline)) { // of a chunk of cnt tokens
-    const Pair last = lane_pair(G, cnt - 1);
-    g_wt = lane < cnt ? exp2_of(last + -G) : 0.f;
-    g_all = exp2_of(last);
-  };
-  const auto scan_decays = [&](int cnt) __attribute__((always_inline)) {
+  const auto scan_decays = [&](auto out_tag, int cnt) __attribute__((always_inline)) {
     if (w != kScan)
       return;
     G = prefix_sum(lane < cnt ? log2_decay(gn) : Pair{0.f, 0.f});
+    const Pair last = lane_pair(G, cnt - 1);
     g_exp = exp2_of(G);
-    end_decays(cnt);
+    g_wt = lane < cnt ? exp2_of(last + -G) : 0.f;
+    g_all = grows(gn) ? __builtin_inff() : exp2_of(last);
+    if constexpr (!decltype(out_tag)::value)
+      decay_sum += log2_total(last, gn);
   };
   const auto put_decays = [&](int par) __attribute__((always_inline)) {
     Ghi[par][lane] = G.hi;
@@ -471,12 +594,8 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
     if (lane == 0)
       total[par] = g_all;
   };
-  const auto count_decays = [&](int cnt) __attribute__((always_inline)) {
-    const Pair last = lane_pair(G, cnt - 1);
-    decay_sum += (double)last.hi + (double)last.lo;
-  };
-  // The first token of the staged tile that holds other than finite numbers
-  // in k or v (each wave looks at what it has staged itself).
+  // Whether the staged tile holds other than finite numbers in k or v (each wave
+  // looks at what it has staged itself).
   const auto look = [&](int buf, int par) __attribute__((always_inline)) {
     const auto at = [&](const T *copy, int per_lane, int i) __attribute__((always_inline)) {
       return zero_sum(
@@ -489,51 +608,9 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
 #pragma unroll
     for (int i = 0; i < kNV; ++i)
       z += at(Vs[AHEAD ? buf : 0], kNV, i);
-    int bad = kDC;
-    if (__builtin_expect(__any(z != z), 0)) {
-      int row, c;
-      for (int i = 0; i < kNK; ++i) {
-        piece(RowDK(), kNK, i, row, c);
-        const float x = at(Ks[buf], kNK, i);
-        bad = x != x ? min(bad, row) : bad;
-      }
-      for (int i = 0; i < kNV; ++i) {
-        piece(RowV(), kNV, i, row, c);
-        const float x = at(Vs[AHEAD ? buf : 0], kNV, i);
-        bad = x != x ? min(bad, row) : bad;
-      }
-      for (int b = 1; b < 64; b <<= 1)
-        bad = min(bad, __shfl_xor(bad, b));
-    }
+    const bool met = __any(z != z);
     if (lane == 0)
-      first_bad[par][w] = bad;
-  };
-  // The first token of the tile alone, its products in fp32: the state, and o
-  // from the state after it (this lane's rows, summed over the four lane
-  // groups).
-  const auto one_token = [&](auto out_tag, int buf, int par) __attribute__((always_inline)) {
-    // (rare: opaque, lest its addresses and conditions be kept in registers
-    // through every chunk)
-    const int group = opaque_lane() >> 4;
-    const T *qb = q + (tok0 + pos) * a.qs + (int64_t)(h / a.rq) * a.dk;
-    const float x = to_f32(Vs[AHEAD ? buf : 0][lds_at<T, kCols>(0, my_col)]), all = total[par];
-    float sum = 0.f;
-#pragma unroll
-    for (int d = 0; d < kTD; ++d)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = state_tile(d) + 8 * group + r;
-        if (row >= a.dk) // (stays 0 beside an infinite x)
-          continue;
-        S[d][r] = fmaf(to_f32(Ks[buf][lds_at<T, DK>(0, row)]), x, all * S[d][r]);
-        if (decltype(out_tag)::value)
-          sum = fmaf(to_f32(qb[row]), S[d][r], sum);
-      }
-    if constexpr (decltype(out_tag)::value) {
-      sum = add_xor32(add_xor16(sum));
-      if (lg == 0 && my_col < cols)
-        o[(tok0 + pos) * a.os + (int64_t)h * a.dv + col0 + my_col] = from_f32<T>(sum * a.scale);
-    }
+      strange[par][w] = met;
   };
 
   // this lane's places in the LDS matrices: rows of fragments, and transposed
@@ -553,16 +630,15 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
     int cnt = min(kDC, end - pos), buf = 0, par = 0;
     if (cnt <= 0)
       return;
-    const auto first_loads = [&]() __attribute__((always_inline)) {
+    {
       const Source s = source(pos);
       if constexpr (AHEAD || TURNS)
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
           stage_one(s, cnt, buf, i);
       load_g(s, cnt);
-      scan_decays(cnt);
-    };
-    first_loads();
+      scan_decays(out_tag, cnt);
+    }
     while (true) {
       if constexpr (!AHEAD && !TURNS) { // (every wave is done with the tile before)
         const Source s = source(pos);
@@ -573,40 +649,19 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
       if (w == kScan)
         put_decays(par);
       wait_vmem_all(); // this wave's pieces are in LDS
-      look(buf, par);
+      if constexpr (!OUT)
+        look(buf, par);
       lds_barrier();
-      int bad = first_bad[par][0];
+      const float all = total[par];
+      bool one_by_one = false; // this wave's columns of the chunk by the recurrence
+      if constexpr (!OUT) {
+        int met = 0;
 #pragma unroll
-      for (int i = 1; i < NW; ++i)
-        bad = min(bad, first_bad[par][i]);
-      bad = __builtin_amdgcn_readfirstlane(bad);
-      if (__builtin_expect(bad < cnt, 0)) {
-        cnt = max(1, bad);
-        lds_barrier();
-        if (w == kScan) {
-          end_decays(cnt);
-          put_decays(par);
-          count_decays(cnt);
-        }
-        if (bad > 0) { // the tokens in front of it
-          for (int i = tid; i < (kDC - cnt) * DK; i += 64 * NW)
-            Ks[buf][cnt * DK + i] = from_f32<T>(0.f);
-          for (int i = tid; i < (kDC - cnt) * kCols; i += 64 * NW)
-            Vs[AHEAD ? buf : 0][cnt * kCols + i] = from_f32<T>(0.f);
-        }
-        lds_barrier();
-        if (bad == 0) { // itself, by the recurrence
-          one_token(out_tag, buf, par);
-          if (++pos == end)
-            break;
-          cnt = min(kDC, end - pos);
-          lds_barrier();
-          first_loads();
-          par ^= 1;
-          continue;
-        }
-      } else if (w == kScan) {
-        count_decays(cnt);
+        for (int i = 0; i < NW; ++i)
+          met |= strange[par][i];
+        one_by_one = __any(met != 0 || all == __builtin_inff());
+        if (__any(all < kLeast))
+          one_by_one |= any_infinite(S);
       }
       // The next chunk's loads, one here and one there: all at once, they wait
       // for each other.
@@ -727,13 +782,26 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
         T *ob = o + (tok0 + pos) * a.os + (int64_t)h * a.dv + col0;
         const auto ro =
             buffer_rsrc(ob, (uint32_t)(((cnt - 1) * os + cols) * kEs));
+        float z = all * 0.f; // NaN where an output, or the decay, is not finite
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const int i = 16 * t + lr;
-          O[t] *= eG[par][i];
+          O[t] *= eG[par][16 * t + lr];
 #pragma unroll
           for (int c = 0; c <= t >> 1; ++c)
             mma(O[t], vf[c], get_frag(Pb + (2 * t + c) * 512, lane));
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            z = fmaf(O[t][r], 0.f, z);
+        if (__builtin_expect(__any(z != z), 0))
+          one_by_one = by_recurrence(S, O, vf, Pb, eG[par], all);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          if (__builtin_expect(one_by_one, 0))
+            continue; // (by_token writes them)
+          const int i = 16 * t + lr;
           O[t] *= a.scale;
           const int c = 16 * w + 4 * lg;
           if constexpr (FAST) {
@@ -762,38 +830,48 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
 
       // The state's update, four row tiles at a time, each four's operands
       // read while the ones before are multiplied.
-      const float all = total[par];
+      constexpr int kFirst = OUT ? 8 : 0, kHere = kSteps - kFirst; // requests left
+      if (__builtin_expect(one_by_one, 0)) {
 #pragma unroll
-      for (int d = 0; d < kTD; ++d)
-        S[d] *= all;
-      constexpr int kBatch = kTD / 4;
-      Frag<T> kf[2][4];
-      const auto read_k = [&](int b) __attribute__((always_inline)) {
+        for (int y = kFirst; y < kSteps; ++y)
+          request(y);
+        const Source t = source(pos);
+        by_token<OUT>(S, a,
+                      Tokens<T>{t.q, t.k, t.v, t.g,
+                                o + (tok0 + pos) * a.os + (int64_t)h * a.dv + col0},
+                      cnt, my_col, my_col < cols);
+      } else {
 #pragma unroll
-        for (int d = 0; d < 4; ++d)
-          kf[b & 1][d] = tr_frag(Kb + 32 * (b / kBatch) * DK, DK, k_tr,
-                                 state_tile(b % kBatch * 4 + d));
-      };
-      read_k(0);
+        for (int d = 0; d < kTD; ++d)
+          S[d] *= all;
+        constexpr int kBatch = kTD / 4;
+        Frag<T> kf[2][4];
+        const auto read_k = [&](int b) __attribute__((always_inline)) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const f32x4 w0 = *reinterpret_cast<const f32x4 *>(wts[par] + 32 * x + 4 * lg);
-        const f32x4 w1 = *reinterpret_cast<const f32x4 *>(wts[par] + 32 * x + 16 + 4 * lg);
-        const auto vw = weigh(vf[x], w0, w1);
+          for (int d = 0; d < 4; ++d)
+            kf[b & 1][d] = tr_frag(Kb + 32 * (b / kBatch) * DK, DK, k_tr,
+                                   state_tile(b % kBatch * 4 + d));
+        };
+        read_k(0);
 #pragma unroll
-        for (int b = x * kBatch; b < (x + 1) * kBatch; ++b) {
-          reads_stay();
-          if (b + 1 < 2 * kBatch)
-            read_k(b + 1);
-          constexpr int kFirst = OUT ? 8 : 0, kHere = kSteps - kFirst;
+        for (int x = 0; x < 2; ++x) {
+          const f32x4 w0 = *reinterpret_cast<const f32x4 *>(wts[par] + 32 * x + 4 * lg);
+          const f32x4 w1 = *reinterpret_cast<const f32x4 *>(wts[par] + 32 * x + 16 + 4 * lg);
+          const auto vw = weigh(vf[x], w0, w1);
 #pragma unroll
-          for (int y = b * kHere / (2 * kBatch); y < (b + 1) * kHere / (2 * kBatch); ++y)
-            request(kFirst + y);
+          for (int b = x * kBatch; b < (x + 1) * kBatch; ++b) {
+            reads_stay();
+            if (b + 1 < 2 * kBatch)
+              read_k(b + 1);
 #pragma unroll
-          for (const auto &p : vw.part)
+            for (int y = b * kHere / (2 * kBatch); y < (b + 1) * kHere / (2 * kBatch); ++y)
+              request(kFirst + y);
 #pragma unroll
-            for (int d = 0; d < 4; ++d)
-              mma(S[b % kBatch * 4 + d], kf[b & 1][d], p);
+            for (const auto &p : vw.part)
+#pragma unroll
+              for (int d = 0; d < 4; ++d)
+                mma(S[b % kBatch * 4 + d], kf[b & 1][d], p);
+          }
         }
       }
       if (next_cnt <= 0)
@@ -801,7 +879,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
       pos = next;
       cnt = next_cnt;
       par ^= 1;
-      scan_decays(cnt);
+      scan_decays(out_tag, cnt);
       if constexpr (AHEAD || TURNS)
         buf ^= 1;
       else
@@ -859,7 +937,6 @@ __global__ __launch_bounds__(768, 3) void decay_stream_kernel(SeqTable tab, Deca
   __shared__ alignas(16) T Ps[2][kDC * kDC];
   __shared__ alignas(16) float Ghi[3][kDC], Glo[3][kDC], wts[3][kDC], eG[3][kDC];
   __shared__ float total[3];
-  __shared__ alignas(16) int strange[2][NS];
 
   const int64_t unit = (int64_t)(blockIdx.x / (8 * a.slices)) * 8 + blockIdx.x % 8;
   if (unit >= a.units)
@@ -885,15 +962,6 @@ __global__ __launch_bounds__(768, 3) void decay_stream_kernel(SeqTable tab, Deca
   T *o0 = o + tok0 * a.os + (int64_t)h * a.dv + col0;
   const int frag0 = lds_at<T, DK>(lr, 8 * lg);
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  // whether a wave met other than finite numbers in k or v of chunk `par`
-  const auto any_strange = [&](int par) __attribute__((always_inline)) {
-    int any = 0;
-#pragma unroll
-    for (int i = 0; i < NS; ++i)
-      any |= strange[par][i];
-    return __builtin_amdgcn_readfirstlane(any) != 0;
-  };
-
   if (wave >= NW) {
     // ---- scores ----
     const auto stage = [&](auto ld, T *copy, const T *from, int stride, int width, int cnt,
@@ -930,39 +998,18 @@ __global__ __launch_bounds__(768, 3) void decay_stream_kernel(SeqTable tab, Deca
       const int cnt = max(1, min(kDC, end - at));
       const Pair G = prefix_sum(lane < cnt ? log2_decay(gn) : Pair{0.f, 0.f});
       const Pair last = lane_pair(G, cnt - 1);
+      const bool up = grows(gn);
       Ghi[copy][lane] = G.hi;
       Glo[copy][lane] = G.lo;
       eG[copy][lane] = exp2_of(G);
       wts[copy][lane] = lane < cnt ? exp2_of(last + -G) : 0.f;
       if (lane == 0)
-        total[copy] = exp2_of(last);
+        total[copy] = up ? __builtin_inff() : exp2_of(last);
     };
-    // the chunk's k and v looked at, and its scores as operands: unit u is
-    // tokens 16 t .. of q against tokens 32 c .. of k, (t, c) = (u, 0), and
-    // (2, 1), (3, 1) for u = 4, 5; the others are above the diagonal
+    // a chunk's scores as operands: unit u is tokens 16 t .. of q against tokens
+    // 32 c .. of k, (t, c) = (u, 0), and (2, 1), (3, 1) for u = 4, 5; the others
+    // are above the diagonal
     const auto scores = [&](int par, int copy) __attribute__((always_inline)) {
-      // (the last wave, which has the decays to sum, leaves its share to the
-      // one before)
-      float z = 0.f;
-      const auto check = [&](int share) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < kNK; ++i)
-          z += zero_sum(
-              *reinterpret_cast<const u32x4 *>(&Ks[copy][((share * kNK + i) * 64 + lane) * kP]),
-              T());
-#pragma unroll
-        for (int i = 0; i < kNV; ++i)
-          z += zero_sum(
-              *reinterpret_cast<const u32x4 *>(&Vs[copy][((share * kNV + i) * 64 + lane) * kP]),
-              T());
-      };
-      if (w != NS - 1)
-        check(w);
-      if (w == NS - 2)
-        check(NS - 1);
-      const bool met = __any(z != z);
-      if (lane == 0)
-        strange[par][w] = met;
       const float *gh = Ghi[copy], *gl = Glo[copy];
       const auto one = [&](int t, int c) __attribute__((always_inline)) {
         f32x4 P[2] = {zero, zero};
@@ -991,39 +1038,31 @@ __global__ __launch_bounds__(768, 3) void decay_stream_kernel(SeqTable tab, Deca
       if (w < 6)
         one(w < 4 ? w : w - 2, w >> 2);
     };
-    while (pos < end) {
-      request(pos, 0);
-      request(pos + kDC, 1);
-      const float ga = load_g(pos), gb = load_g(pos + kDC);
-      float gn = load_g(pos + 2 * kDC);
-      decays(ga, pos, 0);
-      decays(gb, pos + kDC, 1);
-      wait_vmem_all(); // this wave's pieces are in LDS
+    if (end == 0)
+      return;
+    request(pos, 0);
+    request(pos + kDC, 1);
+    const float ga = load_g(pos), gb = load_g(pos + kDC);
+    float gn = load_g(pos + 2 * kDC);
+    decays(ga, pos, 0);
+    decays(gb, pos + kDC, 1);
+    wait_vmem_all(); // this wave's pieces are in LDS
+    lds_barrier();
+    scores(0, 0);
+    lds_barrier();
+    // copies of the chunks at hand, after it, and after that
+    for (int par = 0, c1 = 1, c2 = 2; pos < end; par ^= 1) {
+      const float gc = gn; // (the next one's request early: it is waited for below)
+      gn = load_g(pos + 3 * kDC);
+      request(pos + 2 * kDC, c2);
+      if (pos + kDC < end)
+        scores(par ^ 1, c1);
+      decays(gc, pos + 2 * kDC, c2);
+      pos += kDC;
+      c1 = c2;
+      c2 = c2 == 2 ? 0 : c2 + 1;
+      wait_vmem_all();
       lds_barrier();
-      scores(0, 0);
-      lds_barrier();
-      bool met = false;
-      // copies of the chunks at hand, after it, and after that
-      for (int par = 0, c1 = 1, c2 = 2; pos < end; par ^= 1) {
-        met = any_strange(par);
-        if (__builtin_expect(met, 0))
-          break;
-        const float gc = gn; // (the next one's request early: it is waited for below)
-        gn = load_g(pos + 3 * kDC);
-        request(pos + 2 * kDC, c2);
-        if (pos + kDC < end)
-          scores(par ^ 1, c1);
-        decays(gc, pos + 2 * kDC, c2);
-        pos += kDC;
-        c1 = c2;
-        c2 = c2 == 2 ? 0 : c2 + 1;
-        wait_vmem_all();
-        lds_barrier();
-      }
-      if (met) { // (the chunk goes by the recurrence, and all begins again)
-        pos += kDC;
-        lds_barrier();
-      }
     }
     return;
   }
@@ -1046,90 +1085,72 @@ __global__ __launch_bounds__(768, 3) void decay_stream_kernel(SeqTable tab, Deca
   int k_tr[1], v_tr[1];
   k_tr[0] = lds_at<T, DK>(4 * lg + (lr >> 2), state_row(4 * (lr & 3)));
   v_tr[0] = lds_at<T, kCols>(4 * lg + (lr >> 2), 16 * w + 4 * (lr & 3));
-  // Tokens one by one, by the recurrence and straight from memory: the state,
-  // and o from the state after a token (this lane's rows, summed over the four
-  // lane groups).
-  const auto by_token = [&](int count) __attribute__((always_inline)) {
-#pragma unroll 1
-    for (int i = 0; i < count; ++i) {
-      const int64_t at = pos + i;
-      // (rare: opaque, lest its conditions be kept in registers all along)
-      const int group = opaque_lane() >> 4;
-      const float decay = exp2_of(log2_decay(g0[at * gs]));
-      const float x = my_col < cols ? to_f32(v0[at * vs + my_col]) : 0.f;
-      float sum = 0.f;
-#pragma unroll
-      for (int d = 0; d < kTD; ++d)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = state_tile(d) + 8 * group + r;
-          if (row >= a.dk) // (stays 0 beside an infinite x)
-            continue;
-          S[d][r] = fmaf(to_f32(k0[at * ks + row]), x, decay * S[d][r]);
-          sum = fmaf(to_f32(q0[at * qs + row]), S[d][r], sum);
-        }
-      sum = add_xor32(add_xor16(sum));
-      if (lg == 0 && my_col < cols)
-        o0[at * os + my_col] = static_cast<T>(sum * a.scale);
-    }
-  };
-  while (pos < end) {
+  if (end > 0) { // (as the score waves)
     lds_barrier();
     lds_barrier();
-    bool met = false;
-    for (int par = 0, c0 = 0; pos < end; par ^= 1) {
-      met = any_strange(par);
-      if (__builtin_expect(met, 0))
-        break;
-      const T *Qb = Qs[c0], *Kb = Ks[c0], *Vb = Vs[c0];
-      Frag<T> vf[2]; // this wave's columns of V, tokens 0 .. 31 and 32 .. 63
+  }
+  for (int par = 0, c0 = 0; pos < end; par ^= 1) {
+    const T *Qb = Qs[c0], *Kb = Ks[c0], *Vb = Vs[c0];
+    Frag<T> vf[2]; // this wave's columns of V, tokens 0 .. 31 and 32 .. 63
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        vf[c] = tr_frag(Vb + 32 * c * kCols, kCols, v_tr, 0);
-      const float all = total[c0];
-      // o^T of this wave's columns: tile t, element r is column 4 lg + r
-      // of token 16 t + lr
-      f32x4 O[4] = {zero, zero, zero, zero};
-      Frag<T> f[2][4];
-      const auto read_q = [&](int x) __attribute__((always_inline)) {
+    for (int c = 0; c < 2; ++c)
+      vf[c] = tr_frag(Vb + 32 * c * kCols, kCols, v_tr, 0);
+    const float all = total[c0];
+    // o^T of this wave's columns: tile t, element r is column 4 lg + r
+    // of token 16 t + lr
+    f32x4 O[4] = {zero, zero, zero, zero};
+    Frag<T> f[2][4];
+    const auto read_q = [&](int x) __attribute__((always_inline)) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-          f[x & 1][t] = lds_frag(Qb + 16 * t * DK, frag0 ^ 32 * x);
-      };
-      Frag<T> pf[4][2];
-      float ei[4];
-      const auto read_p = [&]() __attribute__((always_inline)) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          ei[t] = eG[c0][16 * t + lr];
-#pragma unroll
-          for (int c = 0; c <= t >> 1; ++c)
-            pf[t][c] = get_frag(&Ps[par][(2 * t + c) * 512], lane);
-        }
-      };
-      read_q(0);
-#pragma unroll
-      for (int x = 0; x < kGQ; ++x) {
-        reads_stay();
-        if (x + 1 < kGQ)
-          read_q(x + 1);
-        else
-          read_p();
-        const Frag<T> sf = pack_acc2(S[2 * x], S[2 * x + 1]);
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          mma(O[t], sf, f[x & 1][t]);
-      }
-      reads_stay();
-      const auto ro = buffer_rsrc(o0 + (int64_t)pos * os,
-                                  (uint32_t)(((min(kDC, end - pos) - 1) * os + cols) * kEs));
+      for (int t = 0; t < 4; ++t)
+        f[x & 1][t] = lds_frag(Qb + 16 * t * DK, frag0 ^ 32 * x);
+    };
+    Frag<T> pf[4][2];
+    float ei[4];
+    const auto read_p = [&]() __attribute__((always_inline)) {
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        O[t] *= ei[t];
+        ei[t] = eG[c0][16 * t + lr];
 #pragma unroll
         for (int c = 0; c <= t >> 1; ++c)
-          mma(O[t], vf[c], pf[t][c]);
+          pf[t][c] = get_frag(&Ps[par][(2 * t + c) * 512], lane);
       }
+    };
+    read_q(0);
+#pragma unroll
+    for (int x = 0; x < kGQ; ++x) {
+      reads_stay();
+      if (x + 1 < kGQ)
+        read_q(x + 1);
+      else
+        read_p();
+      const Frag<T> sf = pack_acc2(S[2 * x], S[2 * x + 1]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        mma(O[t], sf, f[x & 1][t]);
+    }
+    reads_stay();
+    const auto ro = buffer_rsrc(o0 + (int64_t)pos * os,
+                                (uint32_t)(((min(kDC, end - pos) - 1) * os + cols) * kEs));
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      O[t] *= ei[t];
+#pragma unroll
+      for (int c = 0; c <= t >> 1; ++c)
+        mma(O[t], vf[c], pf[t][c]);
+    }
+    float z = all * 0.f; // NaN where an output, or the decay, is not finite
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        z = fmaf(O[t][r], 0.f, z);
+    if (__builtin_expect(__any(z != z), 0) && by_recurrence(S, O, vf, Ps[par], eG[c0], all)) {
+      by_token<true>(S, a,
+                     Tokens<T>{q0 + pos * a.qs, k0 + pos * a.ks, v0 + pos * a.vs, g0 + pos * a.gs,
+                               o0 + pos * a.os},
+                     min(kDC, end - pos), my_col, my_col < cols);
+    } else {
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const int i = 16 * t + lr;
@@ -1174,15 +1195,10 @@ __global__ __launch_bounds__(768, 3) void decay_stream_kernel(SeqTable tab, Deca
               mma(S[b % kBatch * 4 + d], kf[b & 1][d], p);
         }
       }
-      pos += kDC;
-      c0 = c0 == 2 ? 0 : c0 + 1;
-      lds_barrier();
     }
-    if (met) {
-      by_token(min(kDC, end - pos));
-      pos += kDC;
-      lds_barrier();
-    }
+    pos += kDC;
+    c0 = c0 == 2 ? 0 : c0 + 1;
+    lds_barrier();
   }
 
   if (a.fin && kept && my_col < cols) {
@@ -1212,9 +1228,19 @@ __global__ __launch_bounds__(256) void decay_fold_kernel(SeqTable tab, DecayArgs
   f32x4 S = *p;
   for (int64_t i = pair0 + 1; i < last; ++i) {
     p += step;
-    const double x = a.pair_decay[i * a.H + h];
-    const float hi = (float)x;
-    S = *p + exp2_of(Pair{hi, (float)(x - (double)hi)}) * S;
+    // 2^(e - ceil(e)), in (1/2, 1], times S, then the whole powers of 2: a state
+    // that is 0 or infinite stays so whatever the size of e.
+    const double e = a.pair_decay[i * a.H + h], whole = ceil(e);
+    const f32x4 in = *p;
+    if (e - e == 0.) {
+      const float part = __builtin_amdgcn_exp2f((float)(e - whole));
+      const int n = (int)fmin(fmax(whole, -1e6), 1e6);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        S[r] = ldexpf(part * S[r], n) + in[r];
+    } else { // a token's decay of 0 or infinity, or a NaN
+      S = in + (e < 0. ? 0.f : (float)e) * S;
+    }
     *p = S;
   }
 }
