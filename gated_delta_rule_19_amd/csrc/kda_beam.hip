@@ -40,9 +40,9 @@ template <typename T> constexpr int kPart = kPartBytes / (int)sizeof(T);
 
 struct BeamArgs {
   int32_t B, W, V, K, eos, order;
-  int32_t parts, groups_log2; // lane groups whose maxima set the threshold
-  int32_t lanes_log2;         // lanes that join a beam's parts
-  double inv_of_beam;         // 1 / (parts K)
+  int32_t parts;
+  int32_t lanes_log2;           // lanes that join a beam's parts
+  double inv_parts, inv_places; // 1 / parts, 1 / (W parts)
   int64_t row_stride;
 };
 
@@ -124,11 +124,24 @@ __device__ __forceinline__ float wave_max(float x) {
   x = dpp_max<0x143, 0xc>(x);
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
 }
-__device__ __forceinline__ double lane_f64(double x, int lane) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, x);
-  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
-  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+// The K-th largest of 256 numbers, four a lane, bit by bit from the top, or with
+// `parts` any number that parts the K largest from the others.
+__device__ __forceinline__ uint32_t kth_of_256(const uint32_t (&of)[4], int K, int bits,
+                                               bool &parts) {
+  uint32_t low = 0;
+  parts = false;
+  for (int bit = bits - 1; bit >= 0 && !parts; --bit) {
+    const uint32_t at = low | 1u << bit;
+    int reach = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      reach += __popcll(__ballot(of[i] >= at));
+    if (reach >= K) {
+      low = at;
+      parts = reach == K;
+    }
+  }
+  return low;
 }
 
 // exp(d) for d <= 0 (0 from -104 down, -inf too; NaN for NaN): exp2 of the
@@ -198,24 +211,12 @@ __global__ __launch_bounds__(256) void beam_part_kernel(BeamArgs a, const T *__r
   const float top = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
 
   if (wv == 0) {
-    // The K-th largest of the lanes' maxima, bit by bit, or any number that
-    // parts the K largest from the others.
-    uint32_t of[4], low = 0;
-    bool parts = false;
+    uint32_t of[4];
+    bool parts;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       of[i] = Order::make(lane_max[i * 64 + lane]);
-    for (int bit = Order::kBits - 1; bit >= 0 && !parts; --bit) {
-      const uint32_t at = low | 1u << bit;
-      int reach = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        reach += __popcll(__ballot(of[i] >= at));
-      if (reach >= a.K) {
-        low = at;
-        parts = reach == a.K;
-      }
-    }
+    const uint32_t low = kth_of_256(of, a.K, Order::kBits, parts);
     if (lane == 0) {
       // (the next number above infinity is a NaN: nothing reaches it)
       bar_at = Order::value(parts ? low : low + 1);
@@ -322,6 +323,7 @@ __global__ __launch_bounds__(256) void beam_part_kernel(BeamArgs a, const T *__r
 
 constexpr int kMergeCap = 1024;
 constexpr int kHeld = 4; // candidates a lane holds at a time
+constexpr int kTurn = 79; // lanes that a block of 256 candidates is turned by
 
 // A valued candidate.  Before another one: the larger value, then the lower
 // beam, then (where 64 bits do not tell a beam's values apart) the larger
@@ -337,27 +339,20 @@ __device__ __forceinline__ bool before(const Valued &p, const Valued &q) {
          ((p.val == q.val) & ((p.w < q.w) | ((p.w == q.w) & tail)));
 }
 
-// The K-th largest of the maxima of 2^groups_log2 >= K lane groups: at least K
-// elements of the wave reach it, or it is -inf.
-__device__ __forceinline__ double kth_of_groups(double m, int K, int groups_log2) {
-  const int lane = threadIdx.x & 63, width = 64 >> groups_log2;
-  for (int b = 1; b < width; b <<= 1) {
-    const double o = __shfl_xor(m, b);
-    m = o > m ? o : m;
-  }
-  int above = 0;
-  for (int g = 0; g < (1 << groups_log2); ++g) {
-    const double o = lane_f64(m, g * width);
-    above += o > m || (o == m && g * width < (lane & -width));
-  }
-  return lane_f64(m, __builtin_ctzll(__ballot(above == K - 1)));
-}
-
 // A chain of latencies, a workgroup a batch: 10 us for 64 batches of 8 beams in
 // 16 parts, 5 us for one of 4 beams in 8; so the candidates are asked for
 // before the sums, a beam's parts are joined by as many lanes, and the ranks
 // are counted by all four waves without branches (one lane each, with
 // branches: 22 us).
+//
+// What is ranked is what reaches the K-th largest of the 256 lanes' own maxima:
+// some 1.2 K candidates if each lane's are a fair draw of all.  So a lane takes
+// them across beams, parts and ranks alike: rank by rank, each block of 256 turned
+// against the one before, lest a lane meet one part's at all ranks (W and parts
+// are often powers of two).  Taken as they lie, with the ranks of a part side by
+// side, a K of 16 or more that divides 256 let thousands through: 64 beams of
+// 128001, K = 64: 4280 us, now 135; 16 of 200000 in fp32, K = 32: 320 to 900, now
+// 64.
 __global__ __launch_bounds__(256) void beam_merge_kernel(
     BeamArgs a, const Cand *__restrict__ cand, const PartSum *__restrict__ sums,
     const float *__restrict__ scores, const uint8_t *__restrict__ finished,
@@ -366,7 +361,7 @@ __global__ __launch_bounds__(256) void beam_merge_kernel(
   __shared__ double lse[KDA_BEAM_MAX], base[KDA_BEAM_MAX]; // base NaN: beam without value
   __shared__ bool done[KDA_BEAM_MAX];
   __shared__ double open_base[KDA_BEAM_MAX]; // base, NaN for a finished beam too
-  __shared__ double wave_kth[4];
+  __shared__ uint32_t lane_key[256];
   __shared__ int rank[kMergeCap];
   __shared__ Valued buf[kMergeCap];
   __shared__ Valued sel[KDA_BEAM_MAX];
@@ -379,18 +374,23 @@ __global__ __launch_bounds__(256) void beam_merge_kernel(
   const PartSum *ps = sums + (int64_t)b * W * P;
   const Cand *cs = cand + (int64_t)b * W * P * K;
 
-  // Candidate i: the (i % K)-th of part i / K % P of beam i / (P K).  The first
-  // ones are asked for before all else, so that their way from memory and the
-  // sums' is one.
-  const int of_beam = P * K, all = W * of_beam;
+  // Candidate i: of place i % (W P), that is beam and part, the i / (W P)-th.  The
+  // first ones are asked for before all else, so that their way from memory and
+  // the sums' is one.  (Quotients: the double is off by less than half of what
+  // parts i + 1/2 from a multiple.)
+  const int places = W * P, all = places * K;
+  const auto index = [&](int block) { return block * 256 + ((tid + kTurn * block) & 255); };
+  Cand held[kHeld];
+  int place[kHeld];
   const auto load = [&](Cand(&c)[kHeld], int i0) {
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
-      const int i = i0 + j * 256 + tid;
-      c[j] = i < all ? cs[i] : Cand{0.f, -1};
+      const int i = index(i0 / 256 + j);
+      const int r = (int)(((double)i + 0.5) * a.inv_places);
+      place[j] = i - r * places;
+      c[j] = i < all ? cs[place[j] * K + r] : Cand{0.f, -1};
     }
   };
-  Cand held[kHeld];
   load(held, 0);
 
   // lse: 2^lanes_log2 lanes a beam
@@ -437,18 +437,16 @@ __global__ __launch_bounds__(256) void beam_merge_kernel(
   // What the held candidates are worth, NaN if nothing.
   double worth[kHeld];
   int beam[kHeld];
-  const auto rate = [&](int i0) {
+  const auto rate = [&]() {
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
-      // (i / of_beam: the double is off by less than half of what parts
-      // i + 1/2 from a multiple)
-      beam[j] = held[j].v >= 0 ? (int)(((double)(i0 + j * 256 + tid) + 0.5) * a.inv_of_beam) : 0;
+      beam[j] = held[j].v >= 0 ? (int)(((double)place[j] + 0.5) * a.inv_parts) : 0;
       const double v = open_base[beam[j]] + ((double)held[j].x - lse[beam[j]]);
       worth[j] = held[j].v >= 0 ? v : __builtin_nan("");
     }
   };
   // goes over the candidates that have a value
-  rate(0);
+  rate();
   const auto for_all = [&](auto &&f) {
     for (int i0 = 0;;) {
 #pragma unroll
@@ -461,18 +459,28 @@ __global__ __launch_bounds__(256) void beam_merge_kernel(
       const bool more = i0 < all;
       i0 = more ? i0 : 0;
       load(held, i0);
-      rate(i0);
+      rate();
       if (!more)
         break;
     }
   };
   double best = -inf;
   for_all([&](const Valued &v) { best = fmax(best, v.val); });
-  const double kth = kth_of_groups(best, K, a.groups_log2);
-  if (lane == 0)
-    wave_kth[wv] = kth;
-  __syncthreads();
-  const double bar = fmax(fmax(wave_kth[0], wave_kth[1]), fmax(wave_kth[2], wave_kth[3]));
+  double bar;
+  {
+    // (in fp32, rounded down: a lane's best still reaches it)
+    typedef OrderOf<float> Order;
+    const float near = (float)best;
+    lane_key[tid] = Order::make(near) - ((double)near > best);
+    __syncthreads();
+    uint32_t of[4];
+    bool parts;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      of[i] = lane_key[i * 64 + lane];
+    const uint32_t low = kth_of_256(of, K, Order::kBits, parts);
+    bar = low > Order::make(-__builtin_inff()) ? (double)Order::value(low) : -inf;
+  }
   const auto push = [&](const Valued &v) {
     const int at = atomicAdd(&count, 1);
     if (at < kMergeCap)
@@ -706,13 +714,10 @@ hipError_t launch_beam_select(int elt, const BeamCall &c, void *ws, hipStream_t 
   a.order = c.order;
   a.row_stride = c.row_stride;
   a.parts = elt == 1 ? part_count<bf16>(c.V) : part_count<float>(c.V);
-  // twice K groups of lanes: their K-th maximum lets through some K elements a
-  // wave
-  while ((1 << a.groups_log2) < 2 * c.K && a.groups_log2 < 6)
-    ++a.groups_log2;
   while ((1 << a.lanes_log2) < a.parts && a.lanes_log2 < 6)
     ++a.lanes_log2;
-  a.inv_of_beam = 1. / ((double)a.parts * c.K);
+  a.inv_parts = 1. / (double)a.parts;
+  a.inv_places = 1. / ((double)c.W * a.parts);
   const int64_t n = (int64_t)c.B * c.W * a.parts;
   if (n * 256 > UINT32_MAX)
     return hipErrorInvalidConfiguration;
