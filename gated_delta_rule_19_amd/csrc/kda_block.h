@@ -27,11 +27,14 @@ struct DecayPlan {
   int64_t seg;
   int64_t pairs; // transition pairs of all cut sequences
   int waves;     // of a workgroup, 16 value columns each
-  bool streams;  // where rows are aligned: a workgroup for each chain, none cut
+  bool streams;  // a workgroup for each chain, none cut
   size_t off_state, off_decay, total; // workspace layout (the table first)
 };
+// `even`: whether all rows start at multiples of 16 bytes, as decay_even has it
+// of a call; what its workspace has to hold is more with the one or the other.
 DecayPlan decay_plan(int elt, int32_t num_seqs, const int64_t *cu, int32_t H, int32_t dk,
-                     int32_t dv, int32_t split_hint);
+                     int32_t dv, int32_t split_hint, bool even);
+bool decay_even(int elt, const kda_decay_io &io);
 
 hipError_t launch_decay(int elt, const DecayCall &c, int32_t num_seqs, const int64_t *cu,
                         const DecayPlan &plan, void *ws, hipStream_t s);

@@ -6,6 +6,8 @@
 #include "kda_block.h"
 #include "kda_checks.h"
 
+#include <algorithm>
+
 using namespace kda;
 
 static_assert(sizeof(kda_decay_io) == 104, "kda_decay_io layout");
@@ -78,7 +80,11 @@ size_t kda_decay_attention_workspace_size(int32_t num_seqs, const int64_t *cu_se
   if (!good_cu(num_seqs, cu_seqlens_host) || check_decay(H, dk, dv, dt) != KDA_OK ||
       split_hint < 0)
     return 0;
-  return decay_plan(elt_of(dt), num_seqs, cu_seqlens_host, H, dk, dv, split_hint).total;
+  size_t most = 0; // (a call's pointers and strides are not known yet)
+  for (bool even : {false, true})
+    most = std::max(most, decay_plan(elt_of(dt), num_seqs, cu_seqlens_host, H, dk, dv, split_hint,
+                                     even).total);
+  return most;
 }
 
 kda_status kda_decay_attention(int32_t num_seqs, const int64_t *cu_seqlens_host, int32_t H,
@@ -103,8 +109,8 @@ kda_status kda_decay_attention(int32_t num_seqs, const int64_t *cu_seqlens_host,
   if (overlaps_any(r.o, r.in) || overlaps_any(fin, r.in) || overlaps_any(r.o, {init, fin}) ||
       (initial_state != final_state && overlap(init, fin)))
     return KDA_ERR_INVALID_ARG;
-  const DecayPlan plan =
-      decay_plan(elt_of(dt), num_seqs, cu_seqlens_host, H, io->dk, io->dv, split_hint);
+  const DecayPlan plan = decay_plan(elt_of(dt), num_seqs, cu_seqlens_host, H, io->dk, io->dv,
+                                    split_hint, decay_even(elt_of(dt), *io));
   st = check_workspace(plan.total, workspace, workspace_bytes);
   if (st != KDA_OK)
     return st;

@@ -1388,15 +1388,25 @@ int64_t num_segments(int64_t len, int64_t seg) { return len <= seg ? 1 : (len + 
 //   pay at four segments and 256 tokens (32 heads: 1024 tokens in four segments
 //   44 us, uncut 36; 2048 in eight 52, 63; 8192 133, 217; 48 heads and 32768
 //   tokens in five 730, 1020), where the chunk kernel would take a whole
-//   sequence from two and a half on.
+//   sequence from two and a half on.  Rows off 16 bytes have the chunk kernel
+//   alone, and its rule (1024 tokens of 32 heads: uncut 139 us, cut 66).
 // - fp32: 13.1 us a chunk with eight waves and 128 columns, 9.8 with four and
 //   64: four where the longest sequence sets the time (9001 tokens in 37 ragged
 //   sequences, 10 heads of 100: 153 us against 167), eight where the number of
 //   workgroups does (37 sequences of 243: 123 us against 140).
 constexpr int64_t kCUs = 256;
 
+bool decay_even(int elt, const kda_decay_io &io) {
+  const int64_t es = elt == 1 ? 2 : 4;
+  const auto even = [es](const void *p, int64_t stride) {
+    return ((uintptr_t)p & 15u) == 0 && stride * es % 16 == 0;
+  };
+  return io.dk * es % 16 == 0 && io.dv * es % 16 == 0 && even(io.q, io.q_stride) &&
+         even(io.k, io.k_stride) && even(io.v, io.v_stride) && even(io.o, io.o_stride);
+}
+
 DecayPlan decay_plan(int elt, int32_t num_seqs, const int64_t *cu, int32_t H, int32_t dk,
-                     int32_t dv, int32_t split_hint) {
+                     int32_t dv, int32_t split_hint, bool even) {
   DecayPlan p{};
   int64_t longest = 0;
   for (int32_t n = 0; n < num_seqs; ++n)
@@ -1409,8 +1419,7 @@ DecayPlan decay_plan(int elt, int32_t num_seqs, const int64_t *cu, int32_t H, in
   };
   // (heads of more than 128 keys leave no registers, in fp32 no LDS, for eight)
   p.waves = dk > 128 || dv <= 64 ? 4 : 8;
-  p.streams = elt == 1 && dk <= 128 && dk % 8 == 0 && dv % 8 == 0 &&
-              (int64_t)num_seqs * H * slices(4) <= kCUs;
+  p.streams = even && elt == 1 && dk <= 128 && (int64_t)num_seqs * H * slices(4) <= kCUs;
   p.seg = whole(longest);
   if (split_hint > 1) {
     p.seg = whole((longest + split_hint - 1) / split_hint);
@@ -1453,14 +1462,8 @@ DecayPlan decay_plan(int elt, int32_t num_seqs, const int64_t *cu, int32_t H, in
 hipError_t launch_decay(int elt, const DecayCall &c, int32_t num_seqs, const int64_t *cu,
                         const DecayPlan &plan, void *ws, hipStream_t s) {
   DecayArgs a = decay_args(c);
-  const size_t es = elt == 1 ? 2 : 4;
-  const auto even = [es](const void *p, int64_t stride) {
-    return ((uintptr_t)p & 15u) == 0 && stride * es % 16 == 0;
-  };
-  const bool fast = a.dk * es % 16 == 0 && a.dv * es % 16 == 0 && even(c.io.q, a.qs) &&
-                    even(c.io.k, a.ks) && even(c.io.v, a.vs) && even(c.io.o, a.os);
-  const bool streams = plan.streams && fast;
-  const int waves = streams ? 4 : plan.waves;
+  const bool fast = decay_even(elt, c.io);
+  const int waves = plan.streams ? 4 : plan.waves;
   a.slices = (a.dv + 16 * waves - 1) / (16 * waves);
   a.seg = (int32_t)plan.seg;
   a.seg_state = (float *)((uint8_t *)ws + plan.off_state);
@@ -1473,7 +1476,7 @@ hipError_t launch_decay(int elt, const DecayCall &c, int32_t num_seqs, const int
   int64_t total[kCounts];
   if (!seq_totals(num_seqs, cu, tiles, total))
     return hipErrorInvalidConfiguration;
-  const int threads = streams ? 768 : 64 * waves;
+  const int threads = plan.streams ? 768 : 64 * waves;
   int64_t grid[2];
   for (int pass = 0; pass < 2; ++pass) {
     grid[pass] = (total[pass] * a.H + 7) / 8 * 8 * a.slices;
@@ -1488,7 +1491,7 @@ hipError_t launch_decay(int elt, const DecayCall &c, int32_t num_seqs, const int
   const hipError_t e = make_seq_table(tab, num_seqs, cu, tiles, ws, s);
   if (e != hipSuccess)
     return e;
-  if (streams) {
+  if (plan.streams) {
     a.units = total[1] * a.H;
     const auto kernel = a.dk <= 64 ? decay_stream_kernel<64> : decay_stream_kernel<128>;
     kernel<<<(unsigned)grid[1], threads, 0, s>>>(tab, a, (const bf16 *)c.io.q, (const bf16 *)c.io.k,

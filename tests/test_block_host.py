@@ -362,3 +362,12 @@ def test_reorder_form_by_hand():
     assert ref.reorder(state, parents).view(-1).tolist() == [1, 0, 0, 5, 4, 5]
     slots = torch.tensor([[5, 4, 3], [2, 1, 9]], dtype=torch.int32)
     assert ref.reorder(state, parents, slots).view(-1).tolist() == [0, 1, 2, 5, 5, 4]
+
+
+def test_workspace_covers_rows_at_any_place(lib):
+    """A prompt that runs uncut where its rows start at multiples of 16 bytes,
+    and in segments where they do not: what is asked for holds both."""
+    keep, p = cu_ptr(0, 1024)
+    size = lib.kda_decay_attention_workspace_size
+    assert size(1, p, 32, 128, 128, BF16, 0) >= size(1, p, 32, 128, 128, BF16, 3) > 0
+    assert size(1, p, 32, 128, 128, BF16, 1) == 0
