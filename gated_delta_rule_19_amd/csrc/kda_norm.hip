@@ -119,14 +119,16 @@ template <bool BLOCK> __device__ __forceinline__ float row_sum(float v, int lane
   for (int b = 0; b < (BLOCK ? 6 : lanes_log2); ++b)
     v += __shfl_xor(v, 1 << b);
   if constexpr (BLOCK) {
-    __shared__ float part[2][16];
+    __shared__ alignas(16) float part[2][16];
     const int waves = blockDim.x >> 6;
     if ((threadIdx.x & 63) == 0)
       part[at][threadIdx.x >> 6] = v;
+    if (threadIdx.x < 16 && (int)threadIdx.x >= waves)
+      part[at][threadIdx.x] = 0.f;
     lds_barrier();
-    v = 0.f;
-    for (int w = 0; w < waves; ++w)
-      v += part[at][w];
+    const f32x4 *p = reinterpret_cast<const f32x4 *>(part[at]);
+    const f32x4 w = (p[0] + p[1]) + (p[2] + p[3]);
+    v = (w[0] + w[1]) + (w[2] + w[3]);
   }
   return v;
 }

@@ -39,3 +39,19 @@ def test_gates_at_the_ends(dtype):
     torch.cuda.synchronize()
     r = r[0].tolist()
     assert r[:6] == [0, 0, 0, 3, 3, 3] and r[6] != r[6] and r[7] == 1.5
+
+
+def test_small_sums_beside_a_large_one():
+    """A square of 2^24 and fifteen of 1 far from each other: added to the large
+    one by one, each would be lost in its rounding.  Joined first, at most one
+    is: 2^-24 of the mean; and root, division and two products half a step each."""
+    print("norm sums", flush=True)
+    D = 65536
+    x = torch.zeros(2, D)
+    x[:, 0] = 4096.0
+    x[1, [256 * i for i in range(1, 16)]] = 1.0
+    r, y = kda.block_norm(x.to(DEV), torch.ones(D, device=DEV), eps=0.0)
+    torch.cuda.synchronize()
+    want = ref.f64(x) / ref.f64(x).square().mean(-1, keepdim=True).sqrt()
+    ref.check("y", y, want, 5 * U * want.abs())
+    assert y[1, 0] < y[0, 0]
