@@ -26,13 +26,13 @@
 // G is summed and kept as two fp32 numbers, so that differences within a chunk
 // keep their accuracy beside a decay of e^-150.
 //
-// Ends of fp32's range.  Where an infinity or a NaN, growth past fp32, or an
-// infinite state under a decay that underflows over a chunk would meet a 0 in
-// these products (an infinity in k or v would even reach earlier tokens of its
-// chunk), a wave's columns of the chunk go by the recurrence, token by token.
-// All of these show in o: a wave that finds one of its outputs not finite looks
-// for the cause (see by_recurrence), so that other chunks pay an operation a
-// value.  Launches that form only states look at k, v and the decay instead.
+// Ends of fp32's range.  Where an infinity or a NaN in q, k or v, or growth past
+// fp32, would meet a 0 in these products (an infinity in k or v would even reach
+// earlier tokens of its chunk), a wave's columns of the chunk go by the
+// recurrence, token by token.  All of these show in o: a wave that finds one of
+// its outputs not finite looks for the cause (see by_recurrence), so that other
+// chunks pay an operation a value.  Launches that form only states look at k, v
+// and the decay instead.
 #include "kda_block.h"
 #include "kda_device.h"
 
@@ -95,13 +95,31 @@ __device__ __forceinline__ bool grows(float g) {
     up += __shfl_xor(up, b);
   return !(up < 44.f);
 }
-// log2 of a chunk's decay, from the sum over its tokens: -inf where a token's is
-// 0 (fp32's exp is, below -104), which an infinite state does not outlast.
+constexpr float kNone = -104.f; // fp32's exp is 0 below
+
+// What a chunk takes of its decays, from G (log2 of the decay from its start to
+// each token), the last of them, and the tokens' g (0 behind the last; `real`:
+// this lane's is not behind).
+struct ChunkDecay {
+  float to_token, to_end, all;
+};
+__device__ __forceinline__ ChunkDecay chunk_decay(const Pair &G, const Pair &last, float g,
+                                                  bool real) {
+  // A product of decays that underflows is the least number above 0, so that an
+  // infinite state outlasts it, as it does token by token; 0 with a token that
+  // forgets everything.
+  constexpr float kLeast = 0x1p-149f;
+  const auto product = [](float e, bool none) { return e < kLeast ? none ? 0.f : kLeast : e; };
+  const uint64_t none = __ballot(g < kNone), upto = (2ull << (threadIdx.x & 63)) - 1;
+  return {product(exp2_of(G), (none & upto) != 0), real ? exp2_of(last + -G) : 0.f,
+          grows(g) ? __builtin_inff() : product(exp2_of(last), none != 0)};
+}
+// log2 of a chunk's decay, from the sum over its tokens: -inf where one is 0.
 __device__ __forceinline__ double log2_total(const Pair &sum, float g) {
-  constexpr float kNone = -104.f;
   if (__builtin_expect(!__any(!(g >= kNone && g < __builtin_inff())), 1))
     return (double)sum.hi + (double)sum.lo;
-  return (__any(g < kNone) ? -__builtin_inf() : 0.) + (__any(g == __builtin_inff()) ? __builtin_inf() : 0.) +
+  return (__any(g < kNone) ? -__builtin_inf() : 0.) +
+         (__any(g == __builtin_inff()) ? __builtin_inf() : 0.) +
          (__any(g != g) ? __builtin_nan("") : 0.);
 }
 // Sum over lanes 0 .. of a wave up to each (DPP: 1, 2, 4 and 8 lanes within
@@ -287,6 +305,13 @@ __device__ __forceinline__ Whole weigh(const Frag<float> &v, const f32x4 &w0, co
   return {{{v.lo * w0, v.hi * w1}}};
 }
 
+// ... of 0 * x over eight numbers, added to z
+__device__ __forceinline__ float zero_sum(const f32x4 &a, const f32x4 &b, float z) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    z = fmaf(b[r], 0.f, fmaf(a[r], 0.f, z));
+  return z;
+}
 __device__ __forceinline__ float zero_sum(const Frag<bf16> &f) {
   return zero_sum(__builtin_bit_cast(u32x4, f.v), bf16());
 }
@@ -305,7 +330,8 @@ template <typename T> struct Tokens {
 
 // `count` of them by the recurrence, in fp32 and straight from memory: this
 // lane's column `col` of the state (`in`: there is one), and with OUT o from the
-// state after a token (this lane's rows, summed over the four lane groups).
+// state after a token (this lane's rows, summed over the four lane groups).  Some
+// 100 us for a chunk of 64 (heads of 128), against 2 to 4.
 template <bool OUT, typename T, int TD>
 __device__ __forceinline__ void by_token(f32x4 (&S)[TD], const DecayArgs &a, const Tokens<T> &s,
                                          int count, int col, bool in) {
@@ -315,17 +341,27 @@ __device__ __forceinline__ void by_token(f32x4 (&S)[TD], const DecayArgs &a, con
     const int group = opaque_lane() >> 4;
     const float decay = decay_of(s.g[i * a.gs]), x = in ? to_f32(s.v[i * a.vs + col]) : 0.f;
     float sum = 0.f;
+    const auto rk = buffer_rsrc(s.k + i * a.ks, a.dk * (uint32_t)sizeof(T));
+    const auto rq = buffer_rsrc(s.q + i * a.qs, a.dk * (uint32_t)sizeof(T));
 #pragma unroll
-    for (int d = 0; d < TD; ++d)
+    for (int d = 0; d < TD; ++d) { // (rows behind dk read 0)
+      float kr[4], qr[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int row = state_tile(d) + 8 * group + r;
-        if (row >= a.dk) // (stays 0 beside an infinite x or decay)
-          continue;
-        S[d][r] = fmaf(to_f32(s.k[i * a.ks + row]), x, decay * S[d][r]);
+        const int at = (state_tile(d) + 8 * group + r) * (int)sizeof(T);
+        kr[r] = buffer_load1(rk, at, (const T *)nullptr);
         if constexpr (OUT)
-          sum = fmaf(to_f32(s.q[i * a.qs + row]), S[d][r], sum);
+          qr[r] = buffer_load1(rq, at, (const T *)nullptr);
       }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        // (... and stay 0 beside an infinite x or decay)
+        const bool real = state_tile(d) + 8 * group + r < a.dk;
+        S[d][r] = fmaf(kr[r], real ? x : 0.f, (real ? decay : 0.f) * S[d][r]);
+        if constexpr (OUT)
+          sum = fmaf(qr[r], S[d][r], sum);
+      }
+    }
     if constexpr (OUT) {
       sum = add_xor32(add_xor16(sum));
       if (group == 0 && in)
@@ -334,55 +370,16 @@ __device__ __forceinline__ void by_token(f32x4 (&S)[TD], const DecayArgs &a, con
   }
 }
 
-template <int TD> __device__ __forceinline__ bool any_infinite(const f32x4 (&S)[TD]) {
-  bool inf = false;
-#pragma unroll
-  for (int d = 0; d < TD; ++d)
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      inf |= fabsf(S[d][r]) == __builtin_inff();
-  return __any(inf);
-}
-
-constexpr float kLeast = 0x1p-126f; // what exp2 of less than -126 falls short of (it is 0)
-
-// Whether a wave that met outputs (O) or a decay (all) that are not finite takes
-// the chunk by the recurrence.  Not where a NaN among the decays is the cause, or
-// the state that enters alone: these the products carry on as the recurrence
-// does, and a sequence that has met a NaN stays as fast as others.  vf, P, eG: the
-// chunk's V (this wave's columns), scores (which an infinity or NaN in q or k
-// leaves not finite) and decays to each token (NaN behind one).
-template <typename T, int TD>
-__device__ __forceinline__ bool by_recurrence(const f32x4 (&S)[TD], const f32x4 (&O)[4],
-                                              const Frag<T> (&vf)[2], const T *P, const float *eG,
-                                              float all) {
-  const int lane = opaque_lane();
-  const bool grown = all == __builtin_inff();
-  float o = 0.f, s = 0.f, z = zero_sum(vf[0]) + zero_sum(vf[1]);
-  bool gone = all < kLeast;
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const float e = eG[16 * t + (lane & 15)]; // (of the token of O[t] and of P's rows)
-    gone |= e < kLeast;
-    if (e == e) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        o = fmaf(O[t][r], 0.f, o);
-#pragma unroll
-      for (int c = 0; c <= t >> 1; ++c)
-        z += zero_sum(get_frag(P + (2 * t + c) * 512, lane));
-    }
-  }
-#pragma unroll
-  for (int d = 0; d < TD; ++d)
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      s = fmaf(S[d][r], 0.f, s);
-  if (__any(grown))
-    return true;
-  if (!__any(o != o)) // (behind a NaN)
-    return false;
-  return !__any(s != s) || __any(z != z) || (__any(gone) && any_infinite(S));
+// Whether a wave that met outputs (or a decay) that are not finite takes the chunk
+// by the recurrence: where q or k (`met`: a score was not finite), this wave's
+// columns of V (vf), or growth (all is infinite) are the cause.  Not where the
+// state that enters or a NaN among the decays is the cause alone: these the
+// products carry on as the recurrence does, and a sequence that has met a NaN or
+// an infinity stays as fast as others.
+template <typename T>
+__device__ __forceinline__ bool by_recurrence(const Frag<T> (&vf)[2], int met, float all) {
+  const float z = zero_sum(vf[0]) + zero_sum(vf[1]);
+  return __any(z != z || met != 0 || all == __builtin_inff());
 }
 
 // ---- the chunks -------------------------------------------------------------------
@@ -573,26 +570,24 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
   // The scan wave: G = log2 of the decay from the tile's start to each of its
   // tokens, and what the chunk takes of it.
   Pair G;
-  float g_exp, g_wt, g_all;
+  ChunkDecay ends;
   double decay_sum = 0.; // of the segment
   const auto scan_decays = [&](auto out_tag, int cnt) __attribute__((always_inline)) {
     if (w != kScan)
       return;
     G = prefix_sum(lane < cnt ? log2_decay(gn) : Pair{0.f, 0.f});
     const Pair last = lane_pair(G, cnt - 1);
-    g_exp = exp2_of(G);
-    g_wt = lane < cnt ? exp2_of(last + -G) : 0.f;
-    g_all = grows(gn) ? __builtin_inff() : exp2_of(last);
+    ends = chunk_decay(G, last, gn, lane < cnt);
     if constexpr (!decltype(out_tag)::value)
       decay_sum += log2_total(last, gn);
   };
   const auto put_decays = [&](int par) __attribute__((always_inline)) {
     Ghi[par][lane] = G.hi;
     Glo[par][lane] = G.lo;
-    eG[par][lane] = g_exp;
-    wts[par][lane] = g_wt;
+    eG[par][lane] = ends.to_token;
+    wts[par][lane] = ends.to_end;
     if (lane == 0)
-      total[par] = g_all;
+      total[par] = ends.all;
   };
   // Whether the staged tile holds other than finite numbers in k or v (each wave
   // looks at what it has staged itself).
@@ -660,8 +655,6 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
         for (int i = 0; i < NW; ++i)
           met |= strange[par][i];
         one_by_one = __any(met != 0 || all == __builtin_inff());
-        if (__any(all < kLeast))
-          one_by_one |= any_infinite(S);
       }
       // The next chunk's loads, one here and one there: all at once, they wait
       // for each other.
@@ -712,6 +705,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
           return u < 6;
         };
         constexpr int kUnits = NW == 8 ? 1 : 2;
+        float zp = 0.f; // NaN where a score is not finite
 #pragma unroll
         for (int y = 0; y < kUnits; ++y) {
           int t, c;
@@ -725,6 +719,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
                 mma(P[y][g], lds_frag(Kb + (32 * c + 16 * g) * DK, frag0 ^ 32 * x), qf);
             }
           }
+          zp = zero_sum(P[y][0], P[y][1], zp);
         }
         // o^T of this wave's columns from the entering state: tile t, element
         // r is column 4 lg + r of token 16 t + lr
@@ -752,6 +747,9 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
           }
           reads_stay();
         }
+        const bool unlike = __any(zp != zp);
+        if (lane == 0)
+          strange[par][w] = unlike;
         const float *gh = Ghi[par], *gl = Glo[par];
         T *Pb = OWN_P ? Ps : Qs[AHEAD ? buf : 0];
         if constexpr (!OWN_P)
@@ -795,8 +793,13 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
 #pragma unroll
           for (int r = 0; r < 4; ++r)
             z = fmaf(O[t][r], 0.f, z);
-        if (__builtin_expect(__any(z != z), 0))
-          one_by_one = by_recurrence(S, O, vf, Pb, eG[par], all);
+        if (__builtin_expect(__any(z != z), 0)) {
+          int met = 0;
+#pragma unroll
+          for (int i = 0; i < NW; ++i)
+            met |= strange[par][i];
+          one_by_one = by_recurrence(vf, met, all);
+        }
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           if (__builtin_expect(one_by_one, 0))
@@ -937,6 +940,7 @@ __global__ __launch_bounds__(768, 3) void decay_stream_kernel(SeqTable tab, Deca
   __shared__ alignas(16) T Ps[2][kDC * kDC];
   __shared__ alignas(16) float Ghi[3][kDC], Glo[3][kDC], wts[3][kDC], eG[3][kDC];
   __shared__ float total[3];
+  __shared__ int strange[2][8];
 
   const int64_t unit = (int64_t)(blockIdx.x / (8 * a.slices)) * 8 + blockIdx.x % 8;
   if (unit >= a.units)
@@ -998,13 +1002,13 @@ __global__ __launch_bounds__(768, 3) void decay_stream_kernel(SeqTable tab, Deca
       const int cnt = max(1, min(kDC, end - at));
       const Pair G = prefix_sum(lane < cnt ? log2_decay(gn) : Pair{0.f, 0.f});
       const Pair last = lane_pair(G, cnt - 1);
-      const bool up = grows(gn);
+      const ChunkDecay ends = chunk_decay(G, last, gn, lane < cnt);
       Ghi[copy][lane] = G.hi;
       Glo[copy][lane] = G.lo;
-      eG[copy][lane] = exp2_of(G);
-      wts[copy][lane] = lane < cnt ? exp2_of(last + -G) : 0.f;
+      eG[copy][lane] = ends.to_token;
+      wts[copy][lane] = ends.to_end;
       if (lane == 0)
-        total[copy] = up ? __builtin_inff() : exp2_of(last);
+        total[copy] = ends.all;
     };
     // a chunk's scores as operands: unit u is tokens 16 t .. of q against tokens
     // 32 c .. of k, (t, c) = (u, 0), and (2, 1), (3, 1) for u = 4, 5; the others
@@ -1020,6 +1024,10 @@ __global__ __launch_bounds__(768, 3) void decay_stream_kernel(SeqTable tab, Deca
           for (int g = 0; g < 2; ++g)
             mma(P[g], lds_frag(Ks[copy] + (32 * c + 16 * g) * DK, frag0 ^ 32 * x), qf);
         }
+        const float z = zero_sum(P[0], P[1], 0.f);
+        const bool unlike = __any(z != z); // a score is not finite
+        if (lane == 0)
+          strange[par][w] = unlike;
         const int i = 16 * t + lr;
         const float hi = gh[i], lo = gl[i];
 #pragma unroll
@@ -1145,7 +1153,15 @@ __global__ __launch_bounds__(768, 3) void decay_stream_kernel(SeqTable tab, Deca
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         z = fmaf(O[t][r], 0.f, z);
-    if (__builtin_expect(__any(z != z), 0) && by_recurrence(S, O, vf, Ps[par], eG[c0], all)) {
+    bool one_by_one = false; // this wave's columns of the chunk by the recurrence
+    if (__builtin_expect(__any(z != z), 0)) {
+      int met = 0;
+#pragma unroll
+      for (int i = 0; i < 6; ++i) // (the units' waves)
+        met |= strange[par][i];
+      one_by_one = by_recurrence(vf, met, all);
+    }
+    if (__builtin_expect(one_by_one, 0)) {
       by_token<true>(S, a,
                      Tokens<T>{q0 + pos * a.qs, k0 + pos * a.ks, v0 + pos * a.vs, g0 + pos * a.gs,
                                o0 + pos * a.os},

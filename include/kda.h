@@ -670,9 +670,9 @@ kda_status kda_state_load(int32_t n, int64_t R, int32_t L, int32_t format, const
  *                  none is needed, and for a call that will be refused: then
  *                  it may be NULL).
  * Infinities, NaN and states that grow (g above 0) go as the recurrence has
- * them, whatever the cut, with two exceptions: a finite value that up to 64
- * tokens decay to less than 2^-126 of itself may count as 0, and behind a g of
- * +inf a cut sequence may hold NaN for an infinity.
+ * them, whatever the cut, with two exceptions: of a finite value that up to 64
+ * tokens decay to less than 2^-126 of itself, less than that may be left, and
+ * behind a g of +inf a cut sequence may hold NaN for an infinity.
  * States, decays and sums are fp32.  With KDA_BF16, o is formed from bf16
  * products (a chunk's scores and the state that enters it, each rounded
  * once), the state is carried and updated to fp32 accuracy, and o is rounded
