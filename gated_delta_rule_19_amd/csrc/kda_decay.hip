@@ -396,8 +396,9 @@ __device__ __forceinline__ u32x4 raw_rsrc(const void *p, uint32_t bytes) {
 // after `to` (wave-uniform).  In assembly because the compiler, which sees such
 // a load as a store to any of LDS, would wait for it before each transposed
 // read; the walk below waits for vmcnt(0) and a barrier before it reads what
-// was loaded.  Nothing is returned in registers, and m0 serves nothing else
-// in these kernels.
+// was loaded.  Nothing is returned in registers.  m0 cannot be named as changed
+// (the compiler reserves it); a test on the listing holds that nothing else in
+// these kernels uses it.
 __device__ __forceinline__ void lds_request16(const u32x4 &r, int at, const void *to) {
   // (the low half of a generic LDS address is the offset in LDS)
   const uint32_t m0 = (uint32_t)(uintptr_t)to;
