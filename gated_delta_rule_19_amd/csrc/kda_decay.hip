@@ -29,10 +29,9 @@
 // Ends of fp32's range.  Where an infinity or a NaN in q, k or v, or growth past
 // fp32, would meet a 0 in these products (an infinity in k or v would even reach
 // earlier tokens of its chunk), a wave's columns of the chunk go by the
-// recurrence, token by token.  All of these show in o: a wave that finds one of
-// its outputs not finite looks for the cause (see by_recurrence), so that other
-// chunks pay an operation a value.  Launches that form only states look at k, v
-// and the decay instead.
+// recurrence, token by token.  Infinities and NaN of q and k show in the scores,
+// which are looked at as they are formed (launches that form only states look at
+// k); those of v each wave finds in its columns.
 #include "kda_block.h"
 #include "kda_device.h"
 
@@ -309,8 +308,12 @@ __device__ __forceinline__ Whole weigh(const Frag<float> &v, const f32x4 &w0, co
 __device__ __forceinline__ float zero_sum(const f32x4 &a, const f32x4 &b, float z) {
 #pragma unroll
   for (int r = 0; r < 4; ++r)
-    z = fmaf(b[r], 0.f, fmaf(a[r], 0.f, z));
-  return z;
+    z = fmaf(a[r], 0.f, z);
+  float y = 0.f;
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    y = fmaf(b[r], 0.f, y);
+  return z + y;
 }
 __device__ __forceinline__ float zero_sum(const Frag<bf16> &f) {
   return zero_sum(__builtin_bit_cast(u32x4, f.v), bf16());
@@ -370,16 +373,15 @@ __device__ __forceinline__ void by_token(f32x4 (&S)[TD], const DecayArgs &a, con
   }
 }
 
-// Whether a wave that met outputs (or a decay) that are not finite takes the chunk
-// by the recurrence: where q or k (`met`: a score was not finite), this wave's
-// columns of V (vf), or growth (all is infinite) are the cause.  Not where the
-// state that enters or a NaN among the decays is the cause alone: these the
-// products carry on as the recurrence does, and a sequence that has met a NaN or
-// an infinity stays as fast as others.
+// Whether a wave takes a chunk by the recurrence: for q or k (`met`: a score was
+// not finite), its columns of V (vf), or growth (all is infinite).  Not for the
+// state that enters or a NaN among the decays: these the products carry on as the
+// recurrence does, and a sequence that has met a NaN or an infinity stays as fast
+// as others.
 template <typename T>
 __device__ __forceinline__ bool by_recurrence(const Frag<T> (&vf)[2], int met, float all) {
   const float z = zero_sum(vf[0]) + zero_sum(vf[1]);
-  return __any(z != z || met != 0 || all == __builtin_inff());
+  return __any((z != z) | (met != 0) | (all == __builtin_inff()));
 }
 
 // ---- the chunks -------------------------------------------------------------------
@@ -694,6 +696,10 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
         request_v();
       }
 
+      // o^T of this wave's columns: tile t, element r is column 4 lg + r of token
+      // 16 t + lr
+      f32x4 O[4] = {zero, zero, zero, zero};
+      T *Pb = OWN_P ? Ps : Qs[AHEAD ? buf : 0];
       if constexpr (OUT) {
         // Scores: unit u is tokens 16 t .. of q against tokens 32 c .. of k,
         // (t, c) = (u, 0), and (2, 1), (3, 1) for u = 4, 5; the others are
@@ -722,9 +728,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
           }
           zp = zero_sum(P[y][0], P[y][1], zp);
         }
-        // o^T of this wave's columns from the entering state: tile t, element
-        // r is column 4 lg + r of token 16 t + lr
-        f32x4 O[4] = {zero, zero, zero, zero};
+        // ... and o from the entering state
         {
           Frag<T> f[2][4];
           const auto read_q = [&](int x) __attribute__((always_inline)) {
@@ -752,7 +756,6 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
         if (lane == 0)
           strange[par][w] = unlike;
         const float *gh = Ghi[par], *gl = Glo[par];
-        T *Pb = OWN_P ? Ps : Qs[AHEAD ? buf : 0];
         if constexpr (!OWN_P)
           lds_barrier(); // every wave has read q
 #pragma unroll
@@ -778,73 +781,64 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
         lds_barrier(); // the scores are there
         if constexpr (TURNS)
           request_v();
-        T *ob = o + (tok0 + pos) * a.os + (int64_t)h * a.dv + col0;
-        const auto ro =
-            buffer_rsrc(ob, (uint32_t)(((cnt - 1) * os + cols) * kEs));
-        float z = all * 0.f; // NaN where an output, or the decay, is not finite
+        int met = 0;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          O[t] *= eG[par][16 * t + lr];
-#pragma unroll
-          for (int c = 0; c <= t >> 1; ++c)
-            mma(O[t], vf[c], get_frag(Pb + (2 * t + c) * 512, lane));
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            z = fmaf(O[t][r], 0.f, z);
-        if (__builtin_expect(__any(z != z), 0)) {
-          int met = 0;
-#pragma unroll
-          for (int i = 0; i < NW; ++i)
-            met |= strange[par][i];
-          one_by_one = by_recurrence(vf, met, all);
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          if (__builtin_expect(one_by_one, 0))
-            continue; // (by_token writes them)
-          const int i = 16 * t + lr;
-          O[t] *= a.scale;
-          const int c = 16 * w + 4 * lg;
-          if constexpr (FAST) {
-            const int at = c < cols ? (i * os + c) * kEs : kNowhere;
-            if constexpr (kEs == 2) {
-              typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
-              typedef uint32_t u32x2_t4 __attribute__((ext_vector_type(2)));
-              bf16x4_t y;
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-                y[r] = static_cast<bf16>(O[t][r]);
-              __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t4, y), ro, at, 0, 0);
-            } else {
-              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[t]), ro, at, 0, 0);
-            }
-          } else if (i < cnt) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (c + r < cols)
-                ob[i * os + c + r] = from_f32<T>(O[t][r]);
-          }
-        }
-        if constexpr (TURNS && !OWN_P)
-          lds_barrier(); // the scores are read: q may come in their place
+        for (int i = 0; i < NW; ++i)
+          met |= strange[par][i];
+        one_by_one = by_recurrence(vf, met, all);
       }
 
-      // The state's update, four row tiles at a time, each four's operands
-      // read while the ones before are multiplied.
       constexpr int kFirst = OUT ? 8 : 0, kHere = kSteps - kFirst; // requests left
+      T *ob = o + (tok0 + pos) * a.os + (int64_t)h * a.dv + col0;
       if (__builtin_expect(one_by_one, 0)) {
+        if constexpr (OUT && TURNS && !OWN_P)
+          lds_barrier(); // (as below)
 #pragma unroll
         for (int y = kFirst; y < kSteps; ++y)
           request(y);
         const Source t = source(pos);
-        by_token<OUT>(S, a,
-                      Tokens<T>{t.q, t.k, t.v, t.g,
-                                o + (tok0 + pos) * a.os + (int64_t)h * a.dv + col0},
-                      cnt, my_col, my_col < cols);
+        by_token<OUT>(S, a, Tokens<T>{t.q, t.k, t.v, t.g, ob}, cnt, my_col, my_col < cols);
       } else {
+        if constexpr (OUT) {
+          const auto ro =
+              buffer_rsrc(ob, (uint32_t)(((cnt - 1) * os + cols) * kEs));
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const int i = 16 * t + lr;
+            O[t] *= eG[par][i];
+#pragma unroll
+            for (int c = 0; c <= t >> 1; ++c)
+              mma(O[t], vf[c], get_frag(Pb + (2 * t + c) * 512, lane));
+            O[t] *= a.scale;
+            const int c = 16 * w + 4 * lg;
+            if constexpr (FAST) {
+              const int at = c < cols ? (i * os + c) * kEs : kNowhere;
+              if constexpr (kEs == 2) {
+                typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
+                typedef uint32_t u32x2_t4 __attribute__((ext_vector_type(2)));
+                bf16x4_t y;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                  y[r] = static_cast<bf16>(O[t][r]);
+                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t4, y), ro, at, 0,
+                                                      0);
+              } else {
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[t]), ro, at, 0,
+                                                       0);
+              }
+            } else if (i < cnt) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (c + r < cols)
+                  ob[i * os + c + r] = from_f32<T>(O[t][r]);
+            }
+          }
+          if constexpr (TURNS && !OWN_P)
+            lds_barrier(); // the scores are read: q may come in their place
+        }
+
+        // The state's update, four row tiles at a time, each four's operands
+        // read while the ones before are multiplied.
 #pragma unroll
         for (int d = 0; d < kTD; ++d)
           S[d] *= all;
@@ -1131,8 +1125,6 @@ __global__ __launch_bounds__(768, 3) void decay_stream_kernel(SeqTable tab, Deca
       reads_stay();
       if (x + 1 < kGQ)
         read_q(x + 1);
-      else
-        read_p();
       const Frag<T> sf = pack_acc2(S[2 * x], S[2 * x + 1]);
 #pragma unroll
       for (int t = 0; t < 4; ++t)
@@ -1141,33 +1133,28 @@ __global__ __launch_bounds__(768, 3) void decay_stream_kernel(SeqTable tab, Deca
     reads_stay();
     const auto ro = buffer_rsrc(o0 + (int64_t)pos * os,
                                 (uint32_t)(((min(kDC, end - pos) - 1) * os + cols) * kEs));
+    int met = 0;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      O[t] *= ei[t];
-#pragma unroll
-      for (int c = 0; c <= t >> 1; ++c)
-        mma(O[t], vf[c], pf[t][c]);
-    }
-    float z = all * 0.f; // NaN where an output, or the decay, is not finite
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        z = fmaf(O[t][r], 0.f, z);
-    bool one_by_one = false; // this wave's columns of the chunk by the recurrence
-    if (__builtin_expect(__any(z != z), 0)) {
-      int met = 0;
-#pragma unroll
-      for (int i = 0; i < 6; ++i) // (the units' waves)
-        met |= strange[par][i];
-      one_by_one = by_recurrence(vf, met, all);
-    }
+    for (int i = 0; i < 6; ++i) // (the units' waves)
+      met |= strange[par][i];
+    const bool one_by_one = by_recurrence(vf, met, all);
     if (__builtin_expect(one_by_one, 0)) {
       by_token<true>(S, a,
                      Tokens<T>{q0 + pos * a.qs, k0 + pos * a.ks, v0 + pos * a.vs, g0 + pos * a.gs,
                                o0 + pos * a.os},
                      min(kDC, end - pos), my_col, my_col < cols);
     } else {
+      read_p();
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        O[t] *= ei[t];
+#pragma unroll
+        for (int c = 0; c <= t >> 1; ++c)
+          mma(O[t], vf[c], pf[t][c]);
+      }
+      // (the stores by themselves: spread over the update by the compiler, they
+      // cost 8192 tokens of 96 heads 288 us, not 280)
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const int i = 16 * t + lr;
@@ -1181,6 +1168,7 @@ __global__ __launch_bounds__(768, 3) void decay_stream_kernel(SeqTable tab, Deca
         __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_o, y), ro,
                                               c < cols ? (i * os + c) * kEs : kNowhere, 0, 0);
       }
+      __builtin_amdgcn_sched_barrier(0);
       // The state's update, four row tiles at a time, each four's operands
       // read while the ones before are multiplied.
 #pragma unroll
