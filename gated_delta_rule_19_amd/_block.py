@@ -125,10 +125,11 @@ def block_norm(x, weight=None, eps: float = 1e-6, residual=None, scale=1.0, gate
 
     x, gate and y ``[rows, D]`` of one dtype, residual and r ``[rows, D]`` of
     residual's dtype (x's without one); weights fp32 ``[D]``; scale a number
-    or fp32 ``[D]``.  ``residual_out`` (it may be residual itself) and ``y``
-    take the outputs.  Returns ``(r, y or None)``; r is not written where
-    neither residual nor residual_out is given and y is formed: then ``(None,
-    y)``.
+    or fp32 ``[D]``.  Weights and a scale ``[D]`` start at multiples of 16
+    bytes: others (slices of larger parameters, for instance) are refused.
+    ``residual_out`` (it may be residual itself) and ``y`` take the outputs.
+    Returns ``(r, y or None)``; r is not written where neither residual nor
+    residual_out is given and y is formed: then ``(None, y)``.
     """
     if x.dim() != 2:
         raise ValueError("x must be [rows, D] (got %s)" % (tuple(x.shape),))
@@ -187,8 +188,9 @@ def beam_select(logits, scores, beams=None, finished=None, eos: int = -1, order:
     beams]`` (beams None: W), best first with ``order="score"``; with
     ``"rows"`` the best continuation of beam w is in row w (where there is
     one) and the others fill the rows left, so that ``state_reorder`` moves
-    as few states as possible.  Values are compared in 64 bits and equal ones
-    taken by the lower ``w * V + v``.
+    as few states as possible.  Values are compared in 64 bits, in which the
+    logarithm of a beam's sum is good to some 2^-23, and equal ones taken by
+    the lower ``w * V + v``.
     """
     if logits.dim() != 3:
         raise ValueError("logits must be [batch, beams, vocabulary] (got %s)"

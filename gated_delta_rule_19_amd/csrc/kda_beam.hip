@@ -339,7 +339,7 @@ __device__ __forceinline__ bool before(const Valued &p, const Valued &q) {
          ((p.val == q.val) & ((p.w < q.w) | ((p.w == q.w) & tail)));
 }
 
-// A chain of latencies, a workgroup a batch: 10 us for 64 batches of 8 beams in
+// A chain of latencies, a workgroup a batch: 8 us for 64 batches of 8 beams in
 // 16 parts, 5 us for one of 4 beams in 8; so the candidates are asked for
 // before the sums, a beam's parts are joined by as many lanes, and the ranks
 // are counted by all four waves without branches (one lane each, with

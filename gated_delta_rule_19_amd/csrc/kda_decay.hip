@@ -20,9 +20,13 @@
 // of lane group g; K and V are read transposed in that order.
 //
 // Roundings: the state is fp32 and its update takes v e^{G_L - G_j} as the sum
-// of three bf16 numbers (24 bits; one alone would leave the state 2^-9 off),
-// beside k as it is; the scores and the entering state are rounded to bf16
-// once each for o, which is rounded to bf16 itself.  fp32 calls round nothing.
+// of three bf16 numbers (24 bits; one alone would leave the state 2^-9 off, for
+// the rest of the prompt), beside k as it is.  For o, which is bf16 itself, the
+// scores and the entering state are rounded to bf16 once each: o is then 2.3e-3
+// of its size off (root mean square), 1.7e-3 of it by its own rounding.  Both in
+// two parts leave its own alone, but take 22 products more of a wave's 70 (8192
+// tokens of 96 heads 291 us against 264, 131072 of 12 777 against 702, 16 x 2048
+// of 96 1030 against 884): who needs the bits has fp32 calls, which round nothing.
 // G is summed and kept as two fp32 numbers, so that differences within a chunk
 // keep their accuracy beside a decay of e^-150.
 //
@@ -192,10 +196,12 @@ __device__ __forceinline__ float zero_sum(const u32x4 &x, float) {
 }
 
 // LDS matrices.  Rows have no padding; the pieces of a row are permuted by an
-// exclusive-or with bits of the row, so that the reads below meet every one of
-// 64 banks once: rows of fragments (16 rows, one piece), and tokens read
-// transposed (bf16: 8 rows, 2 or 4 pieces; fp32: 4 rows, 4 pieces).  K and q
-// have rows of LD = DK elements, V of the workgroup's columns.
+// exclusive-or with bits of the row, so that the same piece of the rows of a tile
+// lies in different banks.  K and q have rows of LD = DK elements, V of the
+// workgroup's columns.  Counted one kind of read at a time (SQ_LDS_BANK_CONFLICT):
+// none for rows of fp32 fragments, V transposed, scores, decays and weights; but 4
+// of the 8 cycles of a row fragment in bf16, and half of those of K transposed (2
+// of 4, fp32 4 of 8): its lanes take one half of their pieces, half the banks.
 template <typename T, int LD> __device__ __forceinline__ int row_flip(int row) {
   if constexpr (sizeof(T) == 4)
     return row & 15;
@@ -319,7 +325,8 @@ __device__ __forceinline__ float zero_sum(const Frag<bf16> &f) {
   return zero_sum(__builtin_bit_cast(u32x4, f.v), bf16());
 }
 __device__ __forceinline__ float zero_sum(const Frag<float> &f) {
-  return zero_sum(__builtin_bit_cast(u32x4, f.lo), 0.f) + zero_sum(__builtin_bit_cast(u32x4, f.hi), 0.f);
+  return zero_sum(__builtin_bit_cast(u32x4, f.lo), 0.f) +
+         zero_sum(__builtin_bit_cast(u32x4, f.hi), 0.f);
 }
 
 // ---- tokens one by one ------------------------------------------------------------
@@ -417,24 +424,25 @@ __device__ __forceinline__ void reads_stay() { __builtin_amdgcn_sched_barrier(0x
 // Launch `pass` 0, of cut sequences: all segments but the last, only their
 // states: the first from the state that enters the sequence, which is put into
 // the workspace as it is, the others from zero.  Pass 1: all segments in full
-// from the states that enter them.  NW waves, 16 value columns each.  FAST: dk, dv and the rows'
-// addresses are multiples of 16 bytes: everything moves through raw buffers,
-// whose bounds take the place of branches at a chunk's end, and q, K and V
-// straight into LDS.  AHEAD: a chunk ahead into the other one of two copies;
+// from the states that enter them.  NW waves, 16 value columns each.  FAST: dk,
+// dv and the rows' addresses are multiples of 16 bytes: everything moves through
+// raw buffers, whose bounds take the place of branches at a chunk's end, and q, K
+// and V straight into LDS.  AHEAD: a chunk ahead into the other one of two copies;
 // TURNS, where LDS holds no two: each of the three as its place gets free;
-// without either, the loads of the one copy are waited for.
+// without either, the loads of the one copy are waited for (heads of 128 in bf16:
+// 8.2 us a chunk, FAST 3.9; of 255 in fp32 28.6, of 256 FAST 17.3).
 //
-// 131072 tokens, 12 heads of 128, bf16: 21 segments a head, 280 us for their
-// states and 445 for the outputs (3.6 TB/s of q, k, v and o).  No unit is full
-// (matrix cores 22 %): what bounds it is the chain of a chunk's products, its
-// barriers and LDS round trips, 8700 cycles for 128 columns alone, some 10500
-// with every CU busy.  Chunks requested two ahead (a third copy, 158 KB of LDS)
+// 131072 tokens, 12 heads of 128, bf16: 21 segments a head, 275 us for their
+// states and 450 for the outputs (3.6 TB/s of q, k, v and o).  No unit is full
+// (matrix cores 22 %): what is seen of its bound is the chain of a chunk's
+// products, barriers and LDS round trips, 3.9 us for 128 columns with 96 CUs
+// busy, 4.6 with all.  Chunks requested two ahead (a third copy, 158 KB of LDS)
 // gain 2 % there and lose 15 % on sequences of two chunks.
 //
 // fp32 multiplies on the fp32 matrix instructions, at a sixteenth of bf16's
-// rate: 9.4 of the 13.1 us of a chunk of eight waves are theirs.  With all loads
-// waited for, without TURNS, a chunk took 14.8; one of bf16 heads of 256 5.5 us,
-// now 4.7.
+// rate: 9.4 of the 13.1 us of a chunk of eight waves are theirs, rows that pad dk
+// and columns that pad dv included.  With all loads waited for, without TURNS, a
+// chunk took 14.8; one of bf16 heads of 256 5.5 us, now 4.4.
 template <typename T, int DK, int NW> constexpr int kCopyBytes =
     kDC * (2 * DK + 16 * NW) * (int)sizeof(T);
 template <typename T, int DK, int NW, bool FAST>
@@ -915,11 +923,10 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void decay_chunk_kernel(
 // sum the decays.  One barrier a chunk.  Three copies of q, K, V and the decays
 // (chunk i % 3), two of the scores.
 //
-// 8192 tokens, 96 heads of 128: 192 workgroups, 292 us on the GPU, 4700 cycles a
-// chunk, of them 3600 of matrix products, transposed reads and roundings in the
-// state waves, the rest the wait for scores and decays.  With the same waves
-// doing both in turn a chunk took 7600.  Four score waves: 5200; a score wave
-// of two units and the wait for the decays behind it set the pace.
+// 8192 tokens, 96 heads of 128: 192 workgroups, 269 us on the GPU, 2.1 us a chunk
+// (1.7 with 64 workgroups).  With the same waves doing both in turn a chunk took
+// 1.6 times as long.  Four score waves: 1.1 times; a score wave of two units and
+// the wait for the decays behind it set the pace.
 template <int DK>
 __global__ __launch_bounds__(768, 3) void decay_stream_kernel(SeqTable tab, DecayArgs a,
                                                               const bf16 *__restrict__ q,
@@ -1380,25 +1387,26 @@ int64_t num_segments(int64_t len, int64_t seg) { return len <= seg ? 1 : (len + 
 // How a call runs.  Measured (MI355X, 96 heads of 128, bf16 unless told):
 //
 // - Streams (four state waves, 64 columns a workgroup, one workgroup a CU) take
-//   1.9 us a chunk of 64 tokens, eight waves of the other kernel 3.6 us for
-//   128 columns, four 3.4 us for 64.  A stream for each chain is the fastest
-//   while all of them run at once: 8192 tokens, 192 streams: 292 us, the
-//   chunk kernel uncut 467, cut 375.  With more chains than CUs the others'
-//   wider blocks are: 16 x 2048 tokens: 868 us, streams 1008.  Four waves are
-//   for value heads that eight would leave half empty (32 sequences of 256
-//   tokens, 16 heads of 64: 25 us, eight waves 36, streams 30).
+//   1.7 to 2.1 us a chunk of 64 tokens, eight waves of the other kernel 3.9 us
+//   for 128 columns, four 3.4 us for 64.  A stream for each chain is the fastest
+//   while all of them run at once: 8192 tokens, 192 streams: 264 us, the
+//   chunk kernel uncut 499, cut in two 433.  With more chains than CUs the
+//   others' wider blocks are: 16 x 2048 tokens: 880 us, streams 930.  Four waves
+//   are for value heads that eight would leave half empty (32 sequences of 256
+//   tokens, 16 heads of 64: 25 us, eight waves 36, streams 29).
 // - Of a cut sequence k and v are read twice, in three launches: 2.8 us a chunk
-//   for the states alone, 4.5 for all of it with every CU busy, some 20 us
+//   for the states alone, 4.6 for all of it with every CU busy, some 20 us
 //   beside.  A stream takes the whole in 2.0 us a chunk, so that cuts begin to
 //   pay at four segments and 256 tokens (32 heads: 1024 tokens in four segments
-//   44 us, uncut 36; 2048 in eight 52, 63; 8192 133, 217; 48 heads and 32768
-//   tokens in five 730, 1020), where the chunk kernel would take a whole
+//   43 us, uncut 37; 2048 in eight 50, 62; 8192 133, 219; 48 heads and 32768
+//   tokens in five 693, 943), where the chunk kernel would take a whole
 //   sequence from two and a half on.  Rows off 16 bytes have the chunk kernel
-//   alone, and its rule (1024 tokens of 32 heads: uncut 139 us, cut 66).
+//   alone, and its rule (1024 tokens of 32 heads: uncut 133 us, cut 65).
 // - fp32: 13.1 us a chunk with eight waves and 128 columns, 9.8 with four and
 //   64: four where the longest sequence sets the time (9001 tokens in 37 ragged
-//   sequences, 10 heads of 100: 153 us against 167), eight where the number of
-//   workgroups does (37 sequences of 243: 123 us against 140).
+//   sequences, 10 heads of 100 x 72, the longest 743: 149 us against 166, 1009:
+//   163 and 216), eight where the number of workgroups does (37 sequences of 243:
+//   123 us against 138).  In between four may be the slower one (616: 152, 141).
 constexpr int64_t kCUs = 256;
 
 bool decay_even(int elt, const kda_decay_io &io) {

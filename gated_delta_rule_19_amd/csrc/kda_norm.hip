@@ -11,10 +11,10 @@
 // workgroup, whose waves join their sums in LDS.  Sums are fp32: each lane's
 // own of up to 64 elements, then the lanes' in a tree: 74 roundings deep at most.
 //
-// 8192 x 12288 bf16 with all parts: 194 us for 1.01 GB, 5.2 TB/s, what a large
+// 8192 x 12288 bf16 with all parts: 184 us for 1.01 GB, 5.5 TB/s, what a large
 // copy reaches on the same card.  Two groups a lane keep more rows in flight
-// than four (205 us), and non-temporal accesses, here larger than all caches,
-// gain as much (cached: 216 us).  20000 x 1002 fp32: 82 us for 401 MB (4.9
+// than four (194 us then, 205), and non-temporal accesses, here larger than all
+// caches, gain as much (cached: 216 us).  20000 x 1002 fp32: 81 us for 401 MB (5.0
 // TB/s): rows that end inside a 128-byte line cost a tenth (1024 columns: 5.5).
 // One row: 5.0 us on the GPU, the latency of three rounds to memory and two
 // joins of sums.
@@ -104,7 +104,8 @@ template <int E> __device__ __forceinline__ void load_param(const float *p, int 
 // all outputs are bf16, half a step of which is hundreds of times that even at the
 // ends of fp32's range (4 rows of 65536: 18.9 us, with it 21.1).
 template <bool EXACT> __device__ __forceinline__ float sigmoid(float w) {
-  constexpr float c1 = 0x1.715476p+0f, c2 = 0x1.4ae0bep-26f, ln2 = 0x1.62e43p-1f; // c1 + c2: log2(e)
+  constexpr float c1 = 0x1.715476p+0f, c2 = 0x1.4ae0bep-26f; // c1 + c2: log2(e)
+  constexpr float ln2 = 0x1.62e43p-1f;
   const float t = -w * c1, e = __builtin_amdgcn_exp2f(t);
   if constexpr (!EXACT)
     return __builtin_amdgcn_rcpf(1.f + e);
