@@ -430,7 +430,8 @@ __device__ __forceinline__ void reads_stay() { __builtin_amdgcn_sched_barrier(0x
 // and V straight into LDS.  AHEAD: a chunk ahead into the other one of two copies;
 // TURNS, where LDS holds no two: each of the three as its place gets free;
 // without either, the loads of the one copy are waited for (heads of 128 in bf16:
-// 8.2 us a chunk, FAST 3.9; of 255 in fp32 28.6, of 256 FAST 17.3).
+// 8.2 us a chunk, FAST 3.9; of 255 in fp32 28.6, of 256 FAST 17.3; fp32 heads of
+// 128, eight waves, spill two registers there).
 //
 // 131072 tokens, 12 heads of 128, bf16: 21 segments a head, 275 us for their
 // states and 450 for the outputs (3.6 TB/s of q, k, v and o).  No unit is full
